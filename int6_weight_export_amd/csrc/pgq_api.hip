@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "pgq_desc.h"
+#include "pgq_train.h"
 #include "../../include/pgq.h"
 
 using namespace pgq;
@@ -620,6 +621,12 @@ pgq_status export_descs(const pgq_tensor_in* t, int32_t n, const pgq_tensor_plan
 }
 
 }  // namespace
+
+// What the entry points of other files share with these (pgq_train.h).
+namespace pgq {
+int32_t note_hip_error(hipError_t e) { return hip_failed(e); }
+uint64_t hash_bytes(const void* data, size_t n, uint64_t h) { return table_hash(data, n, h); }
+}  // namespace pgq
 
 // The checks and launch of both GEMM entry points; esz = bytes of a Y element (4 or 2).
 static pgq_status qgemm(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const int8_t* codes, int64_t ldc,

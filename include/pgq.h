@@ -290,6 +290,85 @@ pgq_status pgq_qgemm_bf16_ybf16(const uint16_t* x, int64_t M, int64_t K, int64_t
                                 int64_t ldc, const uint16_t* scales, int64_t N, uint16_t* y, int64_t ldy, void* stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* The quantized linear layer: the GEMM above with bias, activation and residual in its        */
+/* epilogue, and its gradient.  Source: the activations are those of the cards (leaky ReLU     */
+/* squared: PR #1414 and PR #1202 cards, Architecture; SiLU of the gated MLP: PR #2159); the    */
+/* weights are the STE forward's, What[n][k] = bf16(fp32(code[n][k] * s_n)) (PR #69, Other).   */
+/*   forward    Z = X What^T + b;  Y = act(Z) + R                                              */
+/*   backward   dZ = dY * act'(Z);  dX = dZ What;  dW = mask ? dZ^T X : +0;  db = sum_m dZ     */
+/*   act        none; relu: z > 0 ? z : slope * z; relu2: the square of relu; silu: z / (1 + e^-z) */
+/* Products of bf16 values are exact in fp32 and every sum, bias, activation and residual is    */
+/* formed in fp32; Y, Z, dX and dW are rounded to their type once, at the store.  In backward   */
+/* dZ is rounded to bf16 before the two products (the matrix cores' input type; exact when act  */
+/* is none and dY is bf16); db sums the unrounded dZ.  Sums run in a fixed order: a call on the */
+/* same inputs gives the same bits.                                                            */
+/* The gradient of the weights is the straight-through one: of the bf16 weights, zeroed where   */
+/* the fake-quant mask bit is 0 (pgq_fq_tensor.mask); that of the residual is dY itself.       */
+/* NaN and infinities follow the arithmetic; a masked weight's gradient is +0 whatever they are. */
+/* ------------------------------------------------------------------------------------------ */
+
+#define PGQ_ACT_NONE  0
+#define PGQ_ACT_RELU  1   /* leaky ReLU; slope 0 is the plain one */
+#define PGQ_ACT_RELU2 2   /* its square */
+#define PGQ_ACT_SILU  3
+
+typedef struct {
+    int64_t M, N, K;             /* tokens, outputs, inputs; each below 2^31 */
+    const uint16_t* x;           /* bf16, M x K, row stride ldx */
+    int64_t ldx;
+    const int8_t* codes;         /* N x K, row stride ldc */
+    int64_t ldc;
+    const uint16_t* scales;      /* fp16 bit patterns, N */
+    const void* bias;            /* NULL or N values of bias_dtype (PGQ_F32 or PGQ_BF16) */
+    const void* residual;        /* NULL or M x N of residual_dtype (PGQ_F32 or PGQ_BF16), row stride ldr.
+                                    May be y itself (same pointer, stride and type) */
+    int64_t ldr;
+    uint16_t* z;                 /* NULL or bf16, M x N, row stride ldz: receives Z for backward */
+    int64_t ldz;
+    void* y;                     /* y_dtype (PGQ_F32 or PGQ_BF16), M x N, row stride ldy */
+    int64_t ldy;
+    int32_t bias_dtype, residual_dtype, y_dtype;
+    int32_t act;                 /* PGQ_ACT_* */
+    float slope;                 /* RELU, RELU2: finite */
+    int32_t reserved;            /* 0 */
+} pgq_linear_fwd;
+
+typedef struct {
+    int64_t M, N, K;
+    const void* dy;              /* dy_dtype (PGQ_F32 or PGQ_BF16), M x N, row stride lddy */
+    int64_t lddy;
+    const uint16_t* z;           /* bf16 Z that forward stored, row stride ldz (unused for PGQ_ACT_NONE) */
+    int64_t ldz;
+    const uint16_t* x;           /* bf16, M x K, row stride ldx (unused when dw is NULL) */
+    int64_t ldx;
+    const int8_t* codes;         /* N x K, row stride ldc (unused when dx is NULL) */
+    int64_t ldc;
+    const uint16_t* scales;      /* fp16 bit patterns, N (unused when dx is NULL) */
+    const uint8_t* mask;         /* NULL or N x ceil(K / 8) bytes, bit k % 8 of byte k / 8, as fake-quant writes it */
+    void* dx;                    /* NULL or dx_dtype (PGQ_F32 or PGQ_BF16), M x K, row stride lddx */
+    int64_t lddx;
+    void* dw;                    /* NULL or dw_dtype (PGQ_F32 or PGQ_BF16), N x K, row stride lddw */
+    int64_t lddw;
+    float* dbias;                /* NULL or N fp32 */
+    int32_t dy_dtype, dx_dtype, dw_dtype;
+    int32_t act;                 /* PGQ_ACT_*, as in forward */
+    float slope;
+    int32_t reserved;            /* 0 */
+} pgq_linear_bwd;
+
+/* Device scratch the call below needs for this layer (it depends on sizes, strides, alignment and
+ * on which pointers are NULL, not on the device).  May be 0. */
+pgq_status pgq_linear_forward_workspace(const pgq_linear_fwd* p, size_t* workspace_bytes);
+pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* workspace_bytes);
+
+/* workspace: device memory of at least that many bytes, 256-byte aligned (NULL when 0); its content
+ * is of no account before and after the call, and calls that run at the same time need one each.
+ * p is read during the call only.  M = 0 or N = 0 writes no Y; K = 0 makes Z the bias.  In backward
+ * an empty sum (N = 0 for dX, M = 0 for dW and db) is +0.  May be recorded into a HIP graph. */
+pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t workspace_bytes, void* stream);
+pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Weight averaging without quantization, grouped over n tensors in one launch.               */
 /* w[i]: the weights (fp32 or bf16, rows x cols, row stride ld; awq_s must be NULL; name is    */
 /* ignored).  The averages are caller-owned fp32 device buffers, rows x cols dense, updated in */

@@ -382,3 +382,130 @@ def qgemm(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out: Optio
             _p(scales), N, _p(out), out.stride(0) if M > 1 else N, _stream())
     pgq.check(rc, name)
     return out
+
+
+ACTS = {"none": pgq.PGQ_ACT_NONE, "relu": pgq.PGQ_ACT_RELU, "relu2": pgq.PGQ_ACT_RELU2, "silu": pgq.PGQ_ACT_SILU}
+
+
+def _check_matrix(name: str, t: torch.Tensor, shape: Tuple[int, int], dtypes, device) -> int:
+    """The row stride of a matrix argument whose rows are contiguous."""
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)} < {cols})")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _check_vector(name: str, t: torch.Tensor, n: int, dtypes, device) -> None:
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous values expected")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _launch_linear(fn, size_fn, name: str, p, device) -> None:
+    """One call of a linear-layer entry point on the device of its operands: the scratch comes from
+    torch's allocator (ordered with the current stream, private to a graph under capture)."""
+    need = ctypes.c_size_t(0)
+    pgq.check(size_fn(ctypes.byref(p), ctypes.byref(need)), name)
+    with torch.cuda.device(device):
+        ws = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+        pgq.check(fn(ctypes.byref(p), _p(ws), need.value, _stream()), name)
+
+
+_B16_F32 = (torch.bfloat16, torch.float32)
+_SCALE_TYPES = (torch.int16, torch.float16)
+
+
+def qlinear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias: Optional[torch.Tensor] = None,
+            act: str = "none", slope: float = 0.0, residual: Optional[torch.Tensor] = None, want_z: bool = False,
+            out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16):
+    """Y = act(X What^T + b) + R with What = bf16(code * s).
+
+    x: bf16 [M, K]; codes: int8 [N, K]; scales: fp16 [N] (or int16 bit patterns); bias: fp32 or bf16
+    [N]; residual: fp32 or bf16 [M, N], which may be `out` itself; act: "none", "relu", "relu2" (both
+    with a leaky slope) or "silu".  Returns Y [M, N] in out_dtype (bf16 or fp32), or (Y, Z) with the
+    bf16 pre-activation Z that qlinear_backward takes when want_z."""
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x and codes must be matrices")
+    (M, K), N, dev = x.shape, codes.shape[0], x.device
+    p = pgq.pgq_linear_fwd(M=M, N=N, K=K, act=ACTS[act], slope=slope)
+    p.ldx = _check_matrix("x", x, (M, K), (torch.bfloat16,), dev)
+    p.ldc = _check_matrix("codes", codes, (N, K), (torch.int8,), dev)
+    _check_vector("scales", scales, N, _SCALE_TYPES, dev)
+    p.x, p.codes, p.scales = x.data_ptr(), codes.data_ptr(), scales.data_ptr()
+    if bias is not None:
+        _check_vector("bias", bias, N, _B16_F32, dev)
+        p.bias, p.bias_dtype = bias.data_ptr(), _dtype_code(bias.dtype)
+    if residual is not None:
+        p.ldr = _check_matrix("residual", residual, (M, N), _B16_F32, dev)
+        p.residual, p.residual_dtype = residual.data_ptr(), _dtype_code(residual.dtype)
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    p.ldy = _check_matrix("out", out, (M, N), (out_dtype,), dev)
+    p.y, p.y_dtype = out.data_ptr(), _dtype_code(out_dtype)
+    z = None
+    if want_z:
+        z = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        p.z, p.ldz = z.data_ptr(), N
+    _launch_linear(pgq.pgq_linear_forward, pgq.pgq_linear_forward_workspace, "pgq_linear_forward", p, dev)
+    return (out, z) if want_z else out
+
+
+def qlinear_backward(dy: torch.Tensor, codes: Optional[torch.Tensor], scales: Optional[torch.Tensor],
+                     x: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, act: str = "none",
+                     slope: float = 0.0, mask: Optional[torch.Tensor] = None, want_dx: bool = True,
+                     want_dw: bool = True, want_dbias: bool = False, dx_dtype: torch.dtype = torch.bfloat16,
+                     dw_dtype: torch.dtype = torch.bfloat16) -> Dict[str, torch.Tensor]:
+    """Gradients of qlinear: "dx" [M, K], "dw" [N, K] (of the bf16 weights, zeroed where the fake-quant
+    mask bit is 0) and "dbias" fp32 [N], each when wanted; the residual's gradient is dy itself.
+
+    dy: bf16 or fp32 [M, N]; z: the bf16 pre-activation of the forward call (not for act "none"); x:
+    bf16 [M, K] (for dw); codes, scales: as in qlinear (for dx); mask: uint8 [N, ceil(K / 8)]."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    (M, N), dev = dy.shape, dy.device
+    if want_dx and (codes is None or scales is None):
+        raise ValueError("dx needs codes and scales")
+    if want_dw and x is None:
+        raise ValueError("dw needs x")
+    if act != "none" and z is None:
+        raise ValueError(f"act {act!r} needs z")
+    K = codes.shape[1] if codes is not None else x.shape[1] if x is not None else 0
+    p = pgq.pgq_linear_bwd(M=M, N=N, K=K, act=ACTS[act], slope=slope)
+    p.lddy = _check_matrix("dy", dy, (M, N), _B16_F32, dev)
+    p.dy, p.dy_dtype = dy.data_ptr(), _dtype_code(dy.dtype)
+    if act != "none":
+        p.ldz = _check_matrix("z", z, (M, N), (torch.bfloat16,), dev)
+        p.z = z.data_ptr()
+    res = {}
+    if want_dx:
+        p.ldc = _check_matrix("codes", codes, (N, K), (torch.int8,), dev)
+        _check_vector("scales", scales, N, _SCALE_TYPES, dev)
+        res["dx"] = torch.empty(M, K, dtype=dx_dtype, device=dev)
+        p.codes, p.scales = codes.data_ptr(), scales.data_ptr()
+        p.dx, p.lddx, p.dx_dtype = res["dx"].data_ptr(), K, _dtype_code(dx_dtype)
+    if want_dw:
+        p.ldx = _check_matrix("x", x, (M, K), (torch.bfloat16,), dev)
+        res["dw"] = torch.empty(N, K, dtype=dw_dtype, device=dev)
+        p.x = x.data_ptr()
+        p.dw, p.lddw, p.dw_dtype = res["dw"].data_ptr(), K, _dtype_code(dw_dtype)
+        if mask is not None:
+            if tuple(mask.shape) != (N, (K + 7) // 8):
+                raise ValueError(f"mask: shape {tuple(mask.shape)}, expected {(N, (K + 7) // 8)}")
+            _check_vector("mask", mask, mask.numel(), (torch.uint8,), dev)
+            p.mask = mask.data_ptr()
+    if want_dbias:
+        res["dbias"] = torch.empty(N, dtype=torch.float32, device=dev)
+        p.dbias = res["dbias"].data_ptr()
+    _launch_linear(pgq.pgq_linear_backward, pgq.pgq_linear_backward_workspace, "pgq_linear_backward", p, dev)
+    return res

@@ -38,6 +38,11 @@ PGQ_FQ_FWD = 1
 PGQ_FQ_BWD = 2
 PGQ_FQ_FWD_BWD = 3
 
+PGQ_ACT_NONE = 0
+PGQ_ACT_RELU = 1
+PGQ_ACT_RELU2 = 2
+PGQ_ACT_SILU = 3
+
 
 class PgqError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
@@ -77,6 +82,27 @@ class pgq_tensor_plan(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class pgq_linear_fwd(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ldr", ctypes.c_int64), ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("slope", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class pgq_linear_bwd(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("dy", ctypes.c_void_p),
+                ("lddy", ctypes.c_int64), ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("dbias", ctypes.c_void_p), ("dy_dtype", ctypes.c_int32), ("dx_dtype", ctypes.c_int32),
+                ("dw_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("slope", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -101,6 +127,10 @@ SIGNATURES = {
     "pgq_qgemm_bf16_ybf16": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
     "pgq_dequant_model": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(pgq_tensor_plan), _P,
                                  ctypes.POINTER(_P), _P, _SZ, _U32, _P, _P]),
+    "pgq_linear_forward_workspace": (_I32, [ctypes.POINTER(pgq_linear_fwd), ctypes.POINTER(_SZ)]),
+    "pgq_linear_backward_workspace": (_I32, [ctypes.POINTER(pgq_linear_bwd), ctypes.POINTER(_SZ)]),
+    "pgq_linear_forward": (_I32, [ctypes.POINTER(pgq_linear_fwd), _P, _SZ, _P]),
+    "pgq_linear_backward": (_I32, [ctypes.POINTER(pgq_linear_bwd), _P, _SZ, _P]),
     "pgq_average_workspace": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_SZ)]),
     "pgq_ema_update": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_P), ctypes.c_float, _I32, _P,
                               _SZ, _U32, _P, _P]),
@@ -182,6 +212,22 @@ def pgq_dequant_codes(codes, packed, rows, cols, scales, per_tensor, awq_mult, o
 
 def pgq_dequant_model(t, n, plan, arena, out, workspace, workspace_bytes, flags, dev_status, stream):
     return _lib.pgq_dequant_model(t, n, plan, arena, out, workspace, workspace_bytes, flags, dev_status, stream)
+
+
+def pgq_linear_forward_workspace(p, workspace_bytes):
+    return _lib.pgq_linear_forward_workspace(p, workspace_bytes)
+
+
+def pgq_linear_backward_workspace(p, workspace_bytes):
+    return _lib.pgq_linear_backward_workspace(p, workspace_bytes)
+
+
+def pgq_linear_forward(p, workspace, workspace_bytes, stream):
+    return _lib.pgq_linear_forward(p, workspace, workspace_bytes, stream)
+
+
+def pgq_linear_backward(p, workspace, workspace_bytes, stream):
+    return _lib.pgq_linear_backward(p, workspace, workspace_bytes, stream)
 
 
 def pgq_average_workspace(w, n, workspace_bytes):

@@ -1,0 +1,79 @@
+"""The linear layer's C ABI on the CPU: argument errors come back before anything is enqueued."""
+import ctypes
+
+import pytest
+
+pgq = pytest.importorskip("int6_weight_export_amd.pgq")
+
+FAKE = 0x10000      # aligned, never dereferenced: every call here fails its checks or has nothing to do
+
+
+def fwd(**kw):
+    a = dict(M=4, N=8, K=16, x=FAKE, ldx=16, codes=FAKE, ldc=16, scales=FAKE, y=FAKE, ldy=8, y_dtype=pgq.PGQ_BF16,
+             act=pgq.PGQ_ACT_NONE)
+    a.update(kw)
+    return pgq.pgq_linear_fwd(**a)
+
+
+def bwd(**kw):
+    a = dict(M=4, N=8, K=16, dy=FAKE, lddy=8, dy_dtype=pgq.PGQ_BF16, x=FAKE, ldx=16, codes=FAKE, ldc=16, scales=FAKE,
+             dx=FAKE, lddx=16, dx_dtype=pgq.PGQ_BF16, dw=FAKE, lddw=16, dw_dtype=pgq.PGQ_BF16, dbias=FAKE)
+    a.update(kw)
+    return pgq.pgq_linear_bwd(**a)
+
+
+FWD_ERRORS = [
+    (dict(M=-1), pgq.PGQ_ERR_SHAPE), (dict(N=1 << 31, ldy=1 << 31), pgq.PGQ_ERR_SHAPE), (dict(ldx=15), pgq.PGQ_ERR_SHAPE),
+    (dict(ldc=15), pgq.PGQ_ERR_SHAPE), (dict(ldy=7), pgq.PGQ_ERR_SHAPE),
+    (dict(residual=FAKE, ldr=7, residual_dtype=pgq.PGQ_F32), pgq.PGQ_ERR_SHAPE), (dict(z=FAKE, ldz=7), pgq.PGQ_ERR_SHAPE),
+    (dict(y_dtype=pgq.PGQ_F16), pgq.PGQ_ERR_DTYPE), (dict(bias=FAKE, bias_dtype=pgq.PGQ_F16), pgq.PGQ_ERR_DTYPE),
+    (dict(residual=FAKE, ldr=8, residual_dtype=9), pgq.PGQ_ERR_DTYPE),
+    (dict(act=4), pgq.PGQ_ERR_PARAM), (dict(act=-1), pgq.PGQ_ERR_PARAM), (dict(reserved=1), pgq.PGQ_ERR_PARAM),
+    (dict(act=pgq.PGQ_ACT_RELU, slope=float("nan")), pgq.PGQ_ERR_PARAM),
+    (dict(act=pgq.PGQ_ACT_RELU2, slope=float("inf")), pgq.PGQ_ERR_PARAM),
+    (dict(residual=FAKE, ldr=8, residual_dtype=pgq.PGQ_F32), pgq.PGQ_ERR_PARAM),        # y as residual of another type
+    (dict(residual=FAKE, ldr=9, residual_dtype=pgq.PGQ_BF16), pgq.PGQ_ERR_PARAM),
+    (dict(x=None), pgq.PGQ_ERR_NULL), (dict(codes=None), pgq.PGQ_ERR_NULL), (dict(scales=None), pgq.PGQ_ERR_NULL),
+    (dict(y=None), pgq.PGQ_ERR_NULL), (dict(y=FAKE + 1), pgq.PGQ_ERR_ALIGN), (dict(x=FAKE + 1), pgq.PGQ_ERR_ALIGN),
+    (dict(bias=FAKE + 2, bias_dtype=pgq.PGQ_F32), pgq.PGQ_ERR_ALIGN), (dict(z=FAKE + 1, ldz=8), pgq.PGQ_ERR_ALIGN),
+    (dict(scales=FAKE + 1), pgq.PGQ_ERR_ALIGN),
+]
+
+BWD_ERRORS = [
+    (dict(K=-1), pgq.PGQ_ERR_SHAPE), (dict(lddy=7), pgq.PGQ_ERR_SHAPE), (dict(ldx=15), pgq.PGQ_ERR_SHAPE),
+    (dict(ldc=15), pgq.PGQ_ERR_SHAPE), (dict(lddx=15), pgq.PGQ_ERR_SHAPE), (dict(lddw=15), pgq.PGQ_ERR_SHAPE),
+    (dict(act=pgq.PGQ_ACT_SILU, z=FAKE, ldz=7), pgq.PGQ_ERR_SHAPE),
+    (dict(dy_dtype=pgq.PGQ_F16), pgq.PGQ_ERR_DTYPE), (dict(dx_dtype=pgq.PGQ_F16), pgq.PGQ_ERR_DTYPE),
+    (dict(dw_dtype=7), pgq.PGQ_ERR_DTYPE), (dict(act=9), pgq.PGQ_ERR_PARAM), (dict(reserved=3), pgq.PGQ_ERR_PARAM),
+    (dict(act=pgq.PGQ_ACT_SILU, ldz=8), pgq.PGQ_ERR_NULL), (dict(dy=None), pgq.PGQ_ERR_NULL),
+    (dict(x=None), pgq.PGQ_ERR_NULL), (dict(codes=None), pgq.PGQ_ERR_NULL), (dict(scales=None), pgq.PGQ_ERR_NULL),
+    (dict(dy=FAKE + 2, dy_dtype=pgq.PGQ_F32), pgq.PGQ_ERR_ALIGN), (dict(dx=FAKE + 1), pgq.PGQ_ERR_ALIGN),
+    (dict(dw=FAKE + 2, dw_dtype=pgq.PGQ_F32), pgq.PGQ_ERR_ALIGN), (dict(dbias=FAKE + 2), pgq.PGQ_ERR_ALIGN),
+]
+
+
+@pytest.mark.parametrize("args,want", FWD_ERRORS)
+def test_forward_argument_errors(args, want):
+    p, n = fwd(**args), ctypes.c_size_t(0)
+    assert pgq.pgq_linear_forward(ctypes.byref(p), None, 0, None) == want
+    assert pgq.pgq_linear_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == want
+
+
+@pytest.mark.parametrize("args,want", BWD_ERRORS)
+def test_backward_argument_errors(args, want):
+    p, n = bwd(**args), ctypes.c_size_t(0)
+    assert pgq.pgq_linear_backward(ctypes.byref(p), None, 0, None) == want
+    assert pgq.pgq_linear_backward_workspace(ctypes.byref(p), ctypes.byref(n)) == want
+
+
+def test_null_descriptors_and_empty_calls():
+    n = ctypes.c_size_t(0)
+    assert pgq.pgq_linear_forward(None, None, 0, None) == pgq.PGQ_ERR_NULL
+    assert pgq.pgq_linear_backward(None, None, 0, None) == pgq.PGQ_ERR_NULL
+    assert pgq.pgq_linear_forward_workspace(ctypes.byref(fwd()), None) == pgq.PGQ_ERR_NULL
+    assert pgq.pgq_linear_backward_workspace(ctypes.byref(bwd()), None) == pgq.PGQ_ERR_NULL
+    assert pgq.pgq_linear_forward(ctypes.byref(fwd(M=0)), None, 0, None) == pgq.PGQ_OK
+    assert pgq.pgq_linear_forward(ctypes.byref(fwd(N=0, y=None, ldy=0)), None, 0, None) == pgq.PGQ_OK
+    nothing = bwd(dx=None, dw=None, dbias=None)
+    assert pgq.pgq_linear_backward(ctypes.byref(nothing), None, 0, None) == pgq.PGQ_OK
+    assert pgq.pgq_linear_backward_workspace(ctypes.byref(nothing), ctypes.byref(n)) == pgq.PGQ_OK and n.value == 0

@@ -394,6 +394,82 @@ pgq_status pgq_swa_accumulate(const pgq_tensor_in* w, int32_t n, float* const* m
                               size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* AdamW over n tensors in one grouped launch, states in binary32 or in 8 bits.  Source: the    */
+/* AdamW groups of the PR #69 card, section Optimizer (a learning rate for each group).        */
+/* Every step one IEEE binary32 operation, no fused multiply-add; for one element, with         */
+/* lr_i = fl(lr_scale_i * lr) and the constants of pgq_adamw_hyper:                             */
+/*   g  = fl(grad_scale * grad)          (binary32 of the gradient first)                       */
+/*   m' = fl(fl(m * beta1) + fl(g * c1));  v' = fl(fl(v * beta2) + fl(fl(g * g) * c2))          */
+/*   w' = fl(fl(w * fl(1 - fl(lr_i * weight_decay_i)))                                          */
+/*           - fl(fl(m' / fl(fl(sqrt(v') * ib2) + eps)) * fl(lr_i * ib1)))                      */
+/* w fp32, or bf16 (rounded to nearest even at the store); copy: bf16 of the stored fp32 w', the */
+/* weights that the next fake-quant forward reads.  An element whose m' or v' is not finite (a  */
+/* NaN or infinite gradient, or one whose square overflows) keeps w, m and v, and               */
+/* PGQ_DEV_NONFINITE is set.                                                                  */
+/* States in 8 bits.  m and r = sqrt(v) are held (v enters as fl(r * r)), one byte each, with a  */
+/* scale byte for every 64 consecutive elements of the tensor and state.  With the scale byte b  */
+/* and magnitude code c (m: bit 7 is the sign, c the low 7 bits; r: c is the byte) the value is  */
+/* x * 2^(b - 7), x being the binary32 number whose bits are c << 20 (m: 4 exponent and 3        */
+/* mantissa bits) or c << 19 (r: 4 and 4).  b = max(E - 7, 0), E the biased exponent of the      */
+/* block's largest |m'| or r'.  Rounding is stochastic, so that a change smaller than a code's   */
+/* step still acts on average: with y = |value| * 2^(7 - b) in binary32, c = (bits(y) + (u <<     */
+/* 4)) >> 20 (r: (u << 3)) >> 19, and never 0 for r' > 0), u the high (m) or low (r) 16 bits of   */
+/* mix(mix(0x9E3779B1 * (i + 1) + seed) ^ j) for element j of tensor i (both modulo 2^32), with    */
+/* mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16.           */
+/* All-zero bytes are the state 0.                                                            */
+/* ------------------------------------------------------------------------------------------ */
+
+typedef struct {
+    void* w;                 /* w_dtype, numel, dense; updated in place */
+    uint16_t* copy;          /* NULL or bf16, numel (PGQ_F32 w only) */
+    void* m;                 /* fp32 numel, or codes: numel bytes */
+    void* v;                 /* fp32 numel, or the codes of r */
+    uint8_t* m_scale;        /* 8 bits: ceil(numel / 64) bytes each; unused for 32 */
+    uint8_t* v_scale;
+    int64_t numel;
+    int32_t w_dtype;         /* PGQ_F32 or PGQ_BF16 */
+    int32_t g_dtype;         /* gradient: PGQ_F32, PGQ_BF16 or PGQ_F16 */
+    float lr_scale;          /* this tensor's share of lr */
+    float weight_decay;
+} pgq_adamw_tensor;
+
+typedef struct {
+    float lr;
+    float beta1, c1;         /* c1 = 1 - beta1, formed before rounding to binary32 */
+    float beta2, c2;
+    float ib1;               /* 1 / (1 - beta1^step) */
+    float ib2;               /* 1 / sqrt(1 - beta2^step) */
+    float eps;
+    float grad_scale;
+    uint32_t seed;           /* of the stochastic rounding; another one each step */
+} pgq_adamw_hyper;
+
+/* Host only: the constants of step number `step` (1-based).  0 <= beta < 1, lr, eps >= 0 and finite. */
+pgq_status pgq_adamw_hyper_at(double lr, double beta1, double beta2, double eps, int64_t step, float grad_scale,
+                              uint32_t seed, pgq_adamw_hyper* out);
+
+/* Workspace bytes (the descriptor table) of the calls below. */
+pgq_status pgq_adamw_workspace(const pgq_adamw_tensor* t, int32_t n, size_t* workspace_bytes);
+
+/* state_bits: 32 or 8.  grad: host array of n device pointers (numel dense values of g_dtype).  They and
+ * g_dtype may change from call to call: they are kernel arguments, not part of the table.  h: host, read during the
+ * call -- or, when h_dev is not NULL, h is ignored and the kernel reads the constants from device memory,
+ * so that a recorded graph can be replayed with those of each step.  workspace: 64-byte aligned; flags: 0
+ * or PGQ_TABLE_RESIDENT as for the other grouped calls.  While the stream is being captured only a resident
+ * table is accepted (PGQ_ERR_PARAM otherwise): its upload would be replayed from freed host memory.  No
+ * two tensors may overlap. */
+pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bits, const void* const* grad,
+                          const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, void* workspace,
+                          size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream);
+
+/* The values 8-bit states stand for, m and r = sqrt(v), as bf16 (exact: 4 and 5 significant bits; a value
+ * below bf16's range becomes a subnormal or zero).  m_out, r_out: host arrays of n device pointers (numel
+ * bf16 each).  The table is the step's: same workspace and flags. */
+pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* const* m_out, uint16_t* const* r_out,
+                            void* workspace, size_t workspace_bytes, uint32_t flags, uint32_t* dev_status,
+                            void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Timing aid (no method step): the next pgq_* call made by this host thread that launches     */
 /* kernels records start_event when its first kernel begins executing and stop_event when its */
 /* last kernel completes, from the kernels' own dispatches (hipExtLaunchKernel), so the pair   */

@@ -509,3 +509,140 @@ def qlinear_backward(dy: torch.Tensor, codes: Optional[torch.Tensor], scales: Op
         p.dbias = res["dbias"].data_ptr()
     _launch_linear(pgq.pgq_linear_backward, pgq.pgq_linear_backward_workspace, "pgq_linear_backward", p, dev)
     return res
+
+
+def _same_device(tensors: Sequence[Optional[torch.Tensor]], device) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"a tensor is on {t.device}, expected {device}")
+
+
+def _dense(name: str, t: torch.Tensor, numel: int, dtypes) -> None:
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: {numel} dense values expected")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+
+
+class AdamW:
+    """AdamW over a fixed list of weight tensors (fp32 or bf16, dense), one grouped launch a step.
+
+    lr_scale, weight_decay: one number, or one per tensor.  state_bits: 32 (fp32 m and v) or 8 (codes
+    of m and sqrt(v) with a scale byte for every 64 elements).  copies: bf16 tensors (or None each)
+    that receive the updated fp32 weights.  states: existing state tensors to go on from -- per tensor
+    (m, v), or (m, v, m_scale, v_scale) for 8 bits; zero states are made when it is None.  The
+    first step (or decode) uploads the descriptor table, so it cannot be the captured one; the steps
+    after it take only the gradients."""
+
+    def __init__(self, weights: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay=0.01, lr_scale=1.0, state_bits: int = 32, states=None, copies=None,
+                 step_count: int = 0, seed: int = 0):
+        self.weights = list(weights)
+        self.n = n = len(self.weights)
+        if n == 0:
+            raise ValueError("no weights")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.lr, self.betas, self.eps, self.state_bits = lr, betas, eps, state_bits
+        self.step_count, self.seed = step_count, seed
+        self.device = self.weights[0].device
+        self.copies = list(copies) if copies is not None else [None] * n
+        per = [[x] * n if isinstance(x, (int, float)) else list(x) for x in (lr_scale, weight_decay)]
+        if states is None:
+            states = [self._zero_state(w.numel()) for w in self.weights]
+        self.states = [tuple(s) for s in states]
+        if any(len(x) != n for x in (self.copies, self.states, *per)):
+            raise ValueError(f"{n} tensors: copies, states, lr_scale and weight_decay must have as many entries")
+        self._arr = (pgq.pgq_adamw_tensor * n)()
+        for i, (w, c, s) in enumerate(zip(self.weights, self.copies, self.states)):
+            k = w.numel()
+            _dense("weight", w, k, _B16_F32)
+            _same_device((w, c, *s), self.device)
+            kinds = (torch.float32,) if state_bits == 32 else (torch.uint8,)
+            if len(s) != (2 if state_bits == 32 else 4):
+                raise ValueError(f"{state_bits}-bit states: {2 if state_bits == 32 else 4} tensors each")
+            for name, t, m in zip(("m", "v", "m_scale", "v_scale"), s, (k, k, (k + 63) // 64, (k + 63) // 64)):
+                _dense(name, t, m, kinds)
+            if c is not None:
+                _dense("copy", c, k, (torch.bfloat16,))
+            self._arr[i] = pgq.pgq_adamw_tensor(
+                w.data_ptr(), 0 if c is None else c.data_ptr(), s[0].data_ptr(), s[1].data_ptr(),
+                s[2].data_ptr() if state_bits == 8 else 0, s[3].data_ptr() if state_bits == 8 else 0, k,
+                _dtype_code(w.dtype), pgq.PGQ_F32, per[0][i], per[1][i])
+        need = ctypes.c_size_t(0)
+        pgq.check(pgq.pgq_adamw_workspace(self._arr, n, ctypes.byref(need)), "pgq_adamw_workspace")
+        self.workspace = torch.empty(max(need.value, 64), dtype=torch.uint8, device=self.device)
+        self.status = new_status(self.device)
+        self.hyper = torch.zeros(10, dtype=torch.int32, device=self.device)
+        self._uploaded = False
+
+    def _zero_state(self, k: int):
+        if self.state_bits == 32:
+            return tuple(torch.zeros(k, dtype=torch.float32, device=self.device) for _ in range(2))
+        return tuple(torch.zeros(m, dtype=torch.uint8, device=self.device) for m in (k, k, (k + 63) // 64, (k + 63) // 64))
+
+    def _hyper(self, lr, grad_scale: float) -> pgq.pgq_adamw_hyper:
+        h = pgq.pgq_adamw_hyper()
+        pgq.check(pgq.pgq_adamw_hyper_at(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
+                                         self.step_count, grad_scale, (self.seed + self.step_count) & 0xFFFFFFFF,
+                                         ctypes.byref(h)), "pgq_adamw_hyper_at")
+        return h
+
+    def load_hyper(self, lr: Optional[float] = None, grad_scale: float = 1.0) -> None:
+        """Count a step and write its constants to device memory, for a step that reads them there
+        (device_hyper=True): before each replay of a graph that holds such a step."""
+        self.step_count += 1
+        host = torch.frombuffer(bytearray(bytes(self._hyper(lr, grad_scale))), dtype=torch.int32)
+        self.hyper.copy_(host)
+
+    def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
+             device_hyper: bool = False) -> None:
+        """One update from the gradients (fp32, bf16 or fp16, dense).  device_hyper: take the constants that load_hyper wrote instead of counting
+        this step here."""
+        if len(grads) != self.n:
+            raise ValueError(f"{len(grads)} gradients for {self.n} weights")
+        ptrs = (ctypes.c_void_p * self.n)()
+        for i, (g, w) in enumerate(zip(grads, self.weights)):
+            if g.numel() != w.numel() or not g.is_contiguous():
+                raise ValueError(f"gradient {i}: {w.numel()} dense values expected")
+            if g.device != self.device:
+                raise ValueError(f"gradient {i} is on {g.device}, expected {self.device}")
+            ptrs[i] = g.data_ptr()
+            self._arr[i].g_dtype = _dtype_code(g.dtype)
+        if not device_hyper:
+            self.step_count += 1
+        h = None if device_hyper else ctypes.byref(self._hyper(lr, grad_scale))
+        with torch.cuda.device(self.device):
+            rc = pgq.pgq_adamw_step(self._arr, self.n, self.state_bits, ptrs, h, _p(self.hyper) if device_hyper else None,
+                                    _p(self.workspace), self.workspace.numel(), self._table_flags(), _p(self.status),
+                                    _stream())
+        if rc != pgq.PGQ_OK and not device_hyper:
+            self.step_count -= 1
+        pgq.check(rc, "pgq_adamw_step")
+        self._uploaded = True
+
+    def _table_flags(self) -> int:
+        return pgq.PGQ_TABLE_RESIDENT if self._uploaded else 0
+
+    def decode_states(self, m_out: Optional[Sequence[torch.Tensor]] = None,
+                      r_out: Optional[Sequence[torch.Tensor]] = None):
+        """The values that 8-bit states hold: lists of bf16 tensors m and r = sqrt(v) (exact)."""
+        if self.state_bits != 8:
+            raise ValueError("32-bit states are held as values")
+        outs = []
+        for given in (m_out, r_out):
+            if given is None:
+                given = [torch.empty(w.numel(), dtype=torch.bfloat16, device=self.device) for w in self.weights]
+            if len(given) != self.n:
+                raise ValueError(f"{len(given)} outputs for {self.n} weights")
+            _same_device(given, self.device)
+            for t, w in zip(given, self.weights):
+                _dense("output", t, w.numel(), (torch.bfloat16,))
+            outs.append(given)
+        ptrs = [(ctypes.c_void_p * self.n)(*[t.data_ptr() for t in o]) for o in outs]
+        with torch.cuda.device(self.device):
+            rc = pgq.pgq_adamw_decode(self._arr, self.n, ptrs[0], ptrs[1], _p(self.workspace), self.workspace.numel(),
+                                      self._table_flags(), _p(self.status), _stream())
+        pgq.check(rc, "pgq_adamw_decode")
+        self._uploaded = True
+        return outs[0], outs[1]

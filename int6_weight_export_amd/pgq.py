@@ -103,6 +103,19 @@ class pgq_linear_bwd(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class pgq_adamw_tensor(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("lr_scale", ctypes.c_float),
+                ("weight_decay", ctypes.c_float)]
+
+
+class pgq_adamw_hyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("c1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("c2", ctypes.c_float), ("ib1", ctypes.c_float), ("ib2", ctypes.c_float), ("eps", ctypes.c_float),
+                ("grad_scale", ctypes.c_float), ("seed", ctypes.c_uint32)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -136,6 +149,13 @@ SIGNATURES = {
                               _SZ, _U32, _P, _P]),
     "pgq_swa_accumulate": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_P), _I32, _P, _SZ, _U32,
                                   _P, _P]),
+    "pgq_adamw_hyper_at": (_I32, [ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double, _I64,
+                                  ctypes.c_float, _U32, ctypes.POINTER(pgq_adamw_hyper)]),
+    "pgq_adamw_workspace": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, ctypes.POINTER(_SZ)]),
+    "pgq_adamw_step": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, _I32, ctypes.POINTER(_P),
+                              ctypes.POINTER(pgq_adamw_hyper), _P, _P, _SZ, _U32, _P, _P]),
+    "pgq_adamw_decode": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, ctypes.POINTER(_P), ctypes.POINTER(_P), _P,
+                                _SZ, _U32, _P, _P]),
     "pgq_time_next_launch": (_I32, [_P, _P]),
     "pgq_status_str": (ctypes.c_char_p, [_I32]),
     "pgq_version": (ctypes.c_char_p, []),
@@ -240,6 +260,22 @@ def pgq_ema_update(w, n, ema, decay, init, workspace, workspace_bytes, flags, de
 
 def pgq_swa_accumulate(w, n, mean, k, workspace, workspace_bytes, flags, dev_status, stream):
     return _lib.pgq_swa_accumulate(w, n, mean, k, workspace, workspace_bytes, flags, dev_status, stream)
+
+
+def pgq_adamw_hyper_at(lr, beta1, beta2, eps, step, grad_scale, seed, out):
+    return _lib.pgq_adamw_hyper_at(lr, beta1, beta2, eps, step, grad_scale, seed, out)
+
+
+def pgq_adamw_workspace(t, n, workspace_bytes):
+    return _lib.pgq_adamw_workspace(t, n, workspace_bytes)
+
+
+def pgq_adamw_step(t, n, state_bits, grad, h, h_dev, workspace, workspace_bytes, flags, dev_status, stream):
+    return _lib.pgq_adamw_step(t, n, state_bits, grad, h, h_dev, workspace, workspace_bytes, flags, dev_status, stream)
+
+
+def pgq_adamw_decode(t, n, m_out, r_out, workspace, workspace_bytes, flags, dev_status, stream):
+    return _lib.pgq_adamw_decode(t, n, m_out, r_out, workspace, workspace_bytes, flags, dev_status, stream)
 
 
 def pgq_time_next_launch(start_event, stop_event):

@@ -42,7 +42,7 @@ HBM_PEAK_GBS = 8000.0
 MFMA_BF16_PEAK_TFLOPS = 2500.0          # dense bf16 matrix-core peak of the MI355X
 RIDGE_FLOP_PER_BYTE = MFMA_BF16_PEAK_TFLOPS * 1e12 / (HBM_PEAK_GBS * 1e9)   # 312.5
 # the linear layer and the optimizer step have kernels of their own that no mode here launches
-OTHER_SOURCES = ("pgq_linear.hip", "pgq_adamw.hip", "pgq_train.h")
+OTHER_SOURCES = ("pgq_linear.hip", "pgq_linear_mm.hip", "pgq_linear.h", "pgq_adamw.hip", "pgq_train.h")
 KERNEL_SOURCES = sorted(os.path.relpath(p, ROOT) for p in glob.glob(os.path.join(ROOT, "int6_weight_export_amd", "csrc", "*"))
                         if p.endswith((".hip", ".h")) and not p.endswith(OTHER_SOURCES))
 GEMM_SOURCE = os.path.join("int6_weight_export_amd", "csrc", "pgq_gemm.hip")

@@ -1,0 +1,78 @@
+// pgq_linear.h -- the matrix products behind the linear layer (pgq_linear_mm.hip), as its host layer
+// (pgq_linear.hip) calls them.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/pgq.h"
+
+namespace pgq {
+
+__device__ __forceinline__ float f16_to_f32(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
+__device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+// 1 / (1 + e^-z): the exponential within 2 units of the last place, the reciprocal within 1
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+
+__device__ __forceinline__ float act_value(int32_t act, float slope, float z)
+{
+    if (act == PGQ_ACT_NONE) return z;
+    if (act == PGQ_ACT_SILU) return z * sigmoid(z);
+    const float r = z > 0.0f ? z : z * slope;
+    return act == PGQ_ACT_RELU ? r : r * r;
+}
+__device__ __forceinline__ float act_slope(int32_t act, float slope, float z)
+{
+    if (act == PGQ_ACT_NONE) return 1.0f;
+    if (act == PGQ_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    const float d = z > 0.0f ? 1.0f : slope;
+    return act == PGQ_ACT_RELU ? d : 2.0f * z * d * d;
+}
+
+// What a product does with its sums on the way out: v = act(sum + bias) + residual, Z stored on the side.
+struct Epilogue {
+    const void* bias;            // per column
+    const void* residual;        // I x J
+    uint16_t* z;                 // I x J bf16
+    void* y;                     // I x J
+    int64_t ldr, ldz, ldy;
+    int32_t bias_dtype, residual_dtype, y_dtype, act;
+    float slope;
+    int32_t vec;                 // rows of y, z and residual take 16-byte accesses of 8 (bf16) or 4 (fp32) columns
+};
+
+// Y[i][j] = epilogue(sum_l A[i][l] B[j][l]): bf16 operands, 16-byte aligned rows, L a multiple of 8 and
+// row strides below 2^21 elements.
+struct MmNt {
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t lda, ldb, I, J, L;
+    Epilogue e;
+};
+hipError_t launch_mm_nt(const MmNt& p, void* stream);
+
+// C[i][j] = sum_l A[l][i] B[l][j]: bf16 operands, 16-byte aligned rows of at least I and J elements rounded
+// up to 8, row strides below 2^23.  C goes out as dw_dtype, zero where the mask bit of (i, j) is 0.
+struct MmTt {
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t lda, ldb, I, J, L;
+    void* c;
+    int64_t ldc;
+    int32_t c_dtype;
+    int32_t splits;              // parts the sum over l is cut into (mm_tt_splits)
+    int64_t chunk;               // l per part, a multiple of 64
+    const uint8_t* mask;         // NULL or I x ceil(J / 8) bytes
+    float* partial;              // splits > 1: mm_tt_partial_bytes() of scratch
+};
+void mm_tt_split(int64_t I, int64_t J, int64_t L, int32_t* splits, int64_t* chunk);
+size_t mm_tt_partial_bytes(int64_t I, int64_t J, int32_t splits);
+hipError_t launch_mm_tt(const MmTt& p, void* stream);
+// splits > 1: the sum of the parts, in their order
+hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream);
+
+}  // namespace pgq

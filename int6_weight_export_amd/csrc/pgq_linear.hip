@@ -13,18 +13,19 @@
 #include <algorithm>
 
 #include "pgq_desc.h"
+#include "pgq_linear.h"
 #include "pgq_train.h"
 #include "../../include/pgq.h"
 
 namespace pgq {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+#define GLB __attribute__((address_space(1)))
 
-__device__ __forceinline__ float f16_to_f32(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
-__device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
-__device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float load_any(const void* p, int32_t dtype, int64_t i)
 {
@@ -34,24 +35,6 @@ __device__ __forceinline__ void store_any(void* p, int32_t dtype, int64_t i, flo
 {
     if (dtype == PGQ_F32) static_cast<float*>(p)[i] = v;
     else static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
-}
-
-__device__ __forceinline__ float act_value(int32_t act, float slope, float z)
-{
-    if (act == PGQ_ACT_NONE) return z;
-    if (act == PGQ_ACT_SILU) return z / (1.0f + expf(-z));
-    const float r = z > 0.0f ? z : z * slope;
-    return act == PGQ_ACT_RELU ? r : r * r;
-}
-__device__ __forceinline__ float act_slope(int32_t act, float slope, float z)
-{
-    if (act == PGQ_ACT_NONE) return 1.0f;
-    if (act == PGQ_ACT_SILU) {
-        const float s = 1.0f / (1.0f + expf(-z));
-        return s * (1.0f + z * (1.0f - s));
-    }
-    const float d = z > 0.0f ? 1.0f : slope;
-    return act == PGQ_ACT_RELU ? d : 2.0f * z * d * d;
 }
 
 enum Product { P_FWD, P_DX, P_DW };
@@ -134,18 +117,333 @@ __global__ void __launch_bounds__(256) pgq_linear_tile_kernel(pgq_linear_fwd f, 
     }
 }
 
-// db[n] = sum over m of the unrounded dZ: 64 columns per workgroup, four row phases joined in LDS
-__global__ void __launch_bounds__(256) pgq_linear_dbias_kernel(pgq_linear_bwd b)
+// 16 (8) bytes at any alignment: one load, the hardware takes unaligned global addresses
+__device__ __forceinline__ u32x4 load16(const void* p)
 {
-    __shared__ float part[4][64];
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ uint64_t load8(const void* p)
+{
+    uint64_t v;
+    __builtin_memcpy(&v, p, 8);
+    return v;
+}
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) { return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16); }
+
+// ---- operands laid out for the matrix products --------------------------------------------------------
+// One launch prepares everything the products of a call read: dZ (and the partial sums of db), What as bf16
+// rows (forward) or transposed (dX), and a copy of X with 16-byte aligned rows where X has none.  Rows are
+// padded to 8 elements with zeros.  What is formed once here instead of in every tile: it is small beside X
+// and Y, and its conversion from codes cost the matrix kernel about a sixth of its time.
+constexpr int kDzRows = 64, kDzCols = 256;     // dZ unit
+constexpr int kFlat = 256 * 4;                 // granules (8 elements) of a flat unit
+
+struct Prep {
+    pgq_linear_bwd b;            // the sources (codes, scales, x and their strides also in forward)
+    uint16_t* dz;                // M x ldz_out, or NULL: only the partial sums
+    float* dbias_part;           // ceil(M / kDzRows) x N, or NULL
+    uint16_t* what;              // N x Kp
+    uint16_t* what_t;            // K x Np
+    uint16_t* xc;                // M x Kp
+    int64_t Kp, Np;
+    int64_t n_dz, n_what, n_what_t, n_x;      // units of each kind, in this order
+};
+
+// two bf16 of a word as fp32
+__device__ __forceinline__ void unpack2(uint32_t w, float* f)
+{
+    f[0] = __builtin_bit_cast(float, w << 16);
+    f[1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
+}
+
+// A thread takes 8 columns of every eighth row of the unit.  Whole granules: the loads of kHold rows are
+// issued together (rows past M repeat the last one and are not used); the ragged edge goes element by element.
+template <bool F32, bool ACT>
+__device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums)
+{
+    constexpr int kHold = 4;
+    const pgq_linear_bwd& b = p.b;
+    const int64_t cu = (p.Np + kDzCols - 1) / kDzCols;
+    const int64_t rb = unit / cu, n = unit % cu * kDzCols + ((int)threadIdx.x & 31) * 8;
+    const int phase = (int)threadIdx.x >> 5;
+    float t[8] = {};
+    auto out = [&](int64_t m, const float* d) __attribute__((always_inline)) {
+        if (p.dz)
+            *(GLB u32x4*)(p.dz + m * p.Np + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] += d[e];
+    };
+    if (n + 8 <= b.N) {
+#pragma unroll
+        for (int k0 = 0; k0 < kDzRows / 8; k0 += kHold) {
+            u32x4 v[kHold][F32 ? 2 : 1], zv[kHold];
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const int64_t m = min(rb * kDzRows + phase + 8 * (k0 + k), b.M - 1);
+                const uint8_t* src = (const uint8_t*)b.dy + (m * b.lddy + n) * (F32 ? 4 : 2);
+                v[k][0] = load16(src);
+                if constexpr (F32) v[k][1] = load16(src + 16);
+                if constexpr (ACT) zv[k] = load16(b.z + m * b.ldz + n);
+            }
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const int64_t m = rb * kDzRows + phase + 8 * (k0 + k);
+                float d[8];
+                if constexpr (F32) {
+                    const f32x4 lo = __builtin_bit_cast(f32x4, v[k][0]), hi = __builtin_bit_cast(f32x4, v[k][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { d[e] = lo[e]; d[4 + e] = hi[e]; }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) unpack2(v[k][0][e], d + 2 * e);
+                }
+                if constexpr (ACT) {
+                    float z[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) unpack2(zv[k][e], z + 2 * e);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] *= act_slope(b.act, b.slope, z[e]);
+                }
+                if (m < b.M) out(m, d);
+            }
+        }
+    } else if (n < p.Np) {
+#pragma unroll 1
+        for (int k = 0; k < kDzRows / 8; ++k) {
+            const int64_t m = rb * kDzRows + phase + 8 * k;
+            if (m >= b.M) break;
+            float d[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d[e] = n + e < b.N ? load_any(b.dy, b.dy_dtype, m * b.lddy + n + e) : 0.0f;
+                if (ACT && n + e < b.N) d[e] *= act_slope(b.act, b.slope, bf16_to_f32(b.z[m * b.ldz + n + e]));
+            }
+            out(m, d);
+        }
+    }
+    if (!p.dbias_part) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[phase * kDzCols + ((int)threadIdx.x & 31) * 8 + e] = t[e];
+    __syncthreads();
+    const int64_t c = unit % cu * kDzCols + threadIdx.x;
+    if (c < b.N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += sums[k * kDzCols + threadIdx.x];
+        p.dbias_part[rb * b.N + c] = v;
+    }
+}
+
+__device__ __forceinline__ void prep_what_t(const Prep& p, int64_t unit, uint16_t* t)
+{
+    constexpr int kPitch = 64 + 8;
+    const pgq_linear_bwd& b = p.b;
+    const int64_t nu = (p.Np + 63) / 64;
+    const int64_t n0 = unit % nu * 64, k0 = unit / nu * 64;
+    const int tid = (int)threadIdx.x;
+    {
+        const int64_t n = n0 + (tid >> 2), k = k0 + (tid & 3) * 16;
+        int8_t q[16] = {};
+        float s = 0.0f;
+        if (n < b.N) {
+            s = f16_to_f32(b.scales[n]);
+            if (k + 16 <= b.K) {
+                const u32x4 v = load16(b.codes + n * b.ldc + k);
+                __builtin_memcpy(q, &v, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) q[e] = k + e < b.K ? b.codes[n * b.ldc + k + e] : (int8_t)0;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) t[((tid & 3) * 16 + e) * kPitch + (tid >> 2)] = n < b.N ? f32_to_bf16((float)q[e] * s) : (uint16_t)0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int r = (tid >> 3) + 32 * c, g = tid & 7;
+        const int64_t k = k0 + r, n = n0 + 8 * g;
+        if (k < b.K && n < p.Np) *(GLB u32x4*)(p.what_t + k * p.Np + n) = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
+    }
+}
+
+__global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
+{
+    __shared__ __align__(16) float lds[8 * kDzCols];           // 8 KB; the transpose needs 9 KB as halves
+    __shared__ __align__(16) uint16_t tr[64 * 72];
+    int64_t unit = blockIdx.x;
+    if (unit < p.n_dz) {
+        const bool act = p.b.act != PGQ_ACT_NONE;
+        if (p.b.dy_dtype == PGQ_F32) return act ? prep_dz<true, true>(p, unit, lds) : prep_dz<true, false>(p, unit, lds);
+        return act ? prep_dz<false, true>(p, unit, lds) : prep_dz<false, false>(p, unit, lds);
+    }
+    unit -= p.n_dz;
+    if (unit < p.n_what_t) return prep_what_t(p, unit, tr);
+    unit -= p.n_what_t;
+    const bool what = unit < p.n_what;
+    if (!what) unit -= p.n_what;
+    const pgq_linear_bwd& b = p.b;
+    const int64_t g = p.Kp / 8, rows = what ? b.N : b.M;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int64_t i = unit * kFlat + c * 256 + threadIdx.x;
+        if (i >= rows * g) return;
+        const int64_t r = i / g, k = i % g * 8;
+        u32x4 o;
+        if (what) {
+            const float s = f16_to_f32(b.scales[r]);
+            const int8_t* src = b.codes + r * b.ldc + k;
+            int8_t q[8] = {};
+            if (k + 8 <= b.K) {
+                const uint64_t v = load8(src);
+                __builtin_memcpy(q, &v, 8);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[e] = k + e < b.K ? src[e] : (int8_t)0;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = k + 2 * e < b.K ? pk_bf16((float)q[2 * e] * s, k + 2 * e + 1 < b.K ? (float)q[2 * e + 1] * s : 0.0f) : 0u;
+            *(GLB u32x4*)(p.what + r * p.Kp + k) = o;
+        } else {
+            const uint16_t* src = b.x + r * b.ldx + k;
+            if (k + 8 <= b.K) {
+                o = load16(src);
+            } else {
+                uint16_t q[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[e] = k + e < b.K ? src[e] : (uint16_t)0;
+                __builtin_memcpy(&o, q, 16);
+            }
+            *(GLB u32x4*)(p.xc + r * p.Kp + k) = o;
+        }
+    }
+}
+
+// db[n]: the row blocks' partial sums, sixteen phases joined in a fixed order
+__global__ void __launch_bounds__(1024) pgq_linear_dbias_kernel(const float* part, int64_t blocks, int64_t N, float* dbias)
+{
+    __shared__ float sums[16][64];
+    const int lane = (int)threadIdx.x & 63, phase = (int)threadIdx.x >> 6;
     const int64_t n = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.0f;
-    if (n < b.N)
-        for (int64_t m = wave; m < b.M; m += 4) s += dz_at(b, m, n);
-    part[wave][lane] = s;
+    if (n < N) {
+#pragma unroll 8
+        for (int64_t i = phase; i < blocks; i += 16) s += part[i * N + n];
+    }
+    sums[phase][lane] = s;
     __syncthreads();
-    if (wave == 0 && n < b.N) b.dbias[n] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if (phase == 0 && n < N) {
+        float v = sums[0][lane];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += sums[i][lane];
+        dbias[n] = v;
+    }
+}
+
+// ---- few tokens -----------------------------------------------------------------------------------
+// Up to 64 tokens: the codes are the traffic (N K bytes), each read once.  A workgroup takes 16 weight rows;
+// its eight wavefronts take 64-wide blocks of K in turn, so that a wavefront's loads cover 64 contiguous
+// codes of each row, and their sums are joined through LDS.  v_mfma_f32_16x16x32_bf16 with the weights as A
+// (row lane % 16, k = 8 (lane / 16) .. + 7) and the tokens as B (column lane % 16): lane quarter q supplies
+// k = 16 q + 8 t .. + 7 of a block in instruction t, so that a lane's 16 codes are one load.  Lanes past M
+// or N repeat the last row, whose sums they do not store.
+constexpr int kSkinnyMost = 64;
+constexpr int kSkinnyWaves = 8;
+
+template <int MB>
+__global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pgq_linear_fwd f)
+{
+    __shared__ f32x4 sums[kSkinnyWaves][MB][64];
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    const int r = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n = min(n0 + r, f.N - 1);
+    const int8_t* crow = f.codes + n * f.ldc + 16 * q;
+    const uint16_t* xrow[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) xrow[i] = f.x + min((int64_t)(16 * i + r), f.M - 1) * f.ldx + 16 * q;
+    const float s = f.K > 0 ? f16_to_f32(f.scales[n]) : 0.0f;
+    const float s128 = -128.0f * s;                       // exact
+    f32x4 acc[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) acc[i] = f32x4{};
+    auto multiply = [&](u32x4 c, const u32x4 (*x)[2]) __attribute__((always_inline)) {
+        // u = code + 128: fma(u, s, -128 s) = code * s exactly (at most 7 + 11 significant bits), then bf16
+        float v[16];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t u = c[w] ^ 0x80808080u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * w + e] = __builtin_fmaf((float)((u >> (8 * e)) & 0xFFu), s, s128);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const u32x4 a = {pk_bf16(v[8 * t], v[8 * t + 1]), pk_bf16(v[8 * t + 2], v[8 * t + 3]),
+                             pk_bf16(v[8 * t + 4], v[8 * t + 5]), pk_bf16(v[8 * t + 6], v[8 * t + 7])};
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, x[i][t]), acc[i], 0, 0, 0);
+        }
+    };
+    const int64_t full = f.K / 64;
+    constexpr int U = MB <= 2 ? 4 : 2;                    // blocks whose loads are in flight together
+    int64_t kb = wave;
+    for (; kb + (int64_t)(U - 1) * kSkinnyWaves < full; kb += (int64_t)U * kSkinnyWaves) {
+        u32x4 c[U], x[U][MB][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = (kb + (int64_t)u * kSkinnyWaves) * 64;
+            c[u] = load16(crow + k);
+#pragma unroll
+            for (int i = 0; i < MB; ++i) { x[u][i][0] = load16(xrow[i] + k); x[u][i][1] = load16(xrow[i] + k + 8); }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(c[u], x[u]);
+    }
+    for (; kb < full; kb += kSkinnyWaves) {
+        const int64_t k = kb * 64;
+        u32x4 x[MB][2];
+        const u32x4 c = load16(crow + k);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) { x[i][0] = load16(xrow[i] + k); x[i][1] = load16(xrow[i] + k + 8); }
+        multiply(c, x);
+    }
+    if (f.K % 64 && kb == full) {                         // the last block, element by element past K
+        const int64_t k = full * 64;
+        const int left = (int)max((int64_t)0, min((int64_t)16, f.K - k - 16 * q));
+        union { u32x4 v; uint8_t b[16]; } c = {};
+        union { u32x4 v[2]; uint16_t h[16]; } x[MB] = {};
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (e < left) {
+                c.b[e] = (uint8_t)crow[k + e];
+#pragma unroll
+                for (int i = 0; i < MB; ++i) x[i].h[e] = xrow[i][k + e];
+            }
+        u32x4 xv[MB][2];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) { xv[i][0] = x[i].v[0]; xv[i][1] = x[i].v[1]; }
+        multiply(c.v, xv);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    // accumulator element e of lane l: weight row 4 (l / 16) + e, token l % 16
+    for (int u = (int)threadIdx.x; u < 64 * MB * 4; u += 64 * kSkinnyWaves) {
+        const int e = u & 3, l = (u >> 2) & 63, i = u >> 8;
+        const int64_t m = 16 * i + (l & 15), nn = n0 + 4 * (l >> 4) + e;
+        if (m >= f.M || nn >= f.N) continue;
+        float z = sums[0][i][l][e];
+#pragma unroll
+        for (int w = 1; w < kSkinnyWaves; ++w) z += sums[w][i][l][e];
+        if (f.bias) z += load_any(f.bias, f.bias_dtype, nn);
+        if (f.z) f.z[m * f.ldz + nn] = f32_to_bf16(z);
+        float y = act_value(f.act, f.slope, z);
+        if (f.residual) y += load_any(f.residual, f.residual_dtype, m * f.ldr + nn);
+        store_any(f.y, f.y_dtype, m * f.ldy + nn, y);
+    }
 }
 
 constexpr int64_t kMaxSize = ((int64_t)1 << 31) - 1;
@@ -205,6 +503,94 @@ pgq_status check_bwd(const pgq_linear_bwd* p)
 }
 
 int64_t tiles_of(int64_t I, int64_t J) { return ((I + kGT - 1) / kGT) * ((J + kGT - 1) / kGT); }
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Contractions and rows this long go through the 64 x 64 element-load kernel: the matrix kernels address
+// a tile's rows with 32-bit byte offsets.
+constexpr int64_t kLong = (int64_t)1 << 21;
+// bf16 rows the matrix kernels can load where they lie
+bool direct(const void* p, int64_t ld, int64_t cols)
+{
+    return cols % 8 == 0 && ld % 8 == 0 && ld < kLong && is_aligned(p, 16);
+}
+
+// How a forward call runs, and where its scratch goes.
+struct FwdPlan {
+    bool skinny, tile;           // few tokens; the element-load kernel; else the matrix kernels
+    bool copy_x;
+    size_t what, xc, bytes;
+};
+FwdPlan plan_fwd(const pgq_linear_fwd& p)
+{
+    FwdPlan q;
+    memset(&q, 0, sizeof(q));
+    q.skinny = p.M <= kSkinnyMost;
+    q.tile = !q.skinny && (p.K >= kLong || p.K == 0);
+    if (p.M == 0 || p.N == 0 || q.skinny || q.tile) return q;
+    q.copy_x = !direct(p.x, p.ldx, p.K);
+    q.bytes = up256((size_t)p.N * up8(p.K) * 2);
+    q.xc = q.bytes;
+    if (q.copy_x) q.bytes += up256((size_t)p.M * up8(p.K) * 2);
+    return q;
+}
+
+struct BwdPlan {
+    bool dx, dw, db;             // what there is to compute
+    bool tile;                   // by the element-load kernel
+    bool dz, copy_x;             // dZ and X go through scratch
+    int32_t splits;
+    int64_t chunk, blocks;       // blocks: row blocks of the db partial sums
+    size_t o_dz, o_db, o_what_t, o_x, o_part, bytes;
+};
+BwdPlan plan_bwd(const pgq_linear_bwd& p)
+{
+    BwdPlan q;
+    memset(&q, 0, sizeof(q));
+    q.dx = p.dx && p.M > 0 && p.K > 0;
+    q.dw = p.dw && p.N > 0 && p.K > 0;
+    q.db = p.dbias && p.N > 0;
+    q.tile = p.N >= kLong || p.K >= kLong;
+    auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += up256(n); return at; };
+    q.blocks = (p.M + kDzRows - 1) / kDzRows;
+    if (q.db) q.o_db = take((size_t)q.blocks * p.N * 4);
+    if (q.tile || p.N == 0 || p.M == 0) return q;
+    if (q.dx || q.dw) {
+        q.dz = p.act != PGQ_ACT_NONE || p.dy_dtype != PGQ_BF16 || !direct(p.dy, p.lddy, p.N);
+        if (q.dz) q.o_dz = take((size_t)p.M * up8(p.N) * 2);
+    }
+    if (q.dx) q.o_what_t = take((size_t)p.K * up8(p.N) * 2);
+    if (q.dw) {
+        q.copy_x = !direct(p.x, p.ldx, p.K);
+        if (q.copy_x) q.o_x = take((size_t)p.M * up8(p.K) * 2);
+        mm_tt_split(p.N, p.K, p.M, &q.splits, &q.chunk);
+        q.o_part = take(mm_tt_partial_bytes(p.N, p.K, q.splits));
+    }
+    return q;
+}
+
+// The launches of one call: the first takes a pending start event, the last the stop event.
+struct Launches {
+    void *start = nullptr, *stop = nullptr, *stream;
+    int left;
+    hipError_t e = hipSuccess;
+    Launches(int n, void* s) : stream(s), left(n) { take_timing_events(&start, &stop); }
+    bool next()
+    {
+        if (e != hipSuccess) return false;
+        set_timing_events(start, --left == 0 ? stop : nullptr);
+        start = nullptr;
+        return true;
+    }
+    void go(const void* fn, int64_t grid, int block, void** args)
+    {
+        if (!next()) return;
+        e = grid > 0x7FFFFFFF ? hipErrorInvalidValue : launch_plain(fn, dim3((unsigned)grid), dim3((unsigned)block), args, stream);
+    }
+    pgq_status done() const { return e == hipSuccess ? PGQ_OK : (pgq_status)note_hip_error(e); }
+};
+
+bool rows16(const void* p, int32_t dtype, int64_t ld) { return is_aligned(p, 16) && ld % (16 / (int64_t)float_size(dtype)) == 0; }
 
 }  // namespace
 }  // namespace pgq
@@ -217,7 +603,7 @@ pgq_status pgq_linear_forward_workspace(const pgq_linear_fwd* p, size_t* workspa
 {
     if (!workspace_bytes) return PGQ_ERR_NULL;
     const pgq_status st = check_fwd(p);
-    if (st == PGQ_OK) *workspace_bytes = 0;
+    if (st == PGQ_OK) *workspace_bytes = plan_fwd(*p).bytes;
     return st;
 }
 
@@ -225,59 +611,168 @@ pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* worksp
 {
     if (!workspace_bytes) return PGQ_ERR_NULL;
     const pgq_status st = check_bwd(p);
-    if (st == PGQ_OK) *workspace_bytes = 0;
+    if (st == PGQ_OK) *workspace_bytes = plan_bwd(*p).bytes;
     return st;
 }
 
 pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t workspace_bytes, void* stream)
 {
-    (void)workspace;
-    (void)workspace_bytes;
-    pgq_status st = check_fwd(p);
+    const pgq_status st = check_fwd(p);
     if (st != PGQ_OK || p->M == 0 || p->N == 0) return st;
-    const int64_t tiles = tiles_of(p->M, p->N);
-    if (tiles > kMaxSize) return PGQ_ERR_SHAPE;
+    const FwdPlan q = plan_fwd(*p);
+    if (q.bytes && (!workspace || workspace_bytes < q.bytes)) return PGQ_ERR_WORKSPACE;
+    if (q.bytes && !is_aligned(workspace, 256)) return PGQ_ERR_ALIGN;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     pgq_linear_fwd f = *p;
     pgq_linear_bwd b;
     memset(&b, 0, sizeof(b));
-    void* args[] = {&f, &b};
-    const hipError_t e = launch_plain(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_FWD>), dim3((unsigned)tiles),
-                                      dim3(256), args, stream);
-    return e != hipSuccess ? (pgq_status)note_hip_error(e) : PGQ_OK;
+    if (q.skinny) {
+        Launches l(1, stream);
+        void* args[] = {&f};
+        const void* k = f.M <= 16   ? reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<1>)
+                        : f.M <= 32 ? reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<2>)
+                                    : reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<4>);
+        l.go(k, (f.N + 15) / 16, 64 * kSkinnyWaves, args);
+        return l.done();
+    }
+    if (q.tile) {
+        Launches l(1, stream);
+        void* args[] = {&f, &b};
+        l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_FWD>), tiles_of(f.M, f.N), 256, args);
+        return l.done();
+    }
+    Launches l(2, stream);
+    Prep pr;
+    memset(&pr, 0, sizeof(pr));
+    pr.b.M = f.M;
+    pr.b.N = f.N;
+    pr.b.K = f.K;
+    pr.b.codes = f.codes;
+    pr.b.ldc = f.ldc;
+    pr.b.scales = f.scales;
+    pr.b.x = f.x;
+    pr.b.ldx = f.ldx;
+    pr.Kp = up8(f.K);
+    pr.what = reinterpret_cast<uint16_t*>(ws + q.what);
+    pr.n_what = (f.N * (pr.Kp / 8) + kFlat - 1) / kFlat;
+    if (q.copy_x) {
+        pr.xc = reinterpret_cast<uint16_t*>(ws + q.xc);
+        pr.n_x = (f.M * (pr.Kp / 8) + kFlat - 1) / kFlat;
+    }
+    void* args[] = {&pr};
+    l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), pr.n_what + pr.n_x, 256, args);
+    MmNt mm;
+    memset(&mm, 0, sizeof(mm));
+    mm.a = q.copy_x ? pr.xc : f.x;
+    mm.lda = q.copy_x ? pr.Kp : f.ldx;
+    mm.b = pr.what;
+    mm.ldb = pr.Kp;
+    mm.I = f.M;
+    mm.J = f.N;
+    mm.L = pr.Kp;
+    mm.e.bias = f.bias;
+    mm.e.residual = f.residual;
+    mm.e.z = f.z;
+    mm.e.y = f.y;
+    mm.e.ldr = f.ldr;
+    mm.e.ldz = f.ldz;
+    mm.e.ldy = f.ldy;
+    mm.e.bias_dtype = f.bias_dtype;
+    mm.e.residual_dtype = f.residual_dtype;
+    mm.e.y_dtype = f.y_dtype;
+    mm.e.act = f.act;
+    mm.e.slope = f.slope;
+    mm.e.vec = rows16(f.y, f.y_dtype, f.ldy) && (!f.z || rows16(f.z, PGQ_BF16, f.ldz)) &&
+               (!f.residual || rows16(f.residual, f.residual_dtype, f.ldr));
+    if (l.next()) l.e = launch_mm_nt(mm, stream);
+    return l.done();
 }
 
 pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t workspace_bytes, void* stream)
 {
-    (void)workspace;
-    (void)workspace_bytes;
-    pgq_status st = check_bwd(p);
+    const pgq_status st = check_bwd(p);
     if (st != PGQ_OK) return st;
-    pgq_linear_fwd f;
-    memset(&f, 0, sizeof(f));
+    const BwdPlan q = plan_bwd(*p);
+    if (!q.dx && !q.dw && !q.db) return PGQ_OK;
+    if (q.bytes && (!workspace || workspace_bytes < q.bytes)) return PGQ_ERR_WORKSPACE;
+    if (q.bytes && !is_aligned(workspace, 256)) return PGQ_ERR_ALIGN;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     pgq_linear_bwd b = *p;
-    void* args[] = {&f, &b};
-    const bool dx = p->dx && p->M > 0 && p->K > 0, dw = p->dw && p->N > 0 && p->K > 0, db = p->dbias && p->N > 0;
-    if ((dx && tiles_of(p->M, p->K) > kMaxSize) || (dw && tiles_of(p->N, p->K) > kMaxSize)) return PGQ_ERR_SHAPE;
-    void *ev_start = nullptr, *ev_stop = nullptr;
-    take_timing_events(&ev_start, &ev_stop);
-    int left = (dx ? 1 : 0) + (dw ? 1 : 0) + (db ? 1 : 0);
-    auto go = [&](const void* fn, int64_t grid) {
-        set_timing_events(ev_start, --left == 0 ? ev_stop : nullptr);
-        ev_start = nullptr;
-        const hipError_t e = launch_plain(fn, dim3((unsigned)grid), dim3(256), args, stream);
-        return e;
-    };
-    hipError_t e = hipSuccess;
-    void* bargs[] = {&b};
-    if (db) {
-        set_timing_events(ev_start, --left == 0 ? ev_stop : nullptr);
-        ev_start = nullptr;
-        e = launch_plain(reinterpret_cast<const void*>(&pgq_linear_dbias_kernel), dim3((unsigned)((p->N + 63) / 64)),
-                         dim3(256), bargs, stream);
+    // an empty sum (N = 0 for dX, M = 0 for dW) is written by the element-load kernel
+    const bool mm = !q.tile && b.M > 0 && b.N > 0;
+    Prep pr;
+    memset(&pr, 0, sizeof(pr));
+    pr.b = b;
+    pr.Kp = up8(b.K);
+    pr.Np = up8(b.N);
+    pr.dz = q.dz ? reinterpret_cast<uint16_t*>(ws + q.o_dz) : nullptr;
+    pr.dbias_part = q.db ? reinterpret_cast<float*>(ws + q.o_db) : nullptr;
+    if (q.dz || q.db) pr.n_dz = q.blocks * ((pr.Np + kDzCols - 1) / kDzCols);
+    if (mm && q.dx) {
+        pr.what_t = reinterpret_cast<uint16_t*>(ws + q.o_what_t);
+        pr.n_what_t = ((pr.Np + 63) / 64) * ((b.K + 63) / 64);
     }
-    if (e == hipSuccess && dx) e = go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DX>), tiles_of(p->M, p->K));
-    if (e == hipSuccess && dw) e = go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DW>), tiles_of(p->N, p->K));
-    return e != hipSuccess ? (pgq_status)note_hip_error(e) : PGQ_OK;
+    if (mm && q.copy_x) {
+        pr.xc = reinterpret_cast<uint16_t*>(ws + q.o_x);
+        pr.n_x = (b.M * (pr.Kp / 8) + kFlat - 1) / kFlat;
+    }
+    const int64_t units = pr.n_dz + pr.n_what_t + pr.n_x;
+    const bool reduce = mm && q.dw && q.splits > 1;
+    Launches l((units > 0) + q.dx + q.dw + reduce + q.db, stream);
+    void* pargs[] = {&pr};
+    if (units > 0) l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), units, 256, pargs);
+    if (q.db) {
+        const float* part = pr.dbias_part;
+        void* args[] = {&part, const_cast<int64_t*>(&q.blocks), &b.N, &b.dbias};
+        l.go(reinterpret_cast<const void*>(&pgq_linear_dbias_kernel), (b.N + 63) / 64, 1024, args);
+    }
+    if (!mm) {
+        pgq_linear_fwd f;
+        memset(&f, 0, sizeof(f));
+        void* args[] = {&f, &b};
+        if (q.dx) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DX>), tiles_of(b.M, b.K), 256, args);
+        if (q.dw) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DW>), tiles_of(b.N, b.K), 256, args);
+        return l.done();
+    }
+    const uint16_t* dz = q.dz ? pr.dz : static_cast<const uint16_t*>(b.dy);
+    const int64_t lddz = q.dz ? pr.Np : b.lddy;
+    if (q.dx) {
+        MmNt m;
+        memset(&m, 0, sizeof(m));
+        m.a = dz;
+        m.lda = lddz;
+        m.b = pr.what_t;
+        m.ldb = pr.Np;
+        m.I = b.M;
+        m.J = b.K;
+        m.L = pr.Np;
+        m.e.y = b.dx;
+        m.e.ldy = b.lddx;
+        m.e.y_dtype = b.dx_dtype;
+        m.e.vec = rows16(b.dx, b.dx_dtype, b.lddx);
+        if (l.next()) l.e = launch_mm_nt(m, stream);
+    }
+    if (q.dw) {
+        MmTt m;
+        memset(&m, 0, sizeof(m));
+        m.a = dz;
+        m.lda = lddz;
+        m.b = q.copy_x ? pr.xc : b.x;
+        m.ldb = q.copy_x ? pr.Kp : b.ldx;
+        m.I = b.N;
+        m.J = b.K;
+        m.L = b.M;
+        m.c = b.dw;
+        m.ldc = b.lddw;
+        m.c_dtype = b.dw_dtype;
+        m.splits = q.splits;
+        m.chunk = q.chunk;
+        m.mask = b.mask;
+        m.partial = reinterpret_cast<float*>(ws + q.o_part);
+        if (l.next()) l.e = launch_mm_tt(m, stream);
+        if (reduce && l.next()) l.e = launch_mm_tt_reduce(m, stream);
+    }
+    return l.done();
 }
 
 }  // extern "C"

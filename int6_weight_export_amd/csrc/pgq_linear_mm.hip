@@ -1,0 +1,499 @@
+// pgq_linear_mm.hip -- the matrix products of the linear layer on the matrix cores (gfx950).
+//
+// Operands are bf16 in memory; v_mfma_f32_32x32x16_bf16 accumulates in fp32.  Operand layout of the
+// instruction (checked on the device): lane l supplies row l % 32 of A (and column l % 32 of B) with 8
+// consecutive l, lanes 32..63 the next 8; accumulator register j of lane l is row 8 (j / 4) + 4 (l / 32) +
+// j % 4, column l % 32.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pgq_desc.h"
+#include "pgq_linear.h"
+
+namespace pgq {
+namespace {
+
+#define GLB __attribute__((address_space(1)))
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr int kTK = 64;                        // contraction per stage
+constexpr uint32_t kOOB = 0x80000000u;         // a buffer offset past every range: the load returns 0
+
+// every wave's LDS reads are complete, then the workgroup barrier (the asm keeps the compiler from
+// moving memory operations across it)
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));   // round to nearest even
+}
+
+// Workgroup -> tile.  Workgroups are dealt to the 8 XCDs round robin and each XCD has its own L2, so
+// each XCD takes a contiguous eighth of the tiles; within it tiles go down kBand tile rows before the
+// next column, so that the ~32 tiles an XCD works on at a time share kBand row panels of A and 32 / kBand
+// column panels of B.
+constexpr uint32_t kBand = 4;
+__device__ __forceinline__ void tile_of(uint32_t wid, uint32_t total, uint32_t gi, uint32_t gj, uint32_t& ti, uint32_t& tj)
+{
+    const uint32_t xcd = wid % 8u, per = total / 8u, rem = total % 8u;
+    const uint32_t t = (xcd < rem ? xcd * (per + 1u) : rem * (per + 1u) + (xcd - rem) * per) + wid / 8u;
+    const uint32_t band = t / (kBand * gj), in = t % (kBand * gj);
+    const uint32_t rows = min(kBand, gi - band * kBand);
+    ti = band * kBand + in % rows;
+    tj = in / rows;
+}
+
+// V consecutive columns of one row through the epilogue
+template <int V, typename YT>
+__device__ __forceinline__ void finish(const Epilogue& e, const float* v, int64_t row, int64_t col, int64_t J)
+{
+    float o[V];
+    if (e.vec && col + V <= J) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            o[i] = v[i];
+            if (e.bias) o[i] += e.bias_dtype == PGQ_F32 ? ((const GLB float*)e.bias)[col + i] : bf16_to_f32(((const GLB uint16_t*)e.bias)[col + i]);
+        }
+        if (e.z) {
+            GLB uint32_t* pz = (GLB uint32_t*)(e.z + row * e.ldz + col);
+            if constexpr (V == 8) {
+                __builtin_nontemporal_store(u32x4{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]), pk_bf16(o[4], o[5]), pk_bf16(o[6], o[7])}, (GLB u32x4*)pz);
+            } else {
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                __builtin_nontemporal_store(u32x2{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3])}, (GLB u32x2*)pz);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = act_value(e.act, e.slope, o[i]);
+        if (e.residual) {
+            if (e.residual_dtype == PGQ_F32) {
+                const GLB f32x4* pr = (const GLB f32x4*)((const float*)e.residual + row * e.ldr + col);
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) {
+                    const f32x4 r = pr[q];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[4 * q + i] += r[i];
+                }
+            } else {
+                const GLB uint32_t* pr = (const GLB uint32_t*)((const uint16_t*)e.residual + row * e.ldr + col);
+#pragma unroll
+                for (int q = 0; q < V / 2; ++q) {
+                    const uint32_t r = pr[q];
+                    o[2 * q] += __builtin_bit_cast(float, r << 16);
+                    o[2 * q + 1] += __builtin_bit_cast(float, r & 0xFFFF0000u);
+                }
+            }
+        }
+        if constexpr (sizeof(YT) == 4) {
+            __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]}, (GLB f32x4*)((float*)e.y + row * e.ldy + col));
+        } else {
+            __builtin_nontemporal_store(u32x4{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]), pk_bf16(o[4], o[5]), pk_bf16(o[6], o[7])},
+                                        (GLB u32x4*)((uint16_t*)e.y + row * e.ldy + col));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int64_t c = col + i;
+        if (c >= J) continue;
+        float x = v[i];
+        if (e.bias) x += e.bias_dtype == PGQ_F32 ? ((const GLB float*)e.bias)[c] : bf16_to_f32(((const GLB uint16_t*)e.bias)[c]);
+        if (e.z) ((GLB uint16_t*)e.z)[row * e.ldz + c] = f32_to_bf16(x);
+        x = act_value(e.act, e.slope, x);
+        if (e.residual)
+            x += e.residual_dtype == PGQ_F32 ? ((const GLB float*)e.residual)[row * e.ldr + c]
+                                             : bf16_to_f32(((const GLB uint16_t*)e.residual)[row * e.ldr + c]);
+        if constexpr (sizeof(YT) == 4) ((GLB float*)e.y)[row * e.ldy + c] = x;
+        else ((GLB uint16_t*)e.y)[row * e.ldy + c] = f32_to_bf16(x);
+    }
+}
+
+// ---- A rows times B rows ----------------------------------------------------------------------------
+// A workgroup of WR x WC wavefronts computes a tile of 32 IB WR x 32 JB WC, each wavefront IB x JB blocks
+// of 32 x 32.  Each 64-wide stage of both operands goes from global memory straight into LDS (buffer
+// loads with the LDS destination), double-buffered, so the next stage's loads are in flight while the
+// matrix cores work on this one; a lane past I, J or L gets zeros from the buffer range check.
+//
+// LDS slots are 16-byte granules, 8 to a row; granule g of row r sits in slot g ^ swz(r), so that the
+// rows a fragment read touches spread over distinct banks in every group of 8 and of 16 lanes.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+template <int WR, int WC, int IB, int JB, typename YT>
+__global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
+pgq_mm_nt_kernel(MmNt p)
+{
+    constexpr int T = 64 * WR * WC, TI = 32 * IB * WR, TJ = 32 * JB * WC;
+    constexpr int AI = TI * 8 / T, BI = TJ * 8 / T;          // load instructions per thread per stage
+    constexpr int AS = TI * kTK * 2, BS = TJ * kTK * 2;      // bytes per stage
+    constexpr int EP = 32 * JB + 4;                          // epilogue row pitch in floats
+    constexpr int LDS = 2 * (AS + BS) > WR * WC * 32 * EP * 4 ? 2 * (AS + BS) : WR * WC * 32 * EP * 4;
+    __shared__ __align__(16) uint8_t lds[LDS];
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ);
+    uint32_t ti, tj;
+    tile_of(blockIdx.x, gridDim.x, gi, gj, ti, tj);
+    const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
+    const int irows = (int)min((int64_t)TI, p.I - i0), jrows = (int)min((int64_t)TJ, p.J - j0);
+    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + i0 * p.lda), 0, (int)((int64_t)irows * p.lda * 2), 0x00020000);
+    const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb), 0, (int)((int64_t)jrows * p.ldb * 2), 0x00020000);
+    // load slot of instruction c: row c T / 8 + tid / 8, slot tid % 8 (its granule is the same for every c)
+    const int r0 = tid >> 3, g0 = (tid & 7) ^ swz(r0);
+    const uint32_t ao = (uint32_t)(r0 * p.lda + 8 * g0) * 2u, bo = (uint32_t)(r0 * p.ldb + 8 * g0) * 2u;
+    const uint32_t astep = (uint32_t)(T / 8 * 2 * p.lda), bstep = (uint32_t)(T / 8 * 2 * p.ldb);
+    const int nst = (int)((p.L + kTK - 1) / kTK);
+    auto issue = [&](int st) {
+        uint8_t* la = lds + (st & 1) * (AS + BS);
+        uint8_t* lb = la + AS;
+        const bool ok = (int64_t)st * kTK + 8 * g0 < p.L;
+        const uint32_t k0 = (uint32_t)st * (kTK * 2);
+        // (mask arithmetic, so that the compiler keeps one load per slot rather than branching around two)
+#pragma unroll
+        for (int c = 0; c < AI; ++c) {
+            const uint32_t bad = 0u - (uint32_t)!(ok && r0 + c * (T / 8) < irows);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr)(la + (c * T + wave * 64) * 16), 16,
+                                                     ((ao + (uint32_t)c * astep + k0) & ~bad) | (kOOB & bad), 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < BI; ++c) {
+            const uint32_t bad = 0u - (uint32_t)!(ok && r0 + c * (T / 8) < jrows);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_ptr)(lb + (c * T + wave * 64) * 16), 16,
+                                                     ((bo + (uint32_t)c * bstep + k0) & ~bad) | (kOOB & bad), 0, 0, 0);
+        }
+    };
+    const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
+    const int r32 = lane & 31, h = lane >> 5;
+    f32x16 acc[IB][JB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[i][j] = f32x16{};
+    // Fragments of one 32-wide half of a stage: lane half h supplies l = 16 h + 8 t .. + 7 in instruction t,
+    // so that its 16 l are contiguous in LDS.
+    struct Frag {
+        bf16x8 a[IB][2], b[JB][2];
+    } f0, f1;
+    auto fetch = [&](Frag& f, int st, int kb) __attribute__((always_inline)) {
+        const uint8_t* la = lds + (st & 1) * (AS + BS);
+        const uint8_t* lb = la + AS;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < IB; ++i) {
+                const int r = wi + 32 * i + r32;
+                f.a[i][t] = *reinterpret_cast<const bf16x8*>(la + (r * 8 + ((4 * kb + 2 * h + t) ^ swz(r))) * 16);
+            }
+#pragma unroll
+            for (int j = 0; j < JB; ++j) {
+                const int r = wj + 32 * j + r32;
+                f.b[j][t] = *reinterpret_cast<const bf16x8*>(lb + (r * 8 + ((4 * kb + 2 * h + t) ^ swz(r))) * 16);
+            }
+        }
+    };
+    auto multiply = [&](const Frag& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < IB; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i][t], f.b[j][t], acc[i][j], 0, 0, 0);
+    };
+    // Two sets of fragments: while the matrix cores work on one half stage, the next half is read from LDS.
+    // The barrier sits between the halves: there every wave has read all of stage st, so the loads of stage
+    // st + 2 may overwrite it, and those of st + 1, issued a stage earlier, have arrived.
+    auto turn = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    if (nst > 0) {
+        issue(0);
+        turn();
+        if (nst > 1) issue(1);
+        fetch(f0, 0, 0);
+    }
+    for (int st = 0; st < nst; ++st) {
+        fetch(f1, st, 1);
+        multiply(f0);
+        turn();
+        if (st + 2 < nst) issue(st + 2);
+        if (st + 1 < nst) fetch(f0, st + 1, 0);
+        if ((int64_t)st * kTK + 32 < p.L) multiply(f1);
+    }
+    // out through LDS, one 32-row block at a time, so that a lane holds consecutive columns
+    constexpr int V = sizeof(YT) == 4 ? 4 : 8;
+    constexpr int LPR = 32 * JB / V;                          // lanes per row
+    constexpr int PASS = 32 * LPR / 64;
+    float* tl = reinterpret_cast<float*>(lds) + wave * (32 * EP);
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) tl[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + r32] = acc[i][j][r];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+        for (int q = 0; q < PASS; ++q) {
+            const int rr = (lane + 64 * q) / LPR, cc = (lane + 64 * q) % LPR * V;
+            float v[V];
+#pragma unroll
+            for (int u = 0; u < V / 4; ++u) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(tl + rr * EP + cc + 4 * u);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[4 * u + w] = x[w];
+            }
+            const int64_t row = i0 + wi + 32 * i + rr, col = j0 + wj + cc;
+            if (row < p.I && col < p.J) finish<V, YT>(p.e, v, row, col, p.J);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+template <int WR, int WC, int IB, int JB>
+hipError_t run_nt(const MmNt& p, void* stream)
+{
+    constexpr int64_t TI = 32 * IB * WR, TJ = 32 * JB * WC;
+    const int64_t tiles = ((p.I + TI - 1) / TI) * ((p.J + TJ - 1) / TJ);
+    if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+    MmNt copy = p;
+    void* args[] = {&copy};
+    const void* k = p.e.y_dtype == PGQ_F32 ? reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, float>)
+                                           : reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, uint16_t>);
+    return launch_plain(k, dim3((unsigned)tiles), dim3(64 * WR * WC), args, stream);
+}
+
+// ---- A columns times B columns ----------------------------------------------------------------------
+// The contraction runs down the rows of both operands (dW sums over tokens).  A stage is 64 rows of TI and
+// TJ columns, loaded straight into LDS as they lie in memory; ds_read_b64_tr_b16 transposes on the way to the
+// registers: the 16 lanes of a group read four rows of 16 columns (lane i the columns 4 (i % 4) .. + 3 of row
+// i / 4) and lane i receives column i of the four rows (checked on the device).
+//
+// A group's four rows are one row pitch apart, a multiple of 128 bytes, so their 32-byte pieces would share
+// banks: granule g (16 bytes) of row r sits in slot g ^ turn(r), which moves the four rows 64 bytes apart.
+template <int COLS>
+__device__ __forceinline__ int turn(int r)
+{
+    return COLS % 128 == 0 ? 4 * (r & 3) : 4 * ((r >> 1) & 1);      // pitch 0 or 128 modulo 256 bytes
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+__device__ __forceinline__ bool mask_bit(const uint8_t* mask, int64_t J, int64_t i, int64_t j)
+{
+    return !mask || ((((const GLB uint8_t*)mask)[i * ((J + 7) / 8) + (j >> 3)] >> (j & 7)) & 1);
+}
+// rows i .. i + 3 of column j
+__device__ __forceinline__ void put4(const MmTt& p, int64_t i, int64_t j, f32x4 v)
+{
+    if (j >= p.J) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (i + e < p.I) {
+            const float x = mask_bit(p.mask, p.J, i + e, j) ? v[e] : 0.0f;
+            if (p.c_dtype == PGQ_F32) ((GLB float*)p.c)[(i + e) * p.ldc + j] = x;
+            else ((GLB uint16_t*)p.c)[(i + e) * p.ldc + j] = f32_to_bf16(x);
+        }
+}
+
+template <int WR, int WC, int IB, int JB>
+__global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
+pgq_mm_tt_kernel(MmTt p)
+{
+    constexpr int T = 64 * WR * WC, TI = 32 * IB * WR, TJ = 32 * JB * WC;
+    constexpr int AG = TI / 8, BG = TJ / 8;                  // granules per row
+    constexpr int AI = 64 * AG / T, BI = 64 * BG / T;        // load instructions per thread per stage
+    constexpr int AS = 64 * TI * 2, BS = 64 * TJ * 2;
+    static_assert(64 * AG % T == 0 && 64 * BG % T == 0, "whole load instructions");
+    __shared__ __align__(16) uint8_t lds[2 * (AS + BS)];
+    const int tid = (int)threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ), tiles = gi * gj;
+    // parts of one l range go to one XCD together: they read the same rows
+    uint32_t ti, tj;
+    const uint32_t total = gridDim.x, xcd = blockIdx.x % 8u, per = total / 8u, rem = total % 8u;
+    const uint32_t w = (xcd < rem ? xcd * (per + 1u) : rem * (per + 1u) + (xcd - rem) * per) + blockIdx.x / 8u;
+    const uint32_t part = w / tiles, tile = w % tiles;
+    {
+        const uint32_t band = tile / (kBand * gj), in = tile % (kBand * gj), rows = min(kBand, gi - band * kBand);
+        ti = band * kBand + in % rows;
+        tj = in / rows;
+    }
+    const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
+    const int64_t l0 = (int64_t)part * p.chunk;
+    const int64_t len = min(p.chunk, p.L - l0);
+    const int nst = len > 0 ? (int)((len + 63) / 64) : 0;
+    const int ig = (int)min((int64_t)AG, (p.I - i0 + 7) / 8), jg = (int)min((int64_t)BG, (p.J - j0 + 7) / 8);
+    auto issue = [&](int st) __attribute__((always_inline)) {
+        uint8_t* la = lds + (st & 1) * (AS + BS);
+        uint8_t* lb = la + AS;
+        const int64_t row = l0 + (int64_t)st * 64;
+        const int rows = (int)min((int64_t)64, l0 + len - row);
+        // ranges over this stage's rows; the last row ends with its last used granule
+        const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + row * p.lda + i0), 0, (int)((rows - 1) * p.lda * 2 + 16 * ig), 0x00020000);
+        const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + row * p.ldb + j0), 0, (int)((rows - 1) * p.ldb * 2 + 16 * jg), 0x00020000);
+#pragma unroll
+        for (int c = 0; c < AI; ++c) {
+            const int s = c * T + tid, r = s / AG, g = (s % AG) ^ turn<TI>(r);
+            const uint32_t bad = 0u - (uint32_t)!(r < rows && g < ig);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr)(la + (c * T + wave * 64) * 16), 16,
+                                                     (((uint32_t)r * (uint32_t)p.lda * 2u + 16u * g) & ~bad) | (kOOB & bad), 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < BI; ++c) {
+            const int s = c * T + tid, r = s / BG, g = (s % BG) ^ turn<TJ>(r);
+            const uint32_t bad = 0u - (uint32_t)!(r < rows && g < jg);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_ptr)(lb + (c * T + wave * 64) * 16), 16,
+                                                     (((uint32_t)r * (uint32_t)p.ldb * 2u + 16u * g) & ~bad) | (kOOB & bad), 0, 0, 0);
+        }
+    };
+    const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
+    const int h = lane >> 5, r32 = lane & 31;
+    f32x16 acc[IB][JB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[i][j] = f32x16{};
+    struct Frag {
+        bf16x8 a[IB][2], b[JB][2];
+    } f0, f1;
+    // half stage kb: lane half h supplies l = 32 kb + 16 t + 8 h .. + 7 in instruction t, four at a read
+    const int rl = 8 * h + ((lane >> 2) & 3);                          // row in the half stage, t = 0, first read
+    const int gc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);          // granule in a block's 32 columns
+    auto read8 = [&](const uint8_t* base, int pitch) __attribute__((always_inline)) -> bf16x8 {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)base);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(base + 4 * pitch));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto fetch = [&](Frag& f, int st, int kb) __attribute__((always_inline)) {
+        const uint8_t* la = lds + (st & 1) * (AS + BS) + (32 * kb + rl) * (2 * TI) + (lane & 1) * 8;
+        const uint8_t* lb = lds + (st & 1) * (AS + BS) + AS + (32 * kb + rl) * (2 * TJ) + (lane & 1) * 8;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < IB; ++i)
+                f.a[i][t] = read8(la + 16 * t * (2 * TI) + ((((wi + 32 * i) >> 3) + gc) ^ turn<TI>(rl)) * 16, 2 * TI);
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+                f.b[j][t] = read8(lb + 16 * t * (2 * TJ) + ((((wj + 32 * j) >> 3) + gc) ^ turn<TJ>(rl)) * 16, 2 * TJ);
+        }
+    };
+    auto multiply = [&](const Frag& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < IB; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i][t], f.b[j][t], acc[i][j], 0, 0, 0);
+    };
+    auto turn_over = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    if (nst > 0) {
+        issue(0);
+        turn_over();
+        if (nst > 1) issue(1);
+        fetch(f0, 0, 0);
+    }
+    for (int st = 0; st < nst; ++st) {
+        fetch(f1, st, 1);
+        multiply(f0);
+        turn_over();
+        if (st + 2 < nst) issue(st + 2);
+        if (st + 1 < nst) fetch(f0, st + 1, 0);
+        multiply(f1);
+    }
+    // one part: to C; several: the parts' sums as they lie in the registers, 16 bytes a lane
+    f32x4* out = reinterpret_cast<f32x4*>(p.partial) + (((size_t)part * tiles + tile) * (WR * WC) + wave) * (IB * JB * 4 * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                if (p.splits > 1) {
+                    if (i0 + wi + 32 * i < p.I && j0 + wj + 32 * j < p.J) out[((i * JB + j) * 4 + q) * 64] = v;
+                } else {
+                    put4(p, i0 + wi + 32 * i + 8 * q + 4 * h, j0 + wj + 32 * j + r32, v);
+                }
+            }
+}
+
+template <int WR, int WC, int IB, int JB>
+__global__ void __launch_bounds__(256) pgq_mm_tt_reduce_kernel(MmTt p)
+{
+    constexpr int TI = 32 * IB * WR, TJ = 32 * JB * WC;
+    const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ), tiles = gi * gj;
+    const uint32_t unit = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;      // one wave: 8 rows of 32 columns
+    const uint32_t tile = unit / (WR * WC * IB * JB * 4), u = unit % (WR * WC * IB * JB * 4);
+    if (tile >= tiles) return;
+    const uint32_t wave = u / (IB * JB * 4), ij = u / 4 % (IB * JB), q = u % 4;
+    const uint32_t band = tile / (kBand * gj), in = tile % (kBand * gj), rows = min(kBand, gi - band * kBand);
+    const int64_t i = (int64_t)(band * kBand + in % rows) * TI + (wave / WC) * (32 * IB) + 32 * (ij / JB);
+    const int64_t j = (int64_t)(in / rows) * TJ + (wave % WC) * (32 * JB) + 32 * (ij % JB);
+    if (i >= p.I || j >= p.J) return;
+    const GLB f32x4* src = (const GLB f32x4*)p.partial + (size_t)unit * 64 + lane;
+    const size_t step = (size_t)tiles * (WR * WC * IB * JB * 4 * 64);
+    f32x4 v = *src;
+    for (int s = 1; s < p.splits; ++s) {
+        src += step;
+        const f32x4 x = *src;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e];
+    }
+    put4(p, i + 8 * q + 4 * (lane >> 5), j + (lane & 31), v);
+}
+
+constexpr int kTtI = 256, kTtJ = 192;
+typedef hipError_t (*TtRun)(const MmTt&, void*);
+int64_t tt_tiles(int64_t I, int64_t J) { return ((I + kTtI - 1) / kTtI) * ((J + kTtJ - 1) / kTtJ); }
+
+}  // namespace
+
+hipError_t launch_mm_nt(const MmNt& p, void* stream)
+{
+    if (p.I <= 1024) return run_nt<2, 2, 1, 1>(p, stream);
+    return p.e.y_dtype == PGQ_F32 ? run_nt<2, 4, 4, 2>(p, stream) : run_nt<4, 2, 2, 4>(p, stream);
+}
+
+void mm_tt_split(int64_t I, int64_t J, int64_t L, int32_t* splits, int64_t* chunk)
+{
+    const int64_t tiles = tt_tiles(I, J), stages = (L + 63) / 64;
+    int64_t s = std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1));
+    s = std::min(s, std::max<int64_t>(1, stages / 4));
+    const int64_t per = std::max<int64_t>(1, (stages + s - 1) / s);
+    *chunk = per * 64;
+    *splits = (int32_t)std::max<int64_t>(1, (stages + per - 1) / per);
+}
+
+size_t mm_tt_partial_bytes(int64_t I, int64_t J, int32_t splits)
+{
+    return splits > 1 ? (size_t)splits * (size_t)tt_tiles(I, J) * kTtI * kTtJ * 4 : 0;
+}
+
+hipError_t launch_mm_tt(const MmTt& p, void* stream)
+{
+    const int64_t grid = tt_tiles(p.I, p.J) * p.splits;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    MmTt copy = p;
+    void* args[] = {&copy};
+    return launch_plain(reinterpret_cast<const void*>(&pgq_mm_tt_kernel<4, 2, 2, 3>), dim3((unsigned)grid), dim3(512), args, stream);
+}
+
+hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream)
+{
+    const int64_t units = tt_tiles(p.I, p.J) * (8 * 6 * 4);
+    if (units / 4 > 0x7FFFFFFF) return hipErrorInvalidValue;
+    MmTt copy = p;
+    void* args[] = {&copy};
+    return launch_plain(reinterpret_cast<const void*>(&pgq_mm_tt_reduce_kernel<4, 2, 2, 3>), dim3((unsigned)(units / 4)), dim3(256), args, stream);
+}
+
+}  // namespace pgq

@@ -51,9 +51,16 @@ struct MmNt {
     const uint16_t* a;
     const uint16_t* b;
     int64_t lda, ldb, I, J, L;
+    int32_t kind, splits;        // tile, and parts the contraction is cut into (mm_nt_plan)
+    int64_t chunk;               // l per part, a multiple of 64
+    float* partial;              // splits > 1: mm_nt_partial_bytes() of scratch
     Epilogue e;
 };
+void mm_nt_plan(MmNt& p);        // kind, splits and chunk from I, J and L
+size_t mm_nt_partial_bytes(const MmNt& p);
 hipError_t launch_mm_nt(const MmNt& p, void* stream);
+// splits > 1: the sums of the parts, in their order, through the epilogue
+hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream);
 
 // C[i][j] = sum_l A[l][i] B[l][j]: bf16 operands, 16-byte aligned rows of at least I and J elements rounded
 // up to 8, row strides below 2^23.  C goes out as dw_dtype, zero where the mask bit of (i, j) is 0.
@@ -64,13 +71,13 @@ struct MmTt {
     void* c;
     int64_t ldc;
     int32_t c_dtype;
-    int32_t splits;              // parts the sum over l is cut into (mm_tt_splits)
+    int32_t kind, splits;        // tile, and parts the sum over l is cut into (mm_tt_plan)
     int64_t chunk;               // l per part, a multiple of 64
     const uint8_t* mask;         // NULL or I x ceil(J / 8) bytes
     float* partial;              // splits > 1: mm_tt_partial_bytes() of scratch
 };
-void mm_tt_split(int64_t I, int64_t J, int64_t L, int32_t* splits, int64_t* chunk);
-size_t mm_tt_partial_bytes(int64_t I, int64_t J, int32_t splits);
+void mm_tt_plan(MmTt& p);        // kind, splits and chunk from I, J and L
+size_t mm_tt_partial_bytes(const MmTt& p);
 hipError_t launch_mm_tt(const MmTt& p, void* stream);
 // splits > 1: the sum of the parts, in their order
 hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream);

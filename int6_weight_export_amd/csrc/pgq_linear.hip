@@ -158,34 +158,61 @@ __device__ __forceinline__ void unpack2(uint32_t w, float* f)
     f[1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
 }
 
-// A thread takes 8 columns of every eighth row of the unit.  Whole granules: the loads of kHold rows are
-// issued together (rows past M repeat the last one and are not used); the ragged edge goes element by element.
+// 16 bytes holding E consecutive values of a row from column n on, with zeros past column N: past the edge the
+// row's last 16 bytes are loaded and shifted down; rows shorter than that go element by element.
+template <int E, typename T>
+__device__ __forceinline__ u32x4 load_cols(const T* row, int64_t n, int64_t N)
+{
+    if (n + E <= N) return load16(row + n);
+    u32x4 v = {};
+    if (n >= N) return v;
+    if (N >= E) {
+        const int bits = (int)(n + E - N) * (128 / E);         // 1 .. E - 1 values
+        uint64_t w[2];
+        v = load16(row + N - E);
+        __builtin_memcpy(w, &v, 16);
+        w[0] = bits < 64 ? (w[0] >> bits) | (w[1] << (64 - bits)) : w[1] >> (bits - 64);
+        w[1] = bits < 64 ? w[1] >> bits : 0;
+        __builtin_memcpy(&v, w, 16);
+        return v;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (n + e < N) {
+            const uint32_t x = E == 8 ? (uint32_t)(uint16_t)row[n + e] : (uint32_t)row[n + e];
+            if (E == 8) v[e / 2] |= x << (16 * (e % 2));
+            else v[e] = x;
+        }
+    return v;
+}
+
+// A thread takes 8 columns of every eighth row of the unit, the loads of kHold rows issued together (rows past M
+// repeat the last one and are not used).  Short loops: a small call runs this code cold, and straight-line
+// code for all eight rows cost 20 us of instruction fetch.
 template <bool F32, bool ACT>
 __device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums)
 {
-    constexpr int kHold = 4;
+    constexpr int kHold = 2;
     const pgq_linear_bwd& b = p.b;
     const int64_t cu = (p.Np + kDzCols - 1) / kDzCols;
     const int64_t rb = unit / cu, n = unit % cu * kDzCols + ((int)threadIdx.x & 31) * 8;
     const int phase = (int)threadIdx.x >> 5;
     float t[8] = {};
-    auto out = [&](int64_t m, const float* d) __attribute__((always_inline)) {
-        if (p.dz)
-            *(GLB u32x4*)(p.dz + m * p.Np + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] += d[e];
-    };
-    if (n + 8 <= b.N) {
-#pragma unroll
+    if (n < p.Np) {
+#pragma unroll 1
         for (int k0 = 0; k0 < kDzRows / 8; k0 += kHold) {
             u32x4 v[kHold][F32 ? 2 : 1], zv[kHold];
 #pragma unroll
             for (int k = 0; k < kHold; ++k) {
                 const int64_t m = min(rb * kDzRows + phase + 8 * (k0 + k), b.M - 1);
-                const uint8_t* src = (const uint8_t*)b.dy + (m * b.lddy + n) * (F32 ? 4 : 2);
-                v[k][0] = load16(src);
-                if constexpr (F32) v[k][1] = load16(src + 16);
-                if constexpr (ACT) zv[k] = load16(b.z + m * b.ldz + n);
+                if constexpr (F32) {
+                    const uint32_t* row = (const uint32_t*)b.dy + m * b.lddy;
+                    v[k][0] = load_cols<4>(row, n, b.N);
+                    v[k][1] = load_cols<4>(row, n + 4, b.N);
+                } else {
+                    v[k][0] = load_cols<8>((const uint16_t*)b.dy + m * b.lddy, n, b.N);
+                }
+                if constexpr (ACT) zv[k] = load_cols<8>(b.z + m * b.ldz, n, b.N);
             }
 #pragma unroll
             for (int k = 0; k < kHold; ++k) {
@@ -199,28 +226,28 @@ __device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums
 #pragma unroll
                     for (int e = 0; e < 4; ++e) unpack2(v[k][0][e], d + 2 * e);
                 }
-                if constexpr (ACT) {
+                if constexpr (ACT) {                          // (in the padding dY is 0 and the slope of Z = 0 finite)
                     float z[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) unpack2(zv[k][e], z + 2 * e);
+                    if (b.act == PGQ_ACT_SILU) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] *= act_slope(b.act, b.slope, z[e]);
+                        for (int e = 0; e < 8; ++e) d[e] *= act_slope(PGQ_ACT_SILU, 0.0f, z[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float g = act_slope(PGQ_ACT_RELU, b.slope, z[e]);
+                            d[e] *= b.act == PGQ_ACT_RELU ? g : 2.0f * z[e] * g * g;
+                        }
+                    }
                 }
-                if (m < b.M) out(m, d);
-            }
-        }
-    } else if (n < p.Np) {
-#pragma unroll 1
-        for (int k = 0; k < kDzRows / 8; ++k) {
-            const int64_t m = rb * kDzRows + phase + 8 * k;
-            if (m >= b.M) break;
-            float d[8];
+                if (m < b.M) {
+                    if (p.dz)
+                        *(GLB u32x4*)(p.dz + m * p.Np + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                d[e] = n + e < b.N ? load_any(b.dy, b.dy_dtype, m * b.lddy + n + e) : 0.0f;
-                if (ACT && n + e < b.N) d[e] *= act_slope(b.act, b.slope, bf16_to_f32(b.z[m * b.ldz + n + e]));
+                    for (int e = 0; e < 8; ++e) t[e] += d[e];
+                }
             }
-            out(m, d);
         }
     }
     if (!p.dbias_part) return;
@@ -254,7 +281,7 @@ __device__ __forceinline__ void prep_what_t(const Prep& p, int64_t unit, uint16_
                 __builtin_memcpy(q, &v, 16);
             } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) q[e] = k + e < b.K ? b.codes[n * b.ldc + k + e] : (int8_t)0;
+                for (int e = 0; e < 16; ++e) q[e] = b.codes[n * b.ldc + min(k + e, b.K - 1)];      // columns past K are not stored
             }
         }
 #pragma unroll
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
     if (!what) unit -= p.n_what;
     const pgq_linear_bwd& b = p.b;
     const int64_t g = p.Kp / 8, rows = what ? b.N : b.M;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         const int64_t i = unit * kFlat + c * 256 + threadIdx.x;
         if (i >= rows * g) return;
@@ -301,21 +328,17 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
                 __builtin_memcpy(q, &v, 8);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) q[e] = k + e < b.K ? src[e] : (int8_t)0;
+                for (int e = 0; e < 8; ++e) {
+                    const int8_t v = src[min((int64_t)e, b.K - 1 - k)];
+                    q[e] = k + e < b.K ? v : (int8_t)0;
+                }
             }
+            // padding is 0 whatever the scale is
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = k + 2 * e < b.K ? pk_bf16((float)q[2 * e] * s, k + 2 * e + 1 < b.K ? (float)q[2 * e + 1] * s : 0.0f) : 0u;
+            for (int e = 0; e < 4; ++e) o[e] = pk_bf16(k + 2 * e < b.K ? (float)q[2 * e] * s : 0.0f, k + 2 * e + 1 < b.K ? (float)q[2 * e + 1] * s : 0.0f);
             *(GLB u32x4*)(p.what + r * p.Kp + k) = o;
         } else {
-            const uint16_t* src = b.x + r * b.ldx + k;
-            if (k + 8 <= b.K) {
-                o = load16(src);
-            } else {
-                uint16_t q[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) q[e] = k + e < b.K ? src[e] : (uint16_t)0;
-                __builtin_memcpy(&o, q, 16);
-            }
+            o = load_cols<8>(b.x + r * b.ldx, k, b.K);
             *(GLB u32x4*)(p.xc + r * p.Kp + k) = o;
         }
     }
@@ -388,7 +411,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
         }
     };
     const int64_t full = f.K / 64;
-    constexpr int U = MB <= 2 ? 4 : 2;                    // blocks whose loads are in flight together
+    constexpr int U = MB == 1 ? 8 : MB == 2 ? 4 : 2;      // blocks whose loads are in flight together
     int64_t kb = wave;
     for (; kb + (int64_t)(U - 1) * kSkinnyWaves < full; kb += (int64_t)U * kSkinnyWaves) {
         u32x4 c[U], x[U][MB][2];
@@ -399,6 +422,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
 #pragma unroll
             for (int i = 0; i < MB; ++i) { x[u][i][0] = load16(xrow[i] + k); x[u][i][1] = load16(xrow[i] + k + 8); }
         }
+        __builtin_amdgcn_sched_barrier(0);                // every load is issued before the first use
 #pragma unroll
         for (int u = 0; u < U; ++u) multiply(c[u], x[u]);
     }
@@ -519,7 +543,8 @@ bool direct(const void* p, int64_t ld, int64_t cols)
 struct FwdPlan {
     bool skinny, tile;           // few tokens; the element-load kernel; else the matrix kernels
     bool copy_x;
-    size_t what, xc, bytes;
+    MmNt nt;                     // sizes, tile and parts
+    size_t what, xc, part, bytes;
 };
 FwdPlan plan_fwd(const pgq_linear_fwd& p)
 {
@@ -532,6 +557,12 @@ FwdPlan plan_fwd(const pgq_linear_fwd& p)
     q.bytes = up256((size_t)p.N * up8(p.K) * 2);
     q.xc = q.bytes;
     if (q.copy_x) q.bytes += up256((size_t)p.M * up8(p.K) * 2);
+    q.nt.I = p.M;
+    q.nt.J = p.N;
+    q.nt.L = up8(p.K);
+    mm_nt_plan(q.nt);
+    q.part = q.bytes;
+    q.bytes += up256(mm_nt_partial_bytes(q.nt));
     return q;
 }
 
@@ -539,9 +570,10 @@ struct BwdPlan {
     bool dx, dw, db;             // what there is to compute
     bool tile;                   // by the element-load kernel
     bool dz, copy_x;             // dZ and X go through scratch
-    int32_t splits;
-    int64_t chunk, blocks;       // blocks: row blocks of the db partial sums
-    size_t o_dz, o_db, o_what_t, o_x, o_part, bytes;
+    MmNt nt;                     // dX, dW: sizes, tiles and parts
+    MmTt tt;
+    int64_t blocks;              // row blocks of the db partial sums
+    size_t o_dz, o_db, o_what_t, o_x, o_part, o_part_dx, bytes;
 };
 BwdPlan plan_bwd(const pgq_linear_bwd& p)
 {
@@ -559,12 +591,22 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
         q.dz = p.act != PGQ_ACT_NONE || p.dy_dtype != PGQ_BF16 || !direct(p.dy, p.lddy, p.N);
         if (q.dz) q.o_dz = take((size_t)p.M * up8(p.N) * 2);
     }
-    if (q.dx) q.o_what_t = take((size_t)p.K * up8(p.N) * 2);
+    if (q.dx) {
+        q.o_what_t = take((size_t)p.K * up8(p.N) * 2);
+        q.nt.I = p.M;
+        q.nt.J = p.K;
+        q.nt.L = up8(p.N);
+        mm_nt_plan(q.nt);
+        q.o_part_dx = take(mm_nt_partial_bytes(q.nt));
+    }
     if (q.dw) {
         q.copy_x = !direct(p.x, p.ldx, p.K);
         if (q.copy_x) q.o_x = take((size_t)p.M * up8(p.K) * 2);
-        mm_tt_split(p.N, p.K, p.M, &q.splits, &q.chunk);
-        q.o_part = take(mm_tt_partial_bytes(p.N, p.K, q.splits));
+        q.tt.I = p.N;
+        q.tt.J = p.K;
+        q.tt.L = p.M;
+        mm_tt_plan(q.tt);
+        q.o_part = take(mm_tt_partial_bytes(q.tt));
     }
     return q;
 }
@@ -641,7 +683,8 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
         l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_FWD>), tiles_of(f.M, f.N), 256, args);
         return l.done();
     }
-    Launches l(2, stream);
+    const bool reduce = q.nt.splits > 1;
+    Launches l(2 + reduce, stream);
     Prep pr;
     memset(&pr, 0, sizeof(pr));
     pr.b.M = f.M;
@@ -661,15 +704,12 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     }
     void* args[] = {&pr};
     l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), pr.n_what + pr.n_x, 256, args);
-    MmNt mm;
-    memset(&mm, 0, sizeof(mm));
+    MmNt mm = q.nt;
     mm.a = q.copy_x ? pr.xc : f.x;
     mm.lda = q.copy_x ? pr.Kp : f.ldx;
     mm.b = pr.what;
     mm.ldb = pr.Kp;
-    mm.I = f.M;
-    mm.J = f.N;
-    mm.L = pr.Kp;
+    mm.partial = reinterpret_cast<float*>(ws + q.part);
     mm.e.bias = f.bias;
     mm.e.residual = f.residual;
     mm.e.z = f.z;
@@ -685,6 +725,7 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     mm.e.vec = rows16(f.y, f.y_dtype, f.ldy) && (!f.z || rows16(f.z, PGQ_BF16, f.ldz)) &&
                (!f.residual || rows16(f.residual, f.residual_dtype, f.ldr));
     if (l.next()) l.e = launch_mm_nt(mm, stream);
+    if (reduce && l.next()) l.e = launch_mm_nt_reduce(mm, stream);
     return l.done();
 }
 
@@ -717,8 +758,8 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
         pr.n_x = (b.M * (pr.Kp / 8) + kFlat - 1) / kFlat;
     }
     const int64_t units = pr.n_dz + pr.n_what_t + pr.n_x;
-    const bool reduce = mm && q.dw && q.splits > 1;
-    Launches l((units > 0) + q.dx + q.dw + reduce + q.db, stream);
+    const bool reduce = mm && q.dw && q.tt.splits > 1, reduce_dx = mm && q.dx && q.nt.splits > 1;
+    Launches l((units > 0) + q.dx + reduce_dx + q.dw + reduce + q.db, stream);
     void* pargs[] = {&pr};
     if (units > 0) l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), units, 256, pargs);
     if (q.db) {
@@ -737,36 +778,28 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     const uint16_t* dz = q.dz ? pr.dz : static_cast<const uint16_t*>(b.dy);
     const int64_t lddz = q.dz ? pr.Np : b.lddy;
     if (q.dx) {
-        MmNt m;
-        memset(&m, 0, sizeof(m));
+        MmNt m = q.nt;
         m.a = dz;
         m.lda = lddz;
         m.b = pr.what_t;
         m.ldb = pr.Np;
-        m.I = b.M;
-        m.J = b.K;
-        m.L = pr.Np;
+        m.partial = reinterpret_cast<float*>(ws + q.o_part_dx);
         m.e.y = b.dx;
         m.e.ldy = b.lddx;
         m.e.y_dtype = b.dx_dtype;
         m.e.vec = rows16(b.dx, b.dx_dtype, b.lddx);
         if (l.next()) l.e = launch_mm_nt(m, stream);
+        if (reduce_dx && l.next()) l.e = launch_mm_nt_reduce(m, stream);
     }
     if (q.dw) {
-        MmTt m;
-        memset(&m, 0, sizeof(m));
+        MmTt m = q.tt;
         m.a = dz;
         m.lda = lddz;
         m.b = q.copy_x ? pr.xc : b.x;
         m.ldb = q.copy_x ? pr.Kp : b.ldx;
-        m.I = b.N;
-        m.J = b.K;
-        m.L = b.M;
         m.c = b.dw;
         m.ldc = b.lddw;
         m.c_dtype = b.dw_dtype;
-        m.splits = q.splits;
-        m.chunk = q.chunk;
         m.mask = b.mask;
         m.partial = reinterpret_cast<float*>(ws + q.o_part);
         if (l.next()) l.e = launch_mm_tt(m, stream);

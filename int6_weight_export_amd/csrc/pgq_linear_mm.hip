@@ -42,80 +42,150 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b)
 // next column, so that the ~32 tiles an XCD works on at a time share kBand row panels of A and 32 / kBand
 // column panels of B.
 constexpr uint32_t kBand = 4;
-__device__ __forceinline__ void tile_of(uint32_t wid, uint32_t total, uint32_t gi, uint32_t gj, uint32_t& ti, uint32_t& tj)
+__device__ __forceinline__ void tile_at(uint32_t tile, uint32_t gi, uint32_t gj, uint32_t& ti, uint32_t& tj)
 {
-    const uint32_t xcd = wid % 8u, per = total / 8u, rem = total % 8u;
-    const uint32_t t = (xcd < rem ? xcd * (per + 1u) : rem * (per + 1u) + (xcd - rem) * per) + wid / 8u;
-    const uint32_t band = t / (kBand * gj), in = t % (kBand * gj);
+    const uint32_t band = tile / (kBand * gj), in = tile % (kBand * gj);
     const uint32_t rows = min(kBand, gi - band * kBand);
     ti = band * kBand + in % rows;
     tj = in / rows;
 }
-
-// V consecutive columns of one row through the epilogue
-template <int V, typename YT>
-__device__ __forceinline__ void finish(const Epilogue& e, const float* v, int64_t row, int64_t col, int64_t J)
+__device__ __forceinline__ void tile_of(uint32_t wid, uint32_t total, uint32_t gi, uint32_t gj, uint32_t& ti, uint32_t& tj, uint32_t& part)
 {
-    float o[V];
-    if (e.vec && col + V <= J) {
+    const uint32_t xcd = wid % 8u, per = total / 8u, rem = total % 8u;
+    const uint32_t t = (xcd < rem ? xcd * (per + 1u) : rem * (per + 1u) + (xcd - rem) * per) + wid / 8u;
+    part = t / (gi * gj);
+    tile_at(t % (gi * gj), gi, gj, ti, tj);
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// V values as bf16, one store
+template <int V>
+__device__ __forceinline__ void store_bf16(uint16_t* p, const float* o)
+{
+    if constexpr (V == 8)
+        *(GLB u32x4*)p = u32x4{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]), pk_bf16(o[4], o[5]), pk_bf16(o[6], o[7])};
+    else
+        *(GLB u32x2*)p = u32x2{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3])};
+}
+
+// The epilogue of one lane, which holds V consecutive columns of several rows.  The columns are the same
+// for every row, so the bias is loaded once; the residuals of G rows are loaded together.
+template <int V, typename YT>
+struct Out {
+    const Epilogue& e;
+    int64_t col, J;
+    bool vec;
+    float bias[V];
+    __device__ __forceinline__ Out(const Epilogue& e_, int64_t col_, int64_t J_) : e(e_), col(col_), J(J_)
+    {
+        vec = e.vec && col + V <= J;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            o[i] = v[i];
-            if (e.bias) o[i] += e.bias_dtype == PGQ_F32 ? ((const GLB float*)e.bias)[col + i] : bf16_to_f32(((const GLB uint16_t*)e.bias)[col + i]);
+            bias[i] = 0.0f;
+            if (e.bias && col + i < J)
+                bias[i] = e.bias_dtype == PGQ_F32 ? ((const GLB float*)e.bias)[col + i] : bf16_to_f32(((const GLB uint16_t*)e.bias)[col + i]);
         }
-        if (e.z) {
-            GLB uint32_t* pz = (GLB uint32_t*)(e.z + row * e.ldz + col);
-            if constexpr (V == 8) {
-                __builtin_nontemporal_store(u32x4{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]), pk_bf16(o[4], o[5]), pk_bf16(o[6], o[7])}, (GLB u32x4*)pz);
-            } else {
-                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                __builtin_nontemporal_store(u32x2{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3])}, (GLB u32x2*)pz);
-            }
-        }
+    }
+    // G rows, `step` apart, of which those below I are stored; v: their sums
+    template <int G>
+    __device__ __forceinline__ void rows(int64_t row, int step, int64_t I, float (*v)[V]) const
+    {
+        if (!vec) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = act_value(e.act, e.slope, o[i]);
+            for (int g = 0; g < G; ++g)
+                if (row + g * step < I) edge(row + g * step, v[g]);
+            return;
+        }
+        float r[G][V];
         if (e.residual) {
-            if (e.residual_dtype == PGQ_F32) {
-                const GLB f32x4* pr = (const GLB f32x4*)((const float*)e.residual + row * e.ldr + col);
 #pragma unroll
-                for (int q = 0; q < V / 4; ++q) {
-                    const f32x4 r = pr[q];
+            for (int g = 0; g < G; ++g) {
+                const int64_t at = min(row + g * step, I - 1) * e.ldr + col;
+                if (e.residual_dtype == PGQ_F32) {
+                    const GLB f32x4* pr = (const GLB f32x4*)((const float*)e.residual + at);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[4 * q + i] += r[i];
-                }
-            } else {
-                const GLB uint32_t* pr = (const GLB uint32_t*)((const uint16_t*)e.residual + row * e.ldr + col);
+                    for (int q = 0; q < V / 4; ++q) {
+                        const f32x4 x = pr[q];
 #pragma unroll
-                for (int q = 0; q < V / 2; ++q) {
-                    const uint32_t r = pr[q];
-                    o[2 * q] += __builtin_bit_cast(float, r << 16);
-                    o[2 * q + 1] += __builtin_bit_cast(float, r & 0xFFFF0000u);
+                        for (int i = 0; i < 4; ++i) r[g][4 * q + i] = x[i];
+                    }
+                } else {
+                    uint32_t x[V / 2];
+                    if constexpr (V == 8) {
+                        const u32x4 y = *(const GLB u32x4*)((const uint16_t*)e.residual + at);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = y[i];
+                    } else {
+                        const u32x2 y = *(const GLB u32x2*)((const uint16_t*)e.residual + at);
+                        x[0] = y[0];
+                        x[1] = y[1];
+                    }
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        r[g][2 * i] = __builtin_bit_cast(float, x[i] << 16);
+                        r[g][2 * i + 1] = __builtin_bit_cast(float, x[i] & 0xFFFF0000u);
+                    }
                 }
             }
         }
-        if constexpr (sizeof(YT) == 4) {
-            __builtin_nontemporal_store(f32x4{o[0], o[1], o[2], o[3]}, (GLB f32x4*)((float*)e.y + row * e.ldy + col));
-        } else {
-            __builtin_nontemporal_store(u32x4{pk_bf16(o[0], o[1]), pk_bf16(o[2], o[3]), pk_bf16(o[4], o[5]), pk_bf16(o[6], o[7])},
-                                        (GLB u32x4*)((uint16_t*)e.y + row * e.ldy + col));
-        }
-        return;
-    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int64_t c = col + i;
-        if (c >= J) continue;
-        float x = v[i];
-        if (e.bias) x += e.bias_dtype == PGQ_F32 ? ((const GLB float*)e.bias)[c] : bf16_to_f32(((const GLB uint16_t*)e.bias)[c]);
-        if (e.z) ((GLB uint16_t*)e.z)[row * e.ldz + c] = f32_to_bf16(x);
-        x = act_value(e.act, e.slope, x);
-        if (e.residual)
-            x += e.residual_dtype == PGQ_F32 ? ((const GLB float*)e.residual)[row * e.ldr + c]
-                                             : bf16_to_f32(((const GLB uint16_t*)e.residual)[row * e.ldr + c]);
-        if constexpr (sizeof(YT) == 4) ((GLB float*)e.y)[row * e.ldy + c] = x;
-        else ((GLB uint16_t*)e.y)[row * e.ldy + c] = f32_to_bf16(x);
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[g][i] += bias[i];
+        if (e.z) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (row + g * step < I) store_bf16<V>(e.z + (row + g * step) * e.ldz + col, v[g]);
+        }
+        if (e.act == PGQ_ACT_SILU) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[g][i] = act_value(PGQ_ACT_SILU, 0.0f, v[g][i]);
+        } else if (e.act != PGQ_ACT_NONE) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float x = act_value(PGQ_ACT_RELU, e.slope, v[g][i]);
+                    v[g][i] = e.act == PGQ_ACT_RELU ? x : x * x;
+                }
+        }
+        if (e.residual) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[g][i] += r[g][i];
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            if (row + g * step < I) {
+                const int64_t at = (row + g * step) * e.ldy + col;
+                if constexpr (sizeof(YT) == 4)
+                    *(GLB f32x4*)((float*)e.y + at) = f32x4{v[g][0], v[g][1], v[g][2], v[g][3]};
+                else
+                    store_bf16<V>((uint16_t*)e.y + at, v[g]);
+            }
     }
-}
+    // a row element by element: the last columns, and rows without 16-byte alignment
+    __device__ __forceinline__ void edge(int64_t row, const float* v) const
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int64_t c = col + i;
+            if (c >= J) continue;
+            float x = v[i] + bias[i];
+            if (e.z) ((GLB uint16_t*)e.z)[row * e.ldz + c] = f32_to_bf16(x);
+            x = act_value(e.act, e.slope, x);
+            if (e.residual)
+                x += e.residual_dtype == PGQ_F32 ? ((const GLB float*)e.residual)[row * e.ldr + c]
+                                                 : bf16_to_f32(((const GLB uint16_t*)e.residual)[row * e.ldr + c]);
+            if constexpr (sizeof(YT) == 4) ((GLB float*)e.y)[row * e.ldy + c] = x;
+            else ((GLB uint16_t*)e.y)[row * e.ldy + c] = f32_to_bf16(x);
+        }
+    }
+};
 
 // ---- A rows times B rows ----------------------------------------------------------------------------
 // A workgroup of WR x WC wavefronts computes a tile of 32 IB WR x 32 JB WC, each wavefront IB x JB blocks
@@ -140,21 +210,22 @@ pgq_mm_nt_kernel(MmNt p)
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ);
-    uint32_t ti, tj;
-    tile_of(blockIdx.x, gridDim.x, gi, gj, ti, tj);
+    uint32_t ti, tj, part;
+    tile_of(blockIdx.x, gridDim.x, gi, gj, ti, tj, part);
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
+    const int64_t l0 = (int64_t)part * p.chunk, len = min(p.chunk, p.L - l0);      // this part of the contraction
     const int irows = (int)min((int64_t)TI, p.I - i0), jrows = (int)min((int64_t)TJ, p.J - j0);
-    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + i0 * p.lda), 0, (int)((int64_t)irows * p.lda * 2), 0x00020000);
-    const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb), 0, (int)((int64_t)jrows * p.ldb * 2), 0x00020000);
+    const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + i0 * p.lda + l0), 0, (int)(((int64_t)(irows - 1) * p.lda + len) * 2), 0x00020000);
+    const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb + l0), 0, (int)(((int64_t)(jrows - 1) * p.ldb + len) * 2), 0x00020000);
     // load slot of instruction c: row c T / 8 + tid / 8, slot tid % 8 (its granule is the same for every c)
     const int r0 = tid >> 3, g0 = (tid & 7) ^ swz(r0);
     const uint32_t ao = (uint32_t)(r0 * p.lda + 8 * g0) * 2u, bo = (uint32_t)(r0 * p.ldb + 8 * g0) * 2u;
     const uint32_t astep = (uint32_t)(T / 8 * 2 * p.lda), bstep = (uint32_t)(T / 8 * 2 * p.ldb);
-    const int nst = (int)((p.L + kTK - 1) / kTK);
+    const int nst = (int)((len + kTK - 1) / kTK);
     auto issue = [&](int st) {
         uint8_t* la = lds + (st & 1) * (AS + BS);
         uint8_t* lb = la + AS;
-        const bool ok = (int64_t)st * kTK + 8 * g0 < p.L;
+        const bool ok = (int64_t)st * kTK + 8 * g0 < len;
         const uint32_t k0 = (uint32_t)st * (kTK * 2);
         // (mask arithmetic, so that the compiler keeps one load per slot rather than branching around two)
 #pragma unroll
@@ -224,13 +295,28 @@ pgq_mm_nt_kernel(MmNt p)
         turn();
         if (st + 2 < nst) issue(st + 2);
         if (st + 1 < nst) fetch(f0, st + 1, 0);
-        if ((int64_t)st * kTK + 32 < p.L) multiply(f1);
+        if ((int64_t)st * kTK + 32 < len) multiply(f1);
+    }
+    if (p.splits > 1) {                                       // the part's sums as they lie in the registers
+        f32x4* part_out = reinterpret_cast<f32x4*>(p.partial) +
+                          (((size_t)part * (gi * gj) + ti * gj + tj) * (WR * WC) + wave) * (IB * JB * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < IB; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    part_out[((i * JB + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        return;
     }
     // out through LDS, one 32-row block at a time, so that a lane holds consecutive columns
     constexpr int V = sizeof(YT) == 4 ? 4 : 8;
     constexpr int LPR = 32 * JB / V;                          // lanes per row
-    constexpr int PASS = 32 * LPR / 64;
+    constexpr int STEP = 64 / LPR;                            // rows a wavefront covers at once
+    constexpr int G = sizeof(YT) == 4 && STEP <= 8 ? 4 : 2;   // and a lane takes G of those at a time (more spill)
+    static_assert(32 % (STEP * G) == 0, "whole groups");
     float* tl = reinterpret_cast<float*>(lds) + wave * (32 * EP);
+    const Out<V, YT> out(p.e, j0 + wj + lane % LPR * V, p.J);
     lds_barrier();
 #pragma unroll
     for (int i = 0; i < IB; ++i) {
@@ -240,34 +326,84 @@ pgq_mm_nt_kernel(MmNt p)
             for (int r = 0; r < 16; ++r) tl[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + r32] = acc[i][j][r];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
-        for (int q = 0; q < PASS; ++q) {
-            const int rr = (lane + 64 * q) / LPR, cc = (lane + 64 * q) % LPR * V;
-            float v[V];
+        for (int q = 0; q < 32; q += STEP * G) {
+            const int rr = q + lane / LPR;
+            float v[G][V];
 #pragma unroll
-            for (int u = 0; u < V / 4; ++u) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(tl + rr * EP + cc + 4 * u);
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) v[4 * u + w] = x[w];
-            }
-            const int64_t row = i0 + wi + 32 * i + rr, col = j0 + wj + cc;
-            if (row < p.I && col < p.J) finish<V, YT>(p.e, v, row, col, p.J);
+                for (int u = 0; u < V / 4; ++u) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(tl + (rr + g * STEP) * EP + lane % LPR * V + 4 * u);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) v[g][4 * u + w] = x[w];
+                }
+            const int64_t row = i0 + wi + 32 * i + rr;
+            if (row < p.I && out.col < p.J) out.template rows<G>(row, STEP, p.I, v);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
+// the sums of the parts, in their order, through the epilogue: one wavefront takes 8 rows of 32 columns
 template <int WR, int WC, int IB, int JB>
-hipError_t run_nt(const MmNt& p, void* stream)
+__global__ void __launch_bounds__(256) pgq_mm_nt_reduce_kernel(MmNt p)
 {
-    constexpr int64_t TI = 32 * IB * WR, TJ = 32 * JB * WC;
-    const int64_t tiles = ((p.I + TI - 1) / TI) * ((p.J + TJ - 1) / TJ);
-    if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-    MmNt copy = p;
-    void* args[] = {&copy};
-    const void* k = p.e.y_dtype == PGQ_F32 ? reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, float>)
-                                           : reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, uint16_t>);
-    return launch_plain(k, dim3((unsigned)tiles), dim3(64 * WR * WC), args, stream);
+    constexpr int TI = 32 * IB * WR, TJ = 32 * JB * WC;
+    const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ), tiles = gi * gj;
+    const uint32_t unit = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint32_t tile = unit / (WR * WC * IB * JB * 4), u = unit % (WR * WC * IB * JB * 4);
+    if (tile >= tiles) return;
+    const uint32_t wave = u / (IB * JB * 4), ij = u / 4 % (IB * JB), q = u % 4;
+    const int64_t i = (int64_t)(tile / gj) * TI + (wave / WC) * (32 * IB) + 32 * (ij / JB) + 8 * q + 4 * (lane >> 5);
+    const int64_t j = (int64_t)(tile % gj) * TJ + (wave % WC) * (32 * JB) + 32 * (ij % JB) + (lane & 31);
+    if (i >= p.I || j >= p.J) return;
+    const GLB f32x4* src = (const GLB f32x4*)p.partial + (size_t)unit * 64 + lane;
+    const size_t step = (size_t)tiles * (WR * WC * IB * JB * 4 * 64);
+    f32x4 v = *src;
+    for (int s = 1; s < p.splits; ++s) {
+        src += step;
+        const f32x4 x = *src;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e];
+    }
+    const Epilogue& e = p.e;
+    const float bias = !e.bias ? 0.0f : e.bias_dtype == PGQ_F32 ? ((const GLB float*)e.bias)[j] : bf16_to_f32(((const GLB uint16_t*)e.bias)[j]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t row = i + k;
+        if (row >= p.I) break;
+        float x = v[k] + bias;
+        if (e.z) ((GLB uint16_t*)e.z)[row * e.ldz + j] = f32_to_bf16(x);
+        x = act_value(e.act, e.slope, x);
+        if (e.residual)
+            x += e.residual_dtype == PGQ_F32 ? ((const GLB float*)e.residual)[row * e.ldr + j]
+                                             : bf16_to_f32(((const GLB uint16_t*)e.residual)[row * e.ldr + j]);
+        if (e.y_dtype == PGQ_F32) ((GLB float*)e.y)[row * e.ldy + j] = x;
+        else ((GLB uint16_t*)e.y)[row * e.ldy + j] = f32_to_bf16(x);
+    }
 }
+
+// The tiles a product can be cut into.  stage: microseconds of one 64-wide stage of a workgroup that has its
+// compute unit alone; busy: per workgroup when several share it; per_cu: how many fit.  Measured at
+// 1024 x 1024 x 1024 and 8192 x 4096 x 4096.
+struct NtKind {
+    int ti, tj, threads, per_cu;
+    double stage, busy;
+    const void *f32, *bf16, *reduce;
+};
+template <int WR, int WC, int IB, int JB>
+NtKind nt_kind(int per_cu, double stage, double busy)
+{
+    return {32 * IB * WR, 32 * JB * WC, 64 * WR * WC, per_cu, stage, busy,
+            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, float>),
+            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, uint16_t>),
+            reinterpret_cast<const void*>(&pgq_mm_nt_reduce_kernel<WR, WC, IB, JB>)};
+}
+// (two 256 x 256 forms: wavefronts of 64 x 128 write longer row pieces, those of 128 x 64 are 3% faster in long
+// contractions; the choice between them is by L)
+const NtKind kNt[] = {nt_kind<4, 2, 2, 4>(1, 1.75, 1.70), nt_kind<2, 4, 4, 2>(1, 1.75, 1.66), nt_kind<2, 2, 2, 2>(2, 0.85, 0.55),
+                      nt_kind<2, 2, 2, 1>(3, 0.55, 0.31), nt_kind<2, 2, 1, 1>(5, 0.33, 0.19)};
+int64_t nt_tiles(const NtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 // ---- A columns times B columns ----------------------------------------------------------------------
 // The contraction runs down the rows of both operands (dW sums over tokens).  A stage is 64 rows of TI and
@@ -316,16 +452,9 @@ pgq_mm_tt_kernel(MmTt p)
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ), tiles = gi * gj;
-    // parts of one l range go to one XCD together: they read the same rows
-    uint32_t ti, tj;
-    const uint32_t total = gridDim.x, xcd = blockIdx.x % 8u, per = total / 8u, rem = total % 8u;
-    const uint32_t w = (xcd < rem ? xcd * (per + 1u) : rem * (per + 1u) + (xcd - rem) * per) + blockIdx.x / 8u;
-    const uint32_t part = w / tiles, tile = w % tiles;
-    {
-        const uint32_t band = tile / (kBand * gj), in = tile % (kBand * gj), rows = min(kBand, gi - band * kBand);
-        ti = band * kBand + in % rows;
-        tj = in / rows;
-    }
+    uint32_t ti, tj, part;       // the tiles of one part read the same rows: they share an XCD
+    tile_of(blockIdx.x, gridDim.x, gi, gj, ti, tj, part);
+    const uint32_t tile = ti * gj + tj;
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
     const int64_t l0 = (int64_t)part * p.chunk;
     const int64_t len = min(p.chunk, p.L - l0);
@@ -435,9 +564,8 @@ __global__ void __launch_bounds__(256) pgq_mm_tt_reduce_kernel(MmTt p)
     const uint32_t tile = unit / (WR * WC * IB * JB * 4), u = unit % (WR * WC * IB * JB * 4);
     if (tile >= tiles) return;
     const uint32_t wave = u / (IB * JB * 4), ij = u / 4 % (IB * JB), q = u % 4;
-    const uint32_t band = tile / (kBand * gj), in = tile % (kBand * gj), rows = min(kBand, gi - band * kBand);
-    const int64_t i = (int64_t)(band * kBand + in % rows) * TI + (wave / WC) * (32 * IB) + 32 * (ij / JB);
-    const int64_t j = (int64_t)(in / rows) * TJ + (wave % WC) * (32 * JB) + 32 * (ij % JB);
+    const int64_t i = (int64_t)(tile / gj) * TI + (wave / WC) * (32 * IB) + 32 * (ij / JB);
+    const int64_t j = (int64_t)(tile % gj) * TJ + (wave % WC) * (32 * JB) + 32 * (ij % JB);
     if (i >= p.I || j >= p.J) return;
     const GLB f32x4* src = (const GLB f32x4*)p.partial + (size_t)unit * 64 + lane;
     const size_t step = (size_t)tiles * (WR * WC * IB * JB * 4 * 64);
@@ -451,49 +579,133 @@ __global__ void __launch_bounds__(256) pgq_mm_tt_reduce_kernel(MmTt p)
     put4(p, i + 8 * q + 4 * (lane >> 5), j + (lane & 31), v);
 }
 
-constexpr int kTtI = 256, kTtJ = 192;
-typedef hipError_t (*TtRun)(const MmTt&, void*);
-int64_t tt_tiles(int64_t I, int64_t J) { return ((I + kTtI - 1) / kTtI) * ((J + kTtJ - 1) / kTtJ); }
+// The tiles a product can be cut into.  stage: microseconds of one 64-row stage with every slot busy (what the
+// choice below weighs; measured at 4096 x 4096 x 8192 and 1584 x 528 x 16384).
+struct TtKind {
+    int ti, tj, threads, slots;                   // slots: workgroups that run at once
+    double stage;
+    const void *kernel, *reduce;
+};
+template <int WR, int WC, int IB, int JB>
+TtKind tt_kind(int slots, double stage)
+{
+    return {32 * IB * WR, 32 * JB * WC, 64 * WR * WC, slots, stage,
+            reinterpret_cast<const void*>(&pgq_mm_tt_kernel<WR, WC, IB, JB>),
+            reinterpret_cast<const void*>(&pgq_mm_tt_reduce_kernel<WR, WC, IB, JB>)};
+}
+const TtKind kTt[] = {tt_kind<4, 2, 2, 4>(256, 1.9), tt_kind<4, 2, 2, 3>(256, 1.5), tt_kind<2, 2, 2, 2>(512, 1.1)};
+int64_t tt_tiles(const TtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 }  // namespace
 
+// The tile and the number of parts with the least estimated time: for each round of workgroups the stages of a
+// part, a start, and the tile's way out at a compute unit's share of the memory rate (20 KB a microsecond);
+// parts add the trip of their sums through memory and a launch.
+void mm_nt_plan(MmNt& p)
+{
+    double best = 0;
+    const int64_t stages = std::max<int64_t>(1, (p.L + 63) / 64);
+    for (int k = 0; k < (int)(sizeof(kNt) / sizeof(kNt[0])); ++k) {
+        const NtKind& kind = kNt[k];
+        const int64_t tiles = nt_tiles(kind, p.I, p.J);
+        const double out = 3.0 + (double)kind.ti * kind.tj * 4.0 / 20e3;
+        for (int64_t s = 1; s <= 16; s *= 2) {
+            const int64_t per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
+            if (s > 1 && (parts != s || per < 4 || tiles * parts > 512)) break;
+            const int64_t wgs = tiles * parts, slots = 256 * kind.per_cu;
+            double t = (double)(wgs / slots) * ((double)per * kind.busy * kind.per_cu + out * kind.per_cu);
+            if (const int64_t left = wgs % slots) {
+                const int64_t share = (left + 255) / 256;
+                t += (double)per * std::max(kind.stage, kind.busy * (double)share) + out * (double)share;
+            }
+            if (parts > 1) t += 4.0 + (double)wgs * kind.ti * kind.tj * 8.0 / 5e6;
+            if (best == 0 || t < best) {
+                best = t;
+                p.kind = k;
+                p.splits = (int32_t)parts;
+                p.chunk = per * 64;
+            }
+        }
+    }
+}
+
+size_t mm_nt_partial_bytes(const MmNt& p)
+{
+    const NtKind& k = kNt[p.kind];
+    return p.splits > 1 ? (size_t)p.splits * (size_t)nt_tiles(k, p.I, p.J) * k.ti * k.tj * 4 : 0;
+}
+
 hipError_t launch_mm_nt(const MmNt& p, void* stream)
 {
-    if (p.I <= 1024) return run_nt<2, 2, 1, 1>(p, stream);
-    return p.e.y_dtype == PGQ_F32 ? run_nt<2, 4, 4, 2>(p, stream) : run_nt<4, 2, 2, 4>(p, stream);
+    const NtKind& k = kNt[p.kind];
+    const int64_t grid = nt_tiles(k, p.I, p.J) * p.splits;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    MmNt copy = p;
+    void* args[] = {&copy};
+    return launch_plain(p.e.y_dtype == PGQ_F32 ? k.f32 : k.bf16, dim3((unsigned)grid), dim3((unsigned)k.threads), args, stream);
 }
 
-void mm_tt_split(int64_t I, int64_t J, int64_t L, int32_t* splits, int64_t* chunk)
+hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream)
 {
-    const int64_t tiles = tt_tiles(I, J), stages = (L + 63) / 64;
-    int64_t s = std::max<int64_t>(1, 256 / std::max<int64_t>(tiles, 1));
-    s = std::min(s, std::max<int64_t>(1, stages / 4));
-    const int64_t per = std::max<int64_t>(1, (stages + s - 1) / s);
-    *chunk = per * 64;
-    *splits = (int32_t)std::max<int64_t>(1, (stages + per - 1) / per);
+    const NtKind& k = kNt[p.kind];
+    const int64_t grid = nt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4;
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    MmNt copy = p;
+    void* args[] = {&copy};
+    return launch_plain(k.reduce, dim3((unsigned)grid), dim3(256), args, stream);
 }
 
-size_t mm_tt_partial_bytes(int64_t I, int64_t J, int32_t splits)
+// The tile and the number of parts with the least estimated time: stages of a part times the rounds its
+// workgroups take, plus the trip of the parts' sums through memory (5 MB a microsecond, twice) and a launch.
+void mm_tt_plan(MmTt& p)
 {
-    return splits > 1 ? (size_t)splits * (size_t)tt_tiles(I, J) * kTtI * kTtJ * 4 : 0;
+    double best = 0;
+    const int64_t stages = std::max<int64_t>(1, (p.L + 63) / 64);
+    for (int k = 0; k < (int)(sizeof(kTt) / sizeof(kTt[0])); ++k) {
+        const TtKind& kind = kTt[k];
+        const int64_t tiles = tt_tiles(kind, p.I, p.J);
+        int64_t last = 0;
+        for (int64_t s = 1; s <= std::min<int64_t>(stages, 64); ++s) {
+            const int64_t per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
+            if (parts == last || (parts > 1 && tiles * parts > 4 * kind.slots)) continue;
+            last = parts;
+            const int64_t rounds = (tiles * parts + kind.slots - 1) / kind.slots;
+            double t = (double)rounds * ((double)per * kind.stage + 4.0);
+            if (parts > 1) t += 3.0 + (double)(tiles * parts) * kind.ti * kind.tj * 8.0 / 5e6;
+            if (best == 0 || t < best) {
+                best = t;
+                p.kind = k;
+                p.splits = (int32_t)parts;
+                p.chunk = per * 64;
+            }
+        }
+    }
+}
+
+size_t mm_tt_partial_bytes(const MmTt& p)
+{
+    const TtKind& k = kTt[p.kind];
+    return p.splits > 1 ? (size_t)p.splits * (size_t)tt_tiles(k, p.I, p.J) * k.ti * k.tj * 4 : 0;
 }
 
 hipError_t launch_mm_tt(const MmTt& p, void* stream)
 {
-    const int64_t grid = tt_tiles(p.I, p.J) * p.splits;
+    const TtKind& k = kTt[p.kind];
+    const int64_t grid = tt_tiles(k, p.I, p.J) * p.splits;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmTt copy = p;
     void* args[] = {&copy};
-    return launch_plain(reinterpret_cast<const void*>(&pgq_mm_tt_kernel<4, 2, 2, 3>), dim3((unsigned)grid), dim3(512), args, stream);
+    return launch_plain(k.kernel, dim3((unsigned)grid), dim3((unsigned)k.threads), args, stream);
 }
 
 hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream)
 {
-    const int64_t units = tt_tiles(p.I, p.J) * (8 * 6 * 4);
-    if (units / 4 > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const TtKind& k = kTt[p.kind];
+    const int64_t grid = tt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4;      // a wavefront: 8 rows of 32 columns
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmTt copy = p;
     void* args[] = {&copy};
-    return launch_plain(reinterpret_cast<const void*>(&pgq_mm_tt_reduce_kernel<4, 2, 2, 3>), dim3((unsigned)(units / 4)), dim3(256), args, stream);
+    return launch_plain(k.reduce, dim3((unsigned)grid), dim3(256), args, stream);
 }
 
 }  // namespace pgq

@@ -7,6 +7,7 @@ int16 tensors (reinterpret with .view(torch.float16) / .view(torch.bfloat16)).
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence, Tuple
 
@@ -194,6 +195,11 @@ class Exporter:
             self.dq_ptrs = (ctypes.c_void_p * n)(*[d.data_ptr() for d in self.dq])
         self.status = new_status(dev)
         self._uploaded = False
+        self._index = _gpu_of("weight", self.weights[0])
+        self._numel = [w.numel() for w in self.weights]
+        self._ptrs = (ctypes.c_void_p * n)()
+        self._g_dtypes = [torch.float32] * n
+        self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
     def run(self, reuse_table: bool = True):
         flags = pgq.PGQ_TABLE_RESIDENT if (reuse_table and self._uploaded) else 0
@@ -387,43 +393,69 @@ def qgemm(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out: Optio
 ACTS = {"none": pgq.PGQ_ACT_NONE, "relu": pgq.PGQ_ACT_RELU, "relu2": pgq.PGQ_ACT_RELU2, "silu": pgq.PGQ_ACT_SILU}
 
 
-def _check_matrix(name: str, t: torch.Tensor, shape: Tuple[int, int], dtypes, device) -> int:
+# One call per layer and token: the wrappers below keep their own cost to a few microseconds -- plain
+# comparisons, the descriptor packed in one go, scratch only when the call asks for it.
+_FWD = struct.Struct("15q4ifi")         # pgq_linear_fwd
+_BWD = struct.Struct("18q4ifi")        # pgq_linear_bwd
+_B16 = (torch.bfloat16,)
+_B16_F32 = (torch.bfloat16, torch.float32)
+_I8 = (torch.int8,)
+_U8 = (torch.uint8,)
+_SCALE_TYPES = (torch.float16, torch.int16)
+
+
+def _matrix(name: str, t: torch.Tensor, rows: int, cols: int, dtypes, index: int) -> int:
     """The row stride of a matrix argument whose rows are contiguous."""
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {(rows, cols)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected GPU {index}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)} < {cols})")
-    return t.stride(0) if rows > 1 else cols
+    if rows <= 1:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (row stride {ld} < {cols})")
+    return ld
 
 
-def _check_vector(name: str, t: torch.Tensor, n: int, dtypes, device) -> None:
+def _vector(name: str, t: torch.Tensor, n: int, dtypes, index: int) -> int:
+    """The address of an argument of n contiguous values."""
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous values expected")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected GPU {index}")
+    return t.data_ptr()
 
 
-def _launch_linear(fn, size_fn, name: str, p, device) -> None:
-    """One call of a linear-layer entry point on the device of its operands: the scratch comes from
-    torch's allocator (ordered with the current stream, private to a graph under capture)."""
-    need = ctypes.c_size_t(0)
-    pgq.check(size_fn(ctypes.byref(p), ctypes.byref(need)), name)
-    with torch.cuda.device(device):
-        ws = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
-        pgq.check(fn(ctypes.byref(p), _p(ws), need.value, _stream()), name)
+def _gpu_of(name: str, t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} is on {t.device}, not on a GPU")
+    return index
 
 
-_B16_F32 = (torch.bfloat16, torch.float32)
-_SCALE_TYPES = (torch.int16, torch.float16)
+def _launch_linear(fn, size_fn, name: str, desc: bytes, index: int) -> None:
+    """One call of a linear-layer entry point on GPU `index`: the scratch, when the call asks for any,
+    comes from torch's allocator (ordered with the current stream, private to a graph under capture)."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch_linear(fn, size_fn, name, desc, index)
+    stream = _stream()
+    rc = fn(desc, None, 0, stream)
+    if rc == pgq.PGQ_ERR_WORKSPACE:
+        need = ctypes.c_size_t(0)
+        pgq.check(size_fn(desc, ctypes.byref(need)), name)
+        ws = torch.empty(need.value, dtype=torch.uint8, device=torch.device("cuda", index))
+        rc = fn(desc, ws.data_ptr(), need.value, stream)
+    if rc != pgq.PGQ_OK:
+        pgq.check(rc, name)
 
 
 def qlinear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -434,30 +466,32 @@ def qlinear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias: Op
     x: bf16 [M, K]; codes: int8 [N, K]; scales: fp16 [N] (or int16 bit patterns); bias: fp32 or bf16
     [N]; residual: fp32 or bf16 [M, N], which may be `out` itself; act: "none", "relu", "relu2" (both
     with a leaky slope) or "silu".  Returns Y [M, N] in out_dtype (bf16 or fp32), or (Y, Z) with the
-    bf16 pre-activation Z that qlinear_backward takes when want_z."""
+    bf16 pre-activation Z that qlinear_backward takes when want_z.  No gradient is recorded: call
+    qlinear_backward."""
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x and codes must be matrices")
-    (M, K), N, dev = x.shape, codes.shape[0], x.device
-    p = pgq.pgq_linear_fwd(M=M, N=N, K=K, act=ACTS[act], slope=slope)
-    p.ldx = _check_matrix("x", x, (M, K), (torch.bfloat16,), dev)
-    p.ldc = _check_matrix("codes", codes, (N, K), (torch.int8,), dev)
-    _check_vector("scales", scales, N, _SCALE_TYPES, dev)
-    p.x, p.codes, p.scales = x.data_ptr(), codes.data_ptr(), scales.data_ptr()
+    (M, K), N, dev = x.shape, codes.shape[0], _gpu_of("x", x)
+    ldx, ldc = _matrix("x", x, M, K, _B16, dev), _matrix("codes", codes, N, K, _I8, dev)
+    pb = bt = pr = ldr = rt = pz = 0
     if bias is not None:
-        _check_vector("bias", bias, N, _B16_F32, dev)
-        p.bias, p.bias_dtype = bias.data_ptr(), _dtype_code(bias.dtype)
+        pb, bt = _vector("bias", bias, N, _B16_F32, dev), _dtype_code(bias.dtype)
     if residual is not None:
-        p.ldr = _check_matrix("residual", residual, (M, N), _B16_F32, dev)
-        p.residual, p.residual_dtype = residual.data_ptr(), _dtype_code(residual.dtype)
+        ldr = _matrix("residual", residual, M, N, _B16_F32, dev)
+        pr, rt = residual.data_ptr(), _dtype_code(residual.dtype)
+    if out_dtype not in _B16_F32:
+        raise TypeError(f"unsupported out_dtype {out_dtype}")
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=dev)
-    p.ldy = _check_matrix("out", out, (M, N), (out_dtype,), dev)
-    p.y, p.y_dtype = out.data_ptr(), _dtype_code(out_dtype)
+        out = torch.empty(M, N, dtype=out_dtype, device=x.device)
+        ldy = N
+    else:
+        ldy = _matrix("out", out, M, N, (out_dtype,), dev)
     z = None
     if want_z:
-        z = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        p.z, p.ldz = z.data_ptr(), N
-    _launch_linear(pgq.pgq_linear_forward, pgq.pgq_linear_forward_workspace, "pgq_linear_forward", p, dev)
+        z = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        pz = z.data_ptr()
+    desc = _FWD.pack(M, N, K, x.data_ptr(), ldx, codes.data_ptr(), ldc, _vector("scales", scales, N, _SCALE_TYPES, dev),
+                     pb, pr, ldr, pz, N, out.data_ptr(), ldy, bt, rt, _dtype_code(out_dtype), ACTS[act], slope, 0)
+    _launch_linear(pgq._lib.pgq_linear_forward, pgq._lib.pgq_linear_forward_workspace, "pgq_linear_forward", desc, dev)
     return (out, z) if want_z else out
 
 
@@ -473,41 +507,43 @@ def qlinear_backward(dy: torch.Tensor, codes: Optional[torch.Tensor], scales: Op
     bf16 [M, K] (for dw); codes, scales: as in qlinear (for dx); mask: uint8 [N, ceil(K / 8)]."""
     if dy.dim() != 2:
         raise ValueError("dy must be a matrix")
-    (M, N), dev = dy.shape, dy.device
+    (M, N), dev = dy.shape, _gpu_of("dy", dy)
     if want_dx and (codes is None or scales is None):
         raise ValueError("dx needs codes and scales")
     if want_dw and x is None:
         raise ValueError("dw needs x")
     if act != "none" and z is None:
         raise ValueError(f"act {act!r} needs z")
+    for t in (codes, x):
+        if t is not None and t.dim() != 2:
+            raise ValueError("codes and x must be matrices")
+    if dx_dtype not in _B16_F32 or dw_dtype not in _B16_F32:
+        raise TypeError(f"unsupported gradient types {dx_dtype}, {dw_dtype}")
     K = codes.shape[1] if codes is not None else x.shape[1] if x is not None else 0
-    p = pgq.pgq_linear_bwd(M=M, N=N, K=K, act=ACTS[act], slope=slope)
-    p.lddy = _check_matrix("dy", dy, (M, N), _B16_F32, dev)
-    p.dy, p.dy_dtype = dy.data_ptr(), _dtype_code(dy.dtype)
+    lddy = _matrix("dy", dy, M, N, _B16_F32, dev)
+    pz = ldz = px = ldx = pc = ldc = ps = pm = pdx = pdw = pdb = 0
     if act != "none":
-        p.ldz = _check_matrix("z", z, (M, N), (torch.bfloat16,), dev)
-        p.z = z.data_ptr()
+        pz, ldz = z.data_ptr(), _matrix("z", z, M, N, _B16, dev)
     res = {}
     if want_dx:
-        p.ldc = _check_matrix("codes", codes, (N, K), (torch.int8,), dev)
-        _check_vector("scales", scales, N, _SCALE_TYPES, dev)
-        res["dx"] = torch.empty(M, K, dtype=dx_dtype, device=dev)
-        p.codes, p.scales = codes.data_ptr(), scales.data_ptr()
-        p.dx, p.lddx, p.dx_dtype = res["dx"].data_ptr(), K, _dtype_code(dx_dtype)
+        pc, ldc = codes.data_ptr(), _matrix("codes", codes, N, K, _I8, dev)
+        ps = _vector("scales", scales, N, _SCALE_TYPES, dev)
+        res["dx"] = torch.empty(M, K, dtype=dx_dtype, device=dy.device)
+        pdx = res["dx"].data_ptr()
     if want_dw:
-        p.ldx = _check_matrix("x", x, (M, K), (torch.bfloat16,), dev)
-        res["dw"] = torch.empty(N, K, dtype=dw_dtype, device=dev)
-        p.x = x.data_ptr()
-        p.dw, p.lddw, p.dw_dtype = res["dw"].data_ptr(), K, _dtype_code(dw_dtype)
+        px, ldx = x.data_ptr(), _matrix("x", x, M, K, _B16, dev)
+        res["dw"] = torch.empty(N, K, dtype=dw_dtype, device=dy.device)
+        pdw = res["dw"].data_ptr()
         if mask is not None:
             if tuple(mask.shape) != (N, (K + 7) // 8):
                 raise ValueError(f"mask: shape {tuple(mask.shape)}, expected {(N, (K + 7) // 8)}")
-            _check_vector("mask", mask, mask.numel(), (torch.uint8,), dev)
-            p.mask = mask.data_ptr()
+            pm = _vector("mask", mask, mask.numel(), _U8, dev)
     if want_dbias:
-        res["dbias"] = torch.empty(N, dtype=torch.float32, device=dev)
-        p.dbias = res["dbias"].data_ptr()
-    _launch_linear(pgq.pgq_linear_backward, pgq.pgq_linear_backward_workspace, "pgq_linear_backward", p, dev)
+        res["dbias"] = torch.empty(N, dtype=torch.float32, device=dy.device)
+        pdb = res["dbias"].data_ptr()
+    desc = _BWD.pack(M, N, K, dy.data_ptr(), lddy, pz, ldz, px, ldx, pc, ldc, ps, pm, pdx, K, pdw, K, pdb,
+                     _dtype_code(dy.dtype), _dtype_code(dx_dtype), _dtype_code(dw_dtype), ACTS[act], slope, 0)
+    _launch_linear(pgq._lib.pgq_linear_backward, pgq._lib.pgq_linear_backward_workspace, "pgq_linear_backward", desc, dev)
     return res
 
 
@@ -575,6 +611,11 @@ class AdamW:
         self.status = new_status(self.device)
         self.hyper = torch.zeros(10, dtype=torch.int32, device=self.device)
         self._uploaded = False
+        self._index = _gpu_of("weight", self.weights[0])
+        self._numel = [w.numel() for w in self.weights]
+        self._ptrs = (ctypes.c_void_p * n)()
+        self._g_dtypes = [torch.float32] * n
+        self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
     def _zero_state(self, k: int):
         if self.state_bits == 32:
@@ -601,25 +642,39 @@ class AdamW:
         this step here."""
         if len(grads) != self.n:
             raise ValueError(f"{len(grads)} gradients for {self.n} weights")
-        ptrs = (ctypes.c_void_p * self.n)()
-        for i, (g, w) in enumerate(zip(grads, self.weights)):
-            if g.numel() != w.numel() or not g.is_contiguous():
-                raise ValueError(f"gradient {i}: {w.numel()} dense values expected")
-            if g.device != self.device:
-                raise ValueError(f"gradient {i} is on {g.device}, expected {self.device}")
+        ptrs, numel, types, index = self._ptrs, self._numel, self._g_dtypes, self._index
+        for i, g in enumerate(grads):
+            if g.numel() != numel[i] or not g.is_contiguous():
+                raise ValueError(f"gradient {i}: {numel[i]} dense values expected")
+            if g.get_device() != index:
+                raise ValueError(f"gradient {i} is on {g.device}, expected GPU {index}")
             ptrs[i] = g.data_ptr()
-            self._arr[i].g_dtype = _dtype_code(g.dtype)
+            if g.dtype is not types[i]:
+                self._arr[i].g_dtype = _dtype_code(g.dtype)
+                types[i] = g.dtype
         if not device_hyper:
             self.step_count += 1
-        h = None if device_hyper else ctypes.byref(self._hyper(lr, grad_scale))
-        with torch.cuda.device(self.device):
-            rc = pgq.pgq_adamw_step(self._arr, self.n, self.state_bits, ptrs, h, _p(self.hyper) if device_hyper else None,
-                                    _p(self.workspace), self.workspace.numel(), self._table_flags(), _p(self.status),
-                                    _stream())
-        if rc != pgq.PGQ_OK and not device_hyper:
-            self.step_count -= 1
-        pgq.check(rc, "pgq_adamw_step")
+        try:
+            h = None if device_hyper else self._hyper(lr, grad_scale)
+            self._on_device(self._enqueue_step, h, ptrs)
+        except pgq.PgqError:
+            if not device_hyper:
+                self.step_count -= 1
+            raise
         self._uploaded = True
+
+    def _enqueue_step(self, h, ptrs) -> None:
+        rc = pgq._lib.pgq_adamw_step(self._arr, self.n, self.state_bits, ptrs, h, None if h is not None else _p(self.hyper),
+                                     self._ws_ptr, self._ws_bytes, self._table_flags(), self._status_ptr, _stream())
+        if rc != pgq.PGQ_OK:
+            pgq.check(rc, "pgq_adamw_step")
+
+    def _on_device(self, call, *args):
+        """call(*args) with this optimizer's GPU current."""
+        if self._index == torch.cuda.current_device():
+            return call(*args)
+        with torch.cuda.device(self._index):
+            return call(*args)
 
     def _table_flags(self) -> int:
         return pgq.PGQ_TABLE_RESIDENT if self._uploaded else 0
@@ -640,9 +695,10 @@ class AdamW:
                 _dense("output", t, w.numel(), (torch.bfloat16,))
             outs.append(given)
         ptrs = [(ctypes.c_void_p * self.n)(*[t.data_ptr() for t in o]) for o in outs]
-        with torch.cuda.device(self.device):
-            rc = pgq.pgq_adamw_decode(self._arr, self.n, ptrs[0], ptrs[1], _p(self.workspace), self.workspace.numel(),
-                                      self._table_flags(), _p(self.status), _stream())
-        pgq.check(rc, "pgq_adamw_decode")
+        self._on_device(self._enqueue_decode, ptrs[0], ptrs[1])
         self._uploaded = True
         return outs[0], outs[1]
+
+    def _enqueue_decode(self, m_ptrs, r_ptrs) -> None:
+        pgq.check(pgq.pgq_adamw_decode(self._arr, self.n, m_ptrs, r_ptrs, self._ws_ptr, self._ws_bytes, self._table_flags(),
+                                       self._status_ptr, _stream()), "pgq_adamw_decode")

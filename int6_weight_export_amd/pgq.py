@@ -140,10 +140,11 @@ SIGNATURES = {
     "pgq_qgemm_bf16_ybf16": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
     "pgq_dequant_model": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(pgq_tensor_plan), _P,
                                  ctypes.POINTER(_P), _P, _SZ, _U32, _P, _P]),
-    "pgq_linear_forward_workspace": (_I32, [ctypes.POINTER(pgq_linear_fwd), ctypes.POINTER(_SZ)]),
-    "pgq_linear_backward_workspace": (_I32, [ctypes.POINTER(pgq_linear_bwd), ctypes.POINTER(_SZ)]),
-    "pgq_linear_forward": (_I32, [ctypes.POINTER(pgq_linear_fwd), _P, _SZ, _P]),
-    "pgq_linear_backward": (_I32, [ctypes.POINTER(pgq_linear_bwd), _P, _SZ, _P]),
+    # (descriptors by address: byref(struct), or bytes of the same layout)
+    "pgq_linear_forward_workspace": (_I32, [_P, ctypes.POINTER(_SZ)]),
+    "pgq_linear_backward_workspace": (_I32, [_P, ctypes.POINTER(_SZ)]),
+    "pgq_linear_forward": (_I32, [_P, _P, _SZ, _P]),
+    "pgq_linear_backward": (_I32, [_P, _P, _SZ, _P]),
     "pgq_average_workspace": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_SZ)]),
     "pgq_ema_update": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_P), ctypes.c_float, _I32, _P,
                               _SZ, _U32, _P, _P]),

@@ -45,18 +45,23 @@ struct Epilogue {
     int32_t vec;                 // rows of y, z and residual take 16-byte accesses of 8 (bf16) or 4 (fp32) columns
 };
 
-// Y[i][j] = epilogue(sum_l A[i][l] B[j][l]): bf16 operands, 16-byte aligned rows, L a multiple of 8 and
-// row strides below 2^21 elements.
+// Y[i][j] = epilogue(sum_l A[i][l] B[j][l]): 16-byte aligned rows, row strides below 2^21 elements.  B in bf16 and
+// L a multiple of 8, or B as int8 codes with a scale per row (bf16(code * s)) and L a multiple of 16.
 struct MmNt {
     const uint16_t* a;
     const uint16_t* b;
+    const int8_t* codes;         // in place of b where from_codes
+    const uint16_t* scales;
     int64_t lda, ldb, I, J, L;
     int32_t kind, splits;        // tile, and parts the contraction is cut into (mm_nt_plan)
+    int32_t from_codes;
     int64_t chunk;               // l per part, a multiple of 64
     float* partial;              // splits > 1: mm_nt_partial_bytes() of scratch
     Epilogue e;
 };
-void mm_nt_plan(MmNt& p);        // kind, splits and chunk from I, J and L
+// kind, splits, chunk, from_codes from I, J, L, whether codes will do and the bytes in and out for each element
+// of Y; returns the estimated microseconds
+double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes);
 size_t mm_nt_partial_bytes(const MmNt& p);
 hipError_t launch_mm_nt(const MmNt& p, void* stream);
 // splits > 1: the sums of the parts, in their order, through the epilogue

@@ -317,7 +317,14 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
     for (int c = 0; c < 4; ++c) {
         const int64_t i = unit * kFlat + c * 256 + threadIdx.x;
         if (i >= rows * g) return;
-        const int64_t r = i / g, k = i % g * 8;
+        int64_t r, k;
+        if (rows * g <= 0xFFFFFFFFll) {                       // (a 64-bit division costs as much as the rest)
+            r = (uint32_t)i / (uint32_t)g;
+            k = ((uint32_t)i - (uint32_t)r * (uint32_t)g) * 8;
+        } else {
+            r = i / g;
+            k = i % g * 8;
+        }
         u32x4 o;
         if (what) {
             const float s = f16_to_f32(b.scales[r]);
@@ -550,17 +557,30 @@ FwdPlan plan_fwd(const pgq_linear_fwd& p)
 {
     FwdPlan q;
     memset(&q, 0, sizeof(q));
-    q.skinny = p.M <= kSkinnyMost;
+    if (p.M == 0 || p.N == 0) return q;
+    q.skinny = p.M <= 16 || (p.M <= kSkinnyMost && (p.K >= kLong || p.K == 0));
     q.tile = !q.skinny && (p.K >= kLong || p.K == 0);
-    if (p.M == 0 || p.N == 0 || q.skinny || q.tile) return q;
+    if (q.skinny || q.tile) return q;
     q.copy_x = !direct(p.x, p.ldx, p.K);
-    q.bytes = up256((size_t)p.N * up8(p.K) * 2);
-    q.xc = q.bytes;
-    if (q.copy_x) q.bytes += up256((size_t)p.M * up8(p.K) * 2);
     q.nt.I = p.M;
     q.nt.J = p.N;
     q.nt.L = up8(p.K);
-    mm_nt_plan(q.nt);
+    double mm = mm_nt_plan(q.nt, p.K % 16 == 0 && p.ldc % 16 == 0 && p.ldc < kLong && is_aligned(p.codes, 16),
+                           (double)float_size(p.y_dtype) + (p.z ? 2.0 : 0.0) + (p.residual ? (double)float_size(p.residual_dtype) : 0.0));
+    if (p.M <= kSkinnyMost) {
+        // 17 to 64 tokens: the few-token kernel reads all of X again for every 16 weight rows (about 8 MB a
+        // microsecond; at 64 x 4096 x 4096 19.7 us against 13.6 for the tiles, at 64 x 1584 x 528 5.9 against 8.4)
+        const double x = (double)((p.M + 15) / 16 * 16) * (double)p.K * 2.0 * (double)((p.N + 15) / 16);
+        if (q.copy_x || !q.nt.from_codes) mm += 5.0;
+        if (4.0 + x / 8e6 <= mm) {
+            q.skinny = true;
+            q.copy_x = false;
+            return q;
+        }
+    }
+    if (!q.nt.from_codes) q.bytes = up256((size_t)p.N * up8(p.K) * 2);
+    q.xc = q.bytes;
+    if (q.copy_x) q.bytes += up256((size_t)p.M * up8(p.K) * 2);
     q.part = q.bytes;
     q.bytes += up256(mm_nt_partial_bytes(q.nt));
     return q;
@@ -596,7 +616,7 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
         q.nt.I = p.M;
         q.nt.J = p.K;
         q.nt.L = up8(p.N);
-        mm_nt_plan(q.nt);
+        mm_nt_plan(q.nt, false, (double)float_size(p.dx_dtype));
         q.o_part_dx = take(mm_nt_partial_bytes(q.nt));
     }
     if (q.dw) {
@@ -684,7 +704,8 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
         return l.done();
     }
     const bool reduce = q.nt.splits > 1;
-    Launches l(2 + reduce, stream);
+    const bool prep = !q.nt.from_codes || q.copy_x;
+    Launches l(1 + prep + reduce, stream);
     Prep pr;
     memset(&pr, 0, sizeof(pr));
     pr.b.M = f.M;
@@ -696,19 +717,23 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     pr.b.x = f.x;
     pr.b.ldx = f.ldx;
     pr.Kp = up8(f.K);
-    pr.what = reinterpret_cast<uint16_t*>(ws + q.what);
-    pr.n_what = (f.N * (pr.Kp / 8) + kFlat - 1) / kFlat;
+    if (!q.nt.from_codes) {
+        pr.what = reinterpret_cast<uint16_t*>(ws + q.what);
+        pr.n_what = (f.N * (pr.Kp / 8) + kFlat - 1) / kFlat;
+    }
     if (q.copy_x) {
         pr.xc = reinterpret_cast<uint16_t*>(ws + q.xc);
         pr.n_x = (f.M * (pr.Kp / 8) + kFlat - 1) / kFlat;
     }
     void* args[] = {&pr};
-    l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), pr.n_what + pr.n_x, 256, args);
+    if (prep) l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), pr.n_what + pr.n_x, 256, args);
     MmNt mm = q.nt;
     mm.a = q.copy_x ? pr.xc : f.x;
     mm.lda = q.copy_x ? pr.Kp : f.ldx;
     mm.b = pr.what;
-    mm.ldb = pr.Kp;
+    mm.codes = f.codes;
+    mm.scales = f.scales;
+    mm.ldb = q.nt.from_codes ? f.ldc : pr.Kp;
     mm.partial = reinterpret_cast<float*>(ws + q.part);
     mm.e.bias = f.bias;
     mm.e.residual = f.residual;

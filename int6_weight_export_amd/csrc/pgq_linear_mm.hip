@@ -30,6 +30,8 @@ constexpr uint32_t kOOB = 0x80000000u;         // a buffer offset past every ran
 
 // every wave's LDS reads are complete, then the workgroup barrier (the asm keeps the compiler from
 // moving memory operations across it)
+template <int N>        // all but the N youngest loads of this wave have arrived, its LDS reads are complete; then the barrier
+__device__ __forceinline__ void wait_barrier() { asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b)
@@ -197,15 +199,41 @@ struct Out {
 // rows a fragment read touches spread over distinct banks in every group of 8 and of 16 lanes.
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
-template <int WR, int WC, int IB, int JB, typename YT>
+// Q: B is the weights' int8 codes (4 granules to a row, in slot g ^ swz4(r)), which each wavefront turns into bf16
+// in registers right before it multiplies: for few tile rows, where laying What out first costs more.
+__device__ __forceinline__ int swz4(int r) { return (((r >> 1) & 1) ^ ((r >> 3) & 1)) | (((r >> 2) & 1) << 1); }
+
+// 16 codes -> two fragments of bf16(code * s): with u = code + 128, fma(u, s, -128 s) = code * s exactly (at
+// most 7 + 11 significant bits), then one rounding
+__device__ __forceinline__ void codes_to_bf16(u32x4 q, float s, float s128, bf16x8& lo, bf16x8& hi)
+{
+    u32x4 a, c;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t u = q[w] ^ 0x80808080u;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf((float)((u >> (8 * e)) & 0xFFu), s, s128);
+        u32x4& to = w < 2 ? a : c;
+        to[2 * (w & 1)] = pk_bf16(v[0], v[1]);
+        to[2 * (w & 1) + 1] = pk_bf16(v[2], v[3]);
+    }
+    lo = __builtin_bit_cast(bf16x8, a);
+    hi = __builtin_bit_cast(bf16x8, c);
+}
+
+template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
 __global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
 pgq_mm_nt_kernel(MmNt p)
 {
     constexpr int T = 64 * WR * WC, TI = 32 * IB * WR, TJ = 32 * JB * WC;
-    constexpr int AI = TI * 8 / T, BI = TJ * 8 / T;          // load instructions per thread per stage
-    constexpr int AS = TI * kTK * 2, BS = TJ * kTK * 2;      // bytes per stage
-    constexpr int EP = 32 * JB + 4;                          // epilogue row pitch in floats
-    constexpr int LDS = 2 * (AS + BS) > WR * WC * 32 * EP * 4 ? 2 * (AS + BS) : WR * WC * 32 * EP * 4;
+    constexpr int BG = Q ? 4 : 8;                            // granules per row of B
+    constexpr int AI = TI * 8 / T, BI = TJ * BG / T;         // load instructions per thread per stage
+    constexpr int AS = TI * kTK * 2, BS = TJ * BG * 16;      // bytes per stage
+    static_assert(TI * 8 % T == 0 && TJ * BG % T == 0, "whole load instructions");
+    constexpr int CW = (JB & (JB - 1)) == 0 ? 32 * JB : 32;  // columns a wavefront's way out takes at a time
+    constexpr int EP = CW + 4;                               // its row pitch in floats
+    constexpr int LDS = NB * (AS + BS) > WR * WC * 32 * EP * 4 ? NB * (AS + BS) : WR * WC * 32 * EP * 4;
     __shared__ __align__(16) uint8_t lds[LDS];
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -216,17 +244,21 @@ pgq_mm_nt_kernel(MmNt p)
     const int64_t l0 = (int64_t)part * p.chunk, len = min(p.chunk, p.L - l0);      // this part of the contraction
     const int irows = (int)min((int64_t)TI, p.I - i0), jrows = (int)min((int64_t)TJ, p.J - j0);
     const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + i0 * p.lda + l0), 0, (int)(((int64_t)(irows - 1) * p.lda + len) * 2), 0x00020000);
-    const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb + l0), 0, (int)(((int64_t)(jrows - 1) * p.ldb + len) * 2), 0x00020000);
+    const __amdgpu_buffer_rsrc_t br =
+        Q ? __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + j0 * p.ldb + l0), 0, (int)((int64_t)(jrows - 1) * p.ldb + len), 0x00020000)
+          : __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb + l0), 0, (int)(((int64_t)(jrows - 1) * p.ldb + len) * 2), 0x00020000);
     // load slot of instruction c: row c T / 8 + tid / 8, slot tid % 8 (its granule is the same for every c)
     const int r0 = tid >> 3, g0 = (tid & 7) ^ swz(r0);
-    const uint32_t ao = (uint32_t)(r0 * p.lda + 8 * g0) * 2u, bo = (uint32_t)(r0 * p.ldb + 8 * g0) * 2u;
-    const uint32_t astep = (uint32_t)(T / 8 * 2 * p.lda), bstep = (uint32_t)(T / 8 * 2 * p.ldb);
+    const int br0 = tid / BG, bg0 = Q ? (tid & 3) ^ swz4(br0) : g0;
+    const uint32_t ao = (uint32_t)(r0 * p.lda + 8 * g0) * 2u, bo = Q ? (uint32_t)(br0 * p.ldb + 16 * bg0) : (uint32_t)(r0 * p.ldb + 8 * g0) * 2u;
+    const uint32_t astep = (uint32_t)(T / 8 * 2 * p.lda), bstep = Q ? (uint32_t)(T / 4 * p.ldb) : (uint32_t)(T / 8 * 2 * p.ldb);
     const int nst = (int)((len + kTK - 1) / kTK);
     auto issue = [&](int st) {
-        uint8_t* la = lds + (st & 1) * (AS + BS);
+        uint8_t* la = lds + (st % NB) * (AS + BS);
         uint8_t* lb = la + AS;
         const bool ok = (int64_t)st * kTK + 8 * g0 < len;
-        const uint32_t k0 = (uint32_t)st * (kTK * 2);
+        const bool bok = Q ? (int64_t)st * kTK + 16 * bg0 < len : ok;
+        const uint32_t k0 = (uint32_t)st * (kTK * 2), kb0 = Q ? (uint32_t)st * kTK : k0;
         // (mask arithmetic, so that the compiler keeps one load per slot rather than branching around two)
 #pragma unroll
         for (int c = 0; c < AI; ++c) {
@@ -236,13 +268,22 @@ pgq_mm_nt_kernel(MmNt p)
         }
 #pragma unroll
         for (int c = 0; c < BI; ++c) {
-            const uint32_t bad = 0u - (uint32_t)!(ok && r0 + c * (T / 8) < jrows);
+            const uint32_t bad = 0u - (uint32_t)!(bok && br0 + c * (T / BG) < jrows);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_ptr)(lb + (c * T + wave * 64) * 16), 16,
-                                                     ((bo + (uint32_t)c * bstep + k0) & ~bad) | (kOOB & bad), 0, 0, 0);
+                                                     ((bo + (uint32_t)c * bstep + kb0) & ~bad) | (kOOB & bad), 0, 0, 0);
         }
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
     const int r32 = lane & 31, h = lane >> 5;
+    float sc[Q ? JB : 1], sc128[Q ? JB : 1];                 // the scales of this lane's weight rows
+    if constexpr (Q) {
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            const int64_t n = j0 + wj + 32 * j + r32;
+            sc[j] = n < p.J ? f16_to_f32(((const GLB uint16_t*)p.scales)[n]) : 0.0f;
+            sc128[j] = -128.0f * sc[j];                      // exact
+        }
+    }
     f32x16 acc[IB][JB];
 #pragma unroll
     for (int i = 0; i < IB; ++i)
@@ -251,10 +292,10 @@ pgq_mm_nt_kernel(MmNt p)
     // Fragments of one 32-wide half of a stage: lane half h supplies l = 16 h + 8 t .. + 7 in instruction t,
     // so that its 16 l are contiguous in LDS.
     struct Frag {
-        bf16x8 a[IB][2], b[JB][2];
+        bf16x8 a[IB][2], b[JB][Q ? 1 : 2];
     } f0, f1;
     auto fetch = [&](Frag& f, int st, int kb) __attribute__((always_inline)) {
-        const uint8_t* la = lds + (st & 1) * (AS + BS);
+        const uint8_t* la = lds + (st % NB) * (AS + BS);
         const uint8_t* lb = la + AS;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -263,37 +304,59 @@ pgq_mm_nt_kernel(MmNt p)
                 const int r = wi + 32 * i + r32;
                 f.a[i][t] = *reinterpret_cast<const bf16x8*>(la + (r * 8 + ((4 * kb + 2 * h + t) ^ swz(r))) * 16);
             }
+            if constexpr (!Q) {
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    const int r = wj + 32 * j + r32;
+                    f.b[j][t] = *reinterpret_cast<const bf16x8*>(lb + (r * 8 + ((4 * kb + 2 * h + t) ^ swz(r))) * 16);
+                }
+            }
+        }
+        if constexpr (Q) {
 #pragma unroll
             for (int j = 0; j < JB; ++j) {
                 const int r = wj + 32 * j + r32;
-                f.b[j][t] = *reinterpret_cast<const bf16x8*>(lb + (r * 8 + ((4 * kb + 2 * h + t) ^ swz(r))) * 16);
+                f.b[j][0] = *reinterpret_cast<const bf16x8*>(lb + (r * 4 + ((2 * kb + h) ^ swz4(r))) * 16);
             }
         }
     };
     auto multiply = [&](const Frag& f) __attribute__((always_inline)) {
+        bf16x8 b[JB][2];
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            if constexpr (Q) {
+                codes_to_bf16(__builtin_bit_cast(u32x4, f.b[j][0]), sc[j], sc128[j], b[j][0], b[j][1]);
+            } else {
+                b[j][0] = f.b[j][0];
+                b[j][1] = f.b[j][1];
+            }
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < IB; ++i)
 #pragma unroll
                 for (int j = 0; j < JB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i][t], f.b[j][t], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i][t], b[j][t], acc[i][j], 0, 0, 0);
     };
     // Two sets of fragments: while the matrix cores work on one half stage, the next half is read from LDS.
     // The barrier sits between the halves: there every wave has read all of stage st, so the loads of stage
-    // st + 2 may overwrite it, and those of st + 1, issued a stage earlier, have arrived.
-    auto turn = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+    // st + NB may overwrite it, and those of st + 1 have arrived (the younger stages' loads may still be out).
+    constexpr int NL = AI + BI;
     if (nst > 0) {
-        issue(0);
-        turn();
-        if (nst > 1) issue(1);
+#pragma unroll
+        for (int s = 0; s < NB; ++s)
+            if (s < nst) issue(s);
+        if (nst >= NB) wait_barrier<(NB - 1) * NL>();
+        else wait_barrier<0>();
         fetch(f0, 0, 0);
     }
     for (int st = 0; st < nst; ++st) {
         fetch(f1, st, 1);
         multiply(f0);
-        turn();
-        if (st + 2 < nst) issue(st + 2);
+        if (st + NB - 1 < nst) wait_barrier<(NB - 2) * NL>();
+        else wait_barrier<0>();
+        if (st + NB < nst) issue(st + NB);
         if (st + 1 < nst) fetch(f0, st + 1, 0);
         if ((int64_t)st * kTK + 32 < len) multiply(f1);
     }
@@ -309,38 +372,41 @@ pgq_mm_nt_kernel(MmNt p)
                     part_out[((i * JB + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         return;
     }
-    // out through LDS, one 32-row block at a time, so that a lane holds consecutive columns
+    // out through LDS, 32 rows of CW columns at a time, so that a lane holds consecutive columns
     constexpr int V = sizeof(YT) == 4 ? 4 : 8;
-    constexpr int LPR = 32 * JB / V;                          // lanes per row
+    constexpr int LPR = CW / V;                               // lanes per row
     constexpr int STEP = 64 / LPR;                            // rows a wavefront covers at once
     constexpr int G = sizeof(YT) == 4 && STEP <= 8 ? 4 : 2;   // and a lane takes G of those at a time (more spill)
-    static_assert(32 % (STEP * G) == 0, "whole groups");
+    static_assert(64 % LPR == 0 && 32 % (STEP * G) == 0, "whole groups");
     float* tl = reinterpret_cast<float*>(lds) + wave * (32 * EP);
-    const Out<V, YT> out(p.e, j0 + wj + lane % LPR * V, p.J);
     lds_barrier();
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
+    for (int jc = 0; jc < 32 * JB / CW; ++jc) {
+        const Out<V, YT> out(p.e, j0 + wj + jc * CW + lane % LPR * V, p.J);
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
+        for (int i = 0; i < IB; ++i) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) tl[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + r32] = acc[i][j][r];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            for (int j = 0; j < CW / 32; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) tl[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + r32] = acc[i][jc * (CW / 32) + j][r];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
-        for (int q = 0; q < 32; q += STEP * G) {
-            const int rr = q + lane / LPR;
-            float v[G][V];
+            for (int q = 0; q < 32; q += STEP * G) {
+                const int rr = q + lane / LPR;
+                float v[G][V];
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+                for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int u = 0; u < V / 4; ++u) {
-                    const f32x4 x = *reinterpret_cast<const f32x4*>(tl + (rr + g * STEP) * EP + lane % LPR * V + 4 * u);
+                    for (int u = 0; u < V / 4; ++u) {
+                        const f32x4 x = *reinterpret_cast<const f32x4*>(tl + (rr + g * STEP) * EP + lane % LPR * V + 4 * u);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) v[g][4 * u + w] = x[w];
-                }
-            const int64_t row = i0 + wi + 32 * i + rr;
-            if (row < p.I && out.col < p.J) out.template rows<G>(row, STEP, p.I, v);
+                        for (int w = 0; w < 4; ++w) v[g][4 * u + w] = x[w];
+                    }
+                const int64_t row = i0 + wi + 32 * i + rr;
+                if (row < p.I && out.col < p.J) out.template rows<G>(row, STEP, p.I, v);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
@@ -384,25 +450,27 @@ __global__ void __launch_bounds__(256) pgq_mm_nt_reduce_kernel(MmNt p)
 }
 
 // The tiles a product can be cut into.  stage: microseconds of one 64-wide stage of a workgroup that has its
-// compute unit alone; busy: per workgroup when several share it; per_cu: how many fit.  Measured at
-// 1024 x 1024 x 1024 and 8192 x 4096 x 4096.
+// compute unit alone; busy: a stage's share of a compute unit that several keep busy; per_cu: how many fit.
+// Measured at 1024 x 1024 x 1024 and 8192 x 4096 x 4096.
 struct NtKind {
     int ti, tj, threads, per_cu;
     double stage, busy;
     const void *f32, *bf16, *reduce;
+    bool codes;                                   // B as codes
 };
-template <int WR, int WC, int IB, int JB>
+template <int WR, int WC, int IB, int JB, bool Q, int NB>
 NtKind nt_kind(int per_cu, double stage, double busy)
 {
     return {32 * IB * WR, 32 * JB * WC, 64 * WR * WC, per_cu, stage, busy,
-            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, float>),
-            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, uint16_t>),
-            reinterpret_cast<const void*>(&pgq_mm_nt_reduce_kernel<WR, WC, IB, JB>)};
+            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, float>),
+            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, uint16_t>),
+            reinterpret_cast<const void*>(&pgq_mm_nt_reduce_kernel<WR, WC, IB, JB>), Q};
 }
 // (two 256 x 256 forms: wavefronts of 64 x 128 write longer row pieces, those of 128 x 64 are 3% faster in long
 // contractions; the choice between them is by L)
-const NtKind kNt[] = {nt_kind<4, 2, 2, 4>(1, 1.75, 1.70), nt_kind<2, 4, 4, 2>(1, 1.75, 1.66), nt_kind<2, 2, 2, 2>(2, 0.85, 0.55),
-                      nt_kind<2, 2, 2, 1>(3, 0.55, 0.31), nt_kind<2, 2, 1, 1>(5, 0.33, 0.19)};
+const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2>(1, 1.75, 1.70), nt_kind<2, 2, 2, 2, false, 2>(2, 0.85, 0.70), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.33),
+                      nt_kind<2, 2, 1, 1, false, 4>(2, 0.27, 0.21), nt_kind<1, 4, 4, 1, true, 3>(2, 0.75, 0.62),
+                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.35, 0.35)};
 int64_t nt_tiles(const NtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 // ---- A columns times B columns ----------------------------------------------------------------------
@@ -523,17 +591,16 @@ pgq_mm_tt_kernel(MmTt p)
                 for (int j = 0; j < JB; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i][t], f.b[j][t], acc[i][j], 0, 0, 0);
     };
-    auto turn_over = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
     if (nst > 0) {
         issue(0);
-        turn_over();
+        wait_barrier<0>();
         if (nst > 1) issue(1);
         fetch(f0, 0, 0);
     }
     for (int st = 0; st < nst; ++st) {
         fetch(f1, st, 1);
         multiply(f0);
-        turn_over();
+        wait_barrier<0>();
         if (st + 2 < nst) issue(st + 2);
         if (st + 1 < nst) fetch(f0, st + 1, 0);
         multiply(f1);
@@ -598,35 +665,45 @@ int64_t tt_tiles(const TtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1)
 
 }  // namespace
 
-// The tile and the number of parts with the least estimated time: for each round of workgroups the stages of a
-// part, a start, and the tile's way out at a compute unit's share of the memory rate (20 KB a microsecond);
-// parts add the trip of their sums through memory and a launch.
-void mm_nt_plan(MmNt& p)
+// The tile and the number of parts with the least estimated time.  A tile that has its compute unit to itself
+// goes in rounds of 256; smaller ones keep several on a unit and flow.  To that the trip of the outputs (5.3 MB a
+// microsecond: the stores of a tile hardly overlap its stages), a start a round, and, for parts, their sums'
+// trip and a launch.  Measured against the clock at 16384 x 1584 x 528, 16384 x 528 x 1584, 8192 x 8192 x
+// 4096, 4096 x 1536 x 512 and 1009 x 717 x 1032: within 15%, and the tile chosen within 5% of the best.
+double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes)
 {
     double best = 0;
+    // laying What out: codes in, bf16 out, and a launch
+    const double layout = codes_ok ? 4.0 + (double)p.J * (double)p.L * 3.0 / 4e6 : 0.0;
+    const double out = (double)p.I * (double)p.J * out_bytes / 5.3e6;
     const int64_t stages = std::max<int64_t>(1, (p.L + 63) / 64);
     for (int k = 0; k < (int)(sizeof(kNt) / sizeof(kNt[0])); ++k) {
         const NtKind& kind = kNt[k];
+        if (kind.codes && !codes_ok) continue;
         const int64_t tiles = nt_tiles(kind, p.I, p.J);
-        const double out = 3.0 + (double)kind.ti * kind.tj * 4.0 / 20e3;
         for (int64_t s = 1; s <= 16; s *= 2) {
             const int64_t per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
             if (s > 1 && (parts != s || per < 4 || tiles * parts > 512)) break;
-            const int64_t wgs = tiles * parts, slots = 256 * kind.per_cu;
-            double t = (double)(wgs / slots) * ((double)per * kind.busy * kind.per_cu + out * kind.per_cu);
-            if (const int64_t left = wgs % slots) {
-                const int64_t share = (left + 255) / 256;
-                t += (double)per * std::max(kind.stage, kind.busy * (double)share) + out * (double)share;
+            const int64_t wgs = tiles * parts, rounds = (wgs + 255) / 256;
+            double t = out;
+            if (kind.per_cu == 1) {
+                t += (double)rounds * ((double)per * kind.busy + 2.0) + 2.0;
+            } else {
+                const double share = (double)std::min<int64_t>(kind.per_cu, rounds);
+                t += (double)per * std::max(std::max(kind.stage, kind.busy * share), kind.busy * (double)wgs / 256.0) + 4.0;
             }
             if (parts > 1) t += 4.0 + (double)wgs * kind.ti * kind.tj * 8.0 / 5e6;
+            if (!kind.codes) t += layout;
             if (best == 0 || t < best) {
                 best = t;
                 p.kind = k;
+                p.from_codes = kind.codes;
                 p.splits = (int32_t)parts;
                 p.chunk = per * 64;
             }
         }
     }
+    return best;
 }
 
 size_t mm_nt_partial_bytes(const MmNt& p)

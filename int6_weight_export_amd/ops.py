@@ -22,6 +22,12 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+# The current stream's handle of GPU `index`: what torch.cuda.current_stream(index).cuda_stream gives, without
+# building the Stream object (2.8 us a call against 0.1).
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -447,7 +453,7 @@ def _launch_linear(fn, size_fn, name: str, desc: bytes, index: int) -> None:
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return _launch_linear(fn, size_fn, name, desc, index)
-    stream = _stream()
+    stream = _stream_of(index)
     rc = fn(desc, None, 0, stream)
     if rc == pgq.PGQ_ERR_WORKSPACE:
         need = ctypes.c_size_t(0)
@@ -665,7 +671,7 @@ class AdamW:
 
     def _enqueue_step(self, h, ptrs) -> None:
         rc = pgq._lib.pgq_adamw_step(self._arr, self.n, self.state_bits, ptrs, h, None if h is not None else _p(self.hyper),
-                                     self._ws_ptr, self._ws_bytes, self._table_flags(), self._status_ptr, _stream())
+                                     self._ws_ptr, self._ws_bytes, self._table_flags(), self._status_ptr, _stream_of(self._index))
         if rc != pgq.PGQ_OK:
             pgq.check(rc, "pgq_adamw_step")
 
@@ -701,4 +707,4 @@ class AdamW:
 
     def _enqueue_decode(self, m_ptrs, r_ptrs) -> None:
         pgq.check(pgq.pgq_adamw_decode(self._arr, self.n, m_ptrs, r_ptrs, self._ws_ptr, self._ws_bytes, self._table_flags(),
-                                       self._status_ptr, _stream()), "pgq_adamw_decode")
+                                       self._status_ptr, _stream_of(self._index)), "pgq_adamw_decode")

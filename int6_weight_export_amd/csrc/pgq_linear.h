@@ -87,4 +87,15 @@ hipError_t launch_mm_tt(const MmTt& p, void* stream);
 // splits > 1: the sum of the parts, in their order
 hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream);
 
+// db[n] = sum of part[i][n] over the row blocks i.
+struct Dbias {
+    const float* part;
+    int64_t blocks, N;
+    float* out;                  // NULL: nothing to do
+};
+hipError_t launch_mm_dbias(const Dbias& d, void* stream);
+// dX, dW and db in one launch: the pair of tiles, with kind, splits and chunk of both products.
+int mm_both_plan(MmNt& x, MmTt& w, double out_bytes);
+hipError_t launch_mm_both(int both, const MmNt& x, const MmTt& w, const Dbias& d, void* stream);
+
 }  // namespace pgq

@@ -137,13 +137,14 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) { return (uint32_t
 // rows (forward) or transposed (dX), and a copy of X with 16-byte aligned rows where X has none.  Rows are
 // padded to 8 elements with zeros.  What is formed once here instead of in every tile: it is small beside X
 // and Y, and its conversion from codes cost the matrix kernel about a sixth of its time.
-constexpr int kDzRows = 64, kDzCols = 256;     // dZ unit
+constexpr int kDzCols = 256;                   // columns of a dZ unit
 constexpr int kFlat = 256 * 4;                 // granules (8 elements) of a flat unit
 
 struct Prep {
     pgq_linear_bwd b;            // the sources (codes, scales, x and their strides also in forward)
     uint16_t* dz;                // M x ldz_out, or NULL: only the partial sums
-    float* dbias_part;           // ceil(M / kDzRows) x N, or NULL
+    float* dbias_part;           // ceil(M / dz_rows) x N, or NULL
+    int32_t dz_rows;             // rows of a dZ unit
     uint16_t* what;              // N x Kp
     uint16_t* what_t;            // K x Np
     uint16_t* xc;                // M x Kp
@@ -200,11 +201,11 @@ __device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums
     float t[8] = {};
     if (n < p.Np) {
 #pragma unroll 1
-        for (int k0 = 0; k0 < kDzRows / 8; k0 += kHold) {
+        for (int k0 = 0; k0 < p.dz_rows / 8; k0 += kHold) {
             u32x4 v[kHold][F32 ? 2 : 1], zv[kHold];
 #pragma unroll
             for (int k = 0; k < kHold; ++k) {
-                const int64_t m = min(rb * kDzRows + phase + 8 * (k0 + k), b.M - 1);
+                const int64_t m = min(rb * p.dz_rows + phase + 8 * (k0 + k), b.M - 1);
                 if constexpr (F32) {
                     const uint32_t* row = (const uint32_t*)b.dy + m * b.lddy;
                     v[k][0] = load_cols<4>(row, n, b.N);
@@ -216,7 +217,7 @@ __device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums
             }
 #pragma unroll
             for (int k = 0; k < kHold; ++k) {
-                const int64_t m = rb * kDzRows + phase + 8 * (k0 + k);
+                const int64_t m = rb * p.dz_rows + phase + 8 * (k0 + k);
                 float d[8];
                 if constexpr (F32) {
                     const f32x4 lo = __builtin_bit_cast(f32x4, v[k][0]), hi = __builtin_bit_cast(f32x4, v[k][1]);
@@ -348,27 +349,6 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
             o = load_cols<8>(b.x + r * b.ldx, k, b.K);
             *(GLB u32x4*)(p.xc + r * p.Kp + k) = o;
         }
-    }
-}
-
-// db[n]: the row blocks' partial sums, sixteen phases joined in a fixed order
-__global__ void __launch_bounds__(1024) pgq_linear_dbias_kernel(const float* part, int64_t blocks, int64_t N, float* dbias)
-{
-    __shared__ float sums[16][64];
-    const int lane = (int)threadIdx.x & 63, phase = (int)threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
-    float s = 0.0f;
-    if (n < N) {
-#pragma unroll 8
-        for (int64_t i = phase; i < blocks; i += 16) s += part[i * N + n];
-    }
-    sums[phase][lane] = s;
-    __syncthreads();
-    if (phase == 0 && n < N) {
-        float v = sums[0][lane];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) v += sums[i][lane];
-        dbias[n] = v;
     }
 }
 
@@ -592,7 +572,9 @@ struct BwdPlan {
     bool dz, copy_x;             // dZ and X go through scratch
     MmNt nt;                     // dX, dW: sizes, tiles and parts
     MmTt tt;
-    int64_t blocks;              // row blocks of the db partial sums
+    int both;                    // dX and dW: their pair of tiles in one launch
+    int32_t dz_rows;
+    int64_t blocks;              // row blocks of dZ units (and of the db partial sums)
     size_t o_dz, o_db, o_what_t, o_x, o_part, o_part_dx, bytes;
 };
 BwdPlan plan_bwd(const pgq_linear_bwd& p)
@@ -604,7 +586,9 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     q.db = p.dbias && p.N > 0;
     q.tile = p.N >= kLong || p.K >= kLong;
     auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += up256(n); return at; };
-    q.blocks = (p.M + kDzRows - 1) / kDzRows;
+    // long units for few partial sums, short ones where there are not enough of them to fill the machine
+    q.dz_rows = p.M * p.N >= (int64_t)4 << 20 ? 64 : 16;
+    q.blocks = (p.M + q.dz_rows - 1) / q.dz_rows;
     if (q.db) q.o_db = take((size_t)q.blocks * p.N * 4);
     if (q.tile || p.N == 0 || p.M == 0) return q;
     if (q.dx || q.dw) {
@@ -616,8 +600,6 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
         q.nt.I = p.M;
         q.nt.J = p.K;
         q.nt.L = up8(p.N);
-        mm_nt_plan(q.nt, false, (double)float_size(p.dx_dtype));
-        q.o_part_dx = take(mm_nt_partial_bytes(q.nt));
     }
     if (q.dw) {
         q.copy_x = !direct(p.x, p.ldx, p.K);
@@ -625,9 +607,12 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
         q.tt.I = p.N;
         q.tt.J = p.K;
         q.tt.L = p.M;
-        mm_tt_plan(q.tt);
-        q.o_part = take(mm_tt_partial_bytes(q.tt));
     }
+    if (q.dx && q.dw) q.both = mm_both_plan(q.nt, q.tt, (double)float_size(p.dx_dtype));
+    else if (q.dx) mm_nt_plan(q.nt, false, (double)float_size(p.dx_dtype));
+    else if (q.dw) mm_tt_plan(q.tt);
+    if (q.dx) q.o_part_dx = take(mm_nt_partial_bytes(q.nt));
+    if (q.dw) q.o_part = take(mm_tt_partial_bytes(q.tt));
     return q;
 }
 
@@ -772,6 +757,7 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     pr.Kp = up8(b.K);
     pr.Np = up8(b.N);
     pr.dz = q.dz ? reinterpret_cast<uint16_t*>(ws + q.o_dz) : nullptr;
+    pr.dz_rows = q.dz_rows;
     pr.dbias_part = q.db ? reinterpret_cast<float*>(ws + q.o_db) : nullptr;
     if (q.dz || q.db) pr.n_dz = q.blocks * ((pr.Np + kDzCols - 1) / kDzCols);
     if (mm && q.dx) {
@@ -784,14 +770,12 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     }
     const int64_t units = pr.n_dz + pr.n_what_t + pr.n_x;
     const bool reduce = mm && q.dw && q.tt.splits > 1, reduce_dx = mm && q.dx && q.nt.splits > 1;
-    Launches l((units > 0) + q.dx + reduce_dx + q.dw + reduce + q.db, stream);
+    const bool both = mm && q.dx && q.dw;
+    Launches l((units > 0) + (both ? 1 : q.dx + q.dw + q.db) + reduce + reduce_dx, stream);
     void* pargs[] = {&pr};
     if (units > 0) l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), units, 256, pargs);
-    if (q.db) {
-        const float* part = pr.dbias_part;
-        void* args[] = {&part, const_cast<int64_t*>(&q.blocks), &b.N, &b.dbias};
-        l.go(reinterpret_cast<const void*>(&pgq_linear_dbias_kernel), (b.N + 63) / 64, 1024, args);
-    }
+    const Dbias db = {pr.dbias_part, q.blocks, b.N, q.db ? b.dbias : nullptr};
+    if (q.db && !both && l.next()) l.e = launch_mm_dbias(db, stream);
     if (!mm) {
         pgq_linear_fwd f;
         memset(&f, 0, sizeof(f));
@@ -800,36 +784,29 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
         if (q.dw) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DW>), tiles_of(b.N, b.K), 256, args);
         return l.done();
     }
-    const uint16_t* dz = q.dz ? pr.dz : static_cast<const uint16_t*>(b.dy);
-    const int64_t lddz = q.dz ? pr.Np : b.lddy;
-    if (q.dx) {
-        MmNt m = q.nt;
-        m.a = dz;
-        m.lda = lddz;
-        m.b = pr.what_t;
-        m.ldb = pr.Np;
-        m.partial = reinterpret_cast<float*>(ws + q.o_part_dx);
-        m.e.y = b.dx;
-        m.e.ldy = b.lddx;
-        m.e.y_dtype = b.dx_dtype;
-        m.e.vec = rows16(b.dx, b.dx_dtype, b.lddx);
-        if (l.next()) l.e = launch_mm_nt(m, stream);
-        if (reduce_dx && l.next()) l.e = launch_mm_nt_reduce(m, stream);
-    }
-    if (q.dw) {
-        MmTt m = q.tt;
-        m.a = dz;
-        m.lda = lddz;
-        m.b = q.copy_x ? pr.xc : b.x;
-        m.ldb = q.copy_x ? pr.Kp : b.ldx;
-        m.c = b.dw;
-        m.ldc = b.lddw;
-        m.c_dtype = b.dw_dtype;
-        m.mask = b.mask;
-        m.partial = reinterpret_cast<float*>(ws + q.o_part);
-        if (l.next()) l.e = launch_mm_tt(m, stream);
-        if (reduce && l.next()) l.e = launch_mm_tt_reduce(m, stream);
-    }
+    MmNt x = q.nt;
+    MmTt w = q.tt;
+    x.a = w.a = q.dz ? pr.dz : static_cast<const uint16_t*>(b.dy);
+    x.lda = w.lda = q.dz ? pr.Np : b.lddy;
+    x.b = pr.what_t;
+    x.ldb = pr.Np;
+    x.partial = reinterpret_cast<float*>(ws + q.o_part_dx);
+    x.e.y = b.dx;
+    x.e.ldy = b.lddx;
+    x.e.y_dtype = b.dx_dtype;
+    x.e.vec = rows16(b.dx, b.dx_dtype, b.lddx);
+    w.b = q.copy_x ? pr.xc : b.x;
+    w.ldb = q.copy_x ? pr.Kp : b.ldx;
+    w.c = b.dw;
+    w.ldc = b.lddw;
+    w.c_dtype = b.dw_dtype;
+    w.mask = b.mask;
+    w.partial = reinterpret_cast<float*>(ws + q.o_part);
+    if (both && l.next()) l.e = launch_mm_both(q.both, x, w, db, stream);
+    if (q.dx && !both && l.next()) l.e = launch_mm_nt(x, stream);
+    if (q.dw && !both && l.next()) l.e = launch_mm_tt(w, stream);
+    if (reduce_dx && l.next()) l.e = launch_mm_nt_reduce(x, stream);
+    if (reduce && l.next()) l.e = launch_mm_tt_reduce(w, stream);
     return l.done();
 }
 

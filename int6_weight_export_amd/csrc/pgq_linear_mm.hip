@@ -222,9 +222,16 @@ __device__ __forceinline__ void codes_to_bf16(u32x4 q, float s, float s128, bf16
     hi = __builtin_bit_cast(bf16x8, c);
 }
 
+template <int WR, int WC, int IB, int JB, bool Q, int NB>
+constexpr int nt_lds()
+{
+    constexpr int stages = NB * (32 * IB * WR * 8 + 32 * JB * WC * (Q ? 4 : 8)) * 16;
+    constexpr int out = WR * WC * 32 * (((JB & (JB - 1)) == 0 ? 32 * JB : 32) + 4) * 4;
+    return stages > out ? stages : out;
+}
+
 template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
-__global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
-pgq_mm_nt_kernel(MmNt p)
+__device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t total, uint8_t* lds)
 {
     constexpr int T = 64 * WR * WC, TI = 32 * IB * WR, TJ = 32 * JB * WC;
     constexpr int BG = Q ? 4 : 8;                            // granules per row of B
@@ -233,13 +240,11 @@ pgq_mm_nt_kernel(MmNt p)
     static_assert(TI * 8 % T == 0 && TJ * BG % T == 0, "whole load instructions");
     constexpr int CW = (JB & (JB - 1)) == 0 ? 32 * JB : 32;  // columns a wavefront's way out takes at a time
     constexpr int EP = CW + 4;                               // its row pitch in floats
-    constexpr int LDS = NB * (AS + BS) > WR * WC * 32 * EP * 4 ? NB * (AS + BS) : WR * WC * 32 * EP * 4;
-    __shared__ __align__(16) uint8_t lds[LDS];
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ);
     uint32_t ti, tj, part;
-    tile_of(blockIdx.x, gridDim.x, gi, gj, ti, tj, part);
+    tile_of(wid, total, gi, gj, ti, tj, part);
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
     const int64_t l0 = (int64_t)part * p.chunk, len = min(p.chunk, p.L - l0);      // this part of the contraction
     const int irows = (int)min((int64_t)TI, p.I - i0), jrows = (int)min((int64_t)TJ, p.J - j0);
@@ -410,6 +415,14 @@ pgq_mm_nt_kernel(MmNt p)
     }
 }
 
+template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
+__global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
+pgq_mm_nt_kernel(MmNt p)
+{
+    __shared__ __align__(16) uint8_t lds[nt_lds<WR, WC, IB, JB, Q, NB>()];
+    nt_body<WR, WC, IB, JB, Q, NB, YT>(p, blockIdx.x, gridDim.x, lds);
+}
+
 // the sums of the parts, in their order, through the epilogue: one wavefront takes 8 rows of 32 columns
 template <int WR, int WC, int IB, int JB>
 __global__ void __launch_bounds__(256) pgq_mm_nt_reduce_kernel(MmNt p)
@@ -508,20 +521,21 @@ __device__ __forceinline__ void put4(const MmTt& p, int64_t i, int64_t j, f32x4 
 }
 
 template <int WR, int WC, int IB, int JB>
-__global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
-pgq_mm_tt_kernel(MmTt p)
+constexpr int tt_lds() { return 2 * 64 * 2 * (32 * IB * WR + 32 * JB * WC); }
+
+template <int WR, int WC, int IB, int JB>
+__device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t total, uint8_t* lds)
 {
     constexpr int T = 64 * WR * WC, TI = 32 * IB * WR, TJ = 32 * JB * WC;
     constexpr int AG = TI / 8, BG = TJ / 8;                  // granules per row
     constexpr int AI = 64 * AG / T, BI = 64 * BG / T;        // load instructions per thread per stage
     constexpr int AS = 64 * TI * 2, BS = 64 * TJ * 2;
     static_assert(64 * AG % T == 0 && 64 * BG % T == 0, "whole load instructions");
-    __shared__ __align__(16) uint8_t lds[2 * (AS + BS)];
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ), tiles = gi * gj;
     uint32_t ti, tj, part;       // the tiles of one part read the same rows: they share an XCD
-    tile_of(blockIdx.x, gridDim.x, gi, gj, ti, tj, part);
+    tile_of(wid, total, gi, gj, ti, tj, part);
     const uint32_t tile = ti * gj + tj;
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
     const int64_t l0 = (int64_t)part * p.chunk;
@@ -623,6 +637,58 @@ pgq_mm_tt_kernel(MmTt p)
 }
 
 template <int WR, int WC, int IB, int JB>
+__global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
+pgq_mm_tt_kernel(MmTt p)
+{
+    __shared__ __align__(16) uint8_t lds[tt_lds<WR, WC, IB, JB>()];
+    tt_body<WR, WC, IB, JB>(p, blockIdx.x, gridDim.x, lds);
+}
+
+// db[n]: the row blocks' partial sums for 64 columns, sixteen phases of blocks joined in order, by any number of
+// wavefronts (the order of the additions does not depend on it)
+__device__ __forceinline__ void dbias_body(const Dbias& p, uint32_t unit, uint8_t* lds)
+{
+    float(*sums)[64] = reinterpret_cast<float(*)[64]>(lds);
+    const int lane = (int)threadIdx.x & 63, waves = (int)blockDim.x >> 6;
+    const int64_t n = (int64_t)unit * 64 + lane;
+    for (int phase = (int)threadIdx.x >> 6; phase < 16; phase += waves) {
+        float s = 0.0f;
+        if (n < p.N) {
+#pragma unroll 8
+            for (int64_t i = phase; i < p.blocks; i += 16) s += ((const GLB float*)p.part)[i * p.N + n];
+        }
+        sums[phase][lane] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64 && n < p.N) {
+        float v = sums[0][lane];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += sums[i][lane];
+        p.out[n] = v;
+    }
+}
+__global__ void __launch_bounds__(1024) pgq_mm_dbias_kernel(Dbias p)
+{
+    __shared__ __align__(16) uint8_t lds[16 * 64 * 4];
+    dbias_body(p, blockIdx.x, lds);
+}
+
+// A whole backward pass after its operands are laid out: the tiles of dX, those of dW and the sums of db are
+// independent, so one launch holds them all and the second product fills the compute units that the first
+// leaves idle in its last round.
+template <int A0, int A1, int A2, int A3, int NB, int B0, int B1, int B2, int B3, typename YT>
+__global__ void __launch_bounds__(64 * A0 * A1) __attribute__((amdgpu_waves_per_eu(2)))
+pgq_mm_both_kernel(MmNt x, MmTt w, Dbias d, uint32_t nx, uint32_t nw)
+{
+    static_assert(A0 * A1 == B0 * B1, "one block size");
+    constexpr int LX = nt_lds<A0, A1, A2, A3, false, NB>(), LW = tt_lds<B0, B1, B2, B3>();
+    __shared__ __align__(16) uint8_t lds[LX > LW ? LX : LW];
+    if (blockIdx.x < nx) nt_body<A0, A1, A2, A3, false, NB, YT>(x, blockIdx.x, nx, lds);
+    else if (blockIdx.x < nx + nw) tt_body<B0, B1, B2, B3>(w, blockIdx.x - nx, nw, lds);
+    else dbias_body(d, blockIdx.x - nx - nw, lds);
+}
+
+template <int WR, int WC, int IB, int JB>
 __global__ void __launch_bounds__(256) pgq_mm_tt_reduce_kernel(MmTt p)
 {
     constexpr int TI = 32 * IB * WR, TJ = 32 * JB * WC;
@@ -660,7 +726,8 @@ TtKind tt_kind(int slots, double stage)
             reinterpret_cast<const void*>(&pgq_mm_tt_kernel<WR, WC, IB, JB>),
             reinterpret_cast<const void*>(&pgq_mm_tt_reduce_kernel<WR, WC, IB, JB>)};
 }
-const TtKind kTt[] = {tt_kind<4, 2, 2, 4>(256, 1.9), tt_kind<4, 2, 2, 3>(256, 1.5), tt_kind<2, 2, 2, 2>(512, 1.1)};
+const TtKind kTt[] = {tt_kind<4, 2, 2, 4>(256, 1.9), tt_kind<4, 2, 2, 3>(256, 1.5), tt_kind<2, 2, 2, 2>(512, 1.1),
+                      tt_kind<2, 2, 1, 1>(768, 0.8)};
 int64_t tt_tiles(const TtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 }  // namespace
@@ -733,7 +800,8 @@ hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream)
 }
 
 // The tile and the number of parts with the least estimated time: stages of a part times the rounds its
-// workgroups take, plus the trip of the parts' sums through memory (5 MB a microsecond, twice) and a launch.
+// workgroups take, plus the trip of the parts' sums and a launch.
+constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 32, 48, 64};
 void mm_tt_plan(MmTt& p)
 {
     double best = 0;
@@ -741,14 +809,12 @@ void mm_tt_plan(MmTt& p)
     for (int k = 0; k < (int)(sizeof(kTt) / sizeof(kTt[0])); ++k) {
         const TtKind& kind = kTt[k];
         const int64_t tiles = tt_tiles(kind, p.I, p.J);
-        int64_t last = 0;
-        for (int64_t s = 1; s <= std::min<int64_t>(stages, 64); ++s) {
+        for (const int s : kParts) {
             const int64_t per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
-            if (parts == last || (parts > 1 && tiles * parts > 4 * kind.slots)) continue;
-            last = parts;
+            if (s > 1 && (parts != s || tiles * parts > 4 * kind.slots)) continue;
             const int64_t rounds = (tiles * parts + kind.slots - 1) / kind.slots;
             double t = (double)rounds * ((double)per * kind.stage + 4.0);
-            if (parts > 1) t += 3.0 + (double)(tiles * parts) * kind.ti * kind.tj * 8.0 / 5e6;
+            if (parts > 1) t += 4.0 + (double)(tiles * parts) * kind.ti * kind.tj * 5.5 / 6e6;
             if (best == 0 || t < best) {
                 best = t;
                 p.kind = k;
@@ -757,6 +823,103 @@ void mm_tt_plan(MmTt& p)
             }
         }
     }
+}
+
+// The pairs of tiles that dX and dW run with in one launch.
+struct BothKind {
+    int nt, tt;                                   // places in kNt, kTt
+    int per_cu;
+    double nt_stage, tt_stage;                    // microseconds of a stage when every unit is busy, times per_cu
+    const void *f32, *bf16;
+};
+template <int A0, int A1, int A2, int A3, int NB, int B0, int B1, int B2, int B3>
+BothKind both_kind(int nt, int tt, int per_cu, double nt_stage, double tt_stage)
+{
+    return {nt, tt, per_cu, nt_stage, tt_stage,
+            reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, B0, B1, B2, B3, float>),
+            reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, B0, B1, B2, B3, uint16_t>)};
+}
+const BothKind kBoth[] = {both_kind<2, 4, 4, 2, 2, 4, 2, 2, 4>(0, 0, 1, 1.75, 1.9), both_kind<2, 4, 4, 2, 2, 4, 2, 2, 3>(0, 1, 1, 1.75, 1.5),
+                          both_kind<2, 2, 2, 2, 2, 2, 2, 2, 2>(1, 2, 2, 1.4, 1.1), both_kind<2, 2, 1, 1, 4, 2, 2, 1, 1>(3, 3, 2, 0.45, 0.5)};
+
+// When `first` workgroups of one_first microseconds and then `second` of one_second each, taken in that order by
+// `slots` places, are done: the places free after the first kind's last whole round start at t0, the others at
+// t1; the answer is a multiple of one_second after one of these.
+double two_kinds_done(int64_t slots, int64_t first, double one_first, int64_t second, double one_second)
+{
+    const int64_t rem = first % slots;
+    const double t0 = (double)(first / slots) * one_first, t1 = t0 + (rem ? one_first : 0.0);
+    for (int64_t k = 0;; ++k) {
+        const double ta = t0 + (double)k * one_second;                    // k workgroups on each early place
+        const int64_t late = ta > t1 ? (int64_t)((ta - t1) / one_second) : 0;
+        if ((slots - rem) * k + rem * late >= second) return std::max(ta, t1);
+        const double tb = t1 + (double)(late + 1) * one_second;           // one more on each late place first
+        const int64_t early = (int64_t)((tb - t0) / one_second);
+        if (tb < ta + one_second && (slots - rem) * early + rem * (late + 1) >= second) return tb;
+    }
+}
+
+// The pair and the parts with the least estimated time: both kinds of workgroup over the places, the way out of
+// dX, the trip of the parts' sums (written beside the other work, read back at 6 MB a microsecond), a launch for
+// parts.
+int mm_both_plan(MmNt& x, MmTt& w, double out_bytes)
+{
+    double best = 0;
+    int chosen = 0;
+    const int64_t sx = std::max<int64_t>(1, (x.L + 63) / 64), sw = std::max<int64_t>(1, (w.L + 63) / 64);
+    const double out = (double)x.I * (double)x.J * out_bytes / 5.3e6;
+    for (int k = 0; k < (int)(sizeof(kBoth) / sizeof(kBoth[0])); ++k) {
+        const BothKind& b = kBoth[k];
+        const NtKind& nk = kNt[b.nt];
+        const TtKind& tk = kTt[b.tt];
+        const int64_t tx = nt_tiles(nk, x.I, x.J), tw = tt_tiles(tk, w.I, w.J), slots = 256 * b.per_cu;
+        for (int64_t s = 1; s <= 16; s *= 2) {
+            const int64_t perx = (sx + s - 1) / s, partx = (sx + perx - 1) / perx;
+            if (s > 1 && (partx != s || perx < 4 || tx * partx > 2 * slots)) break;
+            const double one_x = (double)perx * b.nt_stage + 3.0;
+            for (const int s2 : kParts) {
+                const int64_t perw = (sw + s2 - 1) / s2, partw = (sw + perw - 1) / perw;
+                if (s2 > 1 && (partw != s2 || tw * partw > 4 * slots)) continue;
+                const double one_w = (double)perw * b.tt_stage + 3.0;
+                double t = two_kinds_done(slots, tx * partx, one_x, tw * partw, one_w) + out;
+                if (partx > 1) t += 4.0 + (double)(tx * partx) * nk.ti * nk.tj * 5.5 / 6e6;
+                if (partw > 1) t += 4.0 + (double)(tw * partw) * tk.ti * tk.tj * 5.5 / 6e6;
+                if (best == 0 || t < best) {
+                    best = t;
+                    chosen = k;
+                    x.splits = (int32_t)partx;
+                    x.chunk = perx * 64;
+                    w.splits = (int32_t)partw;
+                    w.chunk = perw * 64;
+                }
+            }
+        }
+    }
+    x.kind = kBoth[chosen].nt;
+    x.from_codes = 0;
+    w.kind = kBoth[chosen].tt;
+    return chosen;
+}
+
+hipError_t launch_mm_both(int both, const MmNt& x, const MmTt& w, const Dbias& d, void* stream)
+{
+    const BothKind& b = kBoth[both];
+    const int64_t nx = nt_tiles(kNt[x.kind], x.I, x.J) * x.splits, nw = tt_tiles(kTt[w.kind], w.I, w.J) * w.splits;
+    const int64_t grid = nx + nw + (d.out ? (d.N + 63) / 64 : 0);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    MmNt cx = x;
+    MmTt cw = w;
+    Dbias cd = d;
+    uint32_t ux = (uint32_t)nx, uw = (uint32_t)nw;
+    void* args[] = {&cx, &cw, &cd, &ux, &uw};
+    return launch_plain(x.e.y_dtype == PGQ_F32 ? b.f32 : b.bf16, dim3((unsigned)grid), dim3((unsigned)kNt[x.kind].threads), args, stream);
+}
+
+hipError_t launch_mm_dbias(const Dbias& d, void* stream)
+{
+    Dbias copy = d;
+    void* args[] = {&copy};
+    return launch_plain(reinterpret_cast<const void*>(&pgq_mm_dbias_kernel), dim3((unsigned)((d.N + 63) / 64)), dim3(1024), args, stream);
 }
 
 size_t mm_tt_partial_bytes(const MmTt& p)

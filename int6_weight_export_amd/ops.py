@@ -454,7 +454,7 @@ def _launch_linear(fn, size_fn, name: str, desc: bytes, index: int) -> None:
         with torch.cuda.device(index):
             return _launch_linear(fn, size_fn, name, desc, index)
     stream = _stream_of(index)
-    rc = fn(desc, None, 0, stream)
+    rc = fn(desc, None, 0, stream)          # (refused at once, with nothing enqueued, when it needs scratch)
     if rc == pgq.PGQ_ERR_WORKSPACE:
         need = ctypes.c_size_t(0)
         pgq.check(size_fn(desc, ctypes.byref(need)), name)

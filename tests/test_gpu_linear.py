@@ -214,16 +214,19 @@ def test_backward_types_and_strides(act, slope, dy_t, dx, dw, padx, padc):
 
 
 def test_backward_each_gradient_alone():
-    say("linear backward, one gradient at a time equals all at once")
-    codes, scales, w, x, dy, z, mask, _ = grads(300, 120, 200, "silu", 0.0, True, 30)
+    say("linear backward, one gradient at a time beside all at once")
+    codes, scales, w, x, dy, z, mask, keep = grads(300, 120, 200, "silu", 0.0, True, 30)
     kw = dict(z=z, act="silu")
     every = ops.qlinear_backward(dy, codes, scales, x=x, mask=mask, want_dbias=True, **kw)
+    again = ops.qlinear_backward(dy, codes, scales, x=x, mask=mask, want_dbias=True, **kw)
     dx = ops.qlinear_backward(dy, codes, scales, want_dw=False, **kw)
     dw = ops.qlinear_backward(dy, None, None, x=x, mask=mask, want_dx=False, **kw)
     db = ops.qlinear_backward(dy, None, None, want_dx=False, want_dw=False, want_dbias=True, **kw)
     torch.cuda.synchronize()
     assert set(dx) == {"dx"} and set(dw) == {"dw"} and set(db) == {"dbias"}
-    assert torch.equal(dx["dx"], every["dx"]) and torch.equal(dw["dw"], every["dw"])
+    for got in (dx, dw, db):                  # (the tiles, and so the order of the sums, may differ from the joint call's)
+        check_grads(got, dy, z, x, w, "silu", 0.0, keep)
+    assert all(torch.equal(again[k], every[k]) for k in every)
     assert torch.equal(db["dbias"], every["dbias"])
 
 

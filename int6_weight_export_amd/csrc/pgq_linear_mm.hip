@@ -34,6 +34,12 @@ template <int N>        // all but the N youngest loads of this wave have arrive
 __device__ __forceinline__ void wait_barrier() { asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// 16 bytes a lane from buffer offset voff + soff to LDS, the wave's 1 KB in lane order from `to` on
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t voff, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)to, 16, voff, soff, 0, 0);
+}
+
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b)
 {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));   // round to nearest even
@@ -255,27 +261,39 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     // load slot of instruction c: row c T / 8 + tid / 8, slot tid % 8 (its granule is the same for every c)
     const int r0 = tid >> 3, g0 = (tid & 7) ^ swz(r0);
     const int br0 = tid / BG, bg0 = Q ? (tid & 3) ^ swz4(br0) : g0;
-    const uint32_t ao = (uint32_t)(r0 * p.lda + 8 * g0) * 2u, bo = Q ? (uint32_t)(br0 * p.ldb + 16 * bg0) : (uint32_t)(r0 * p.ldb + 8 * g0) * 2u;
-    const uint32_t astep = (uint32_t)(T / 8 * 2 * p.lda), bstep = Q ? (uint32_t)(T / 4 * p.ldb) : (uint32_t)(T / 8 * 2 * p.ldb);
+    // byte offsets of this thread's loads within a stage; rows past the edge are out of range for good
+    uint32_t ao[AI], bo[BI];
+#pragma unroll
+    for (int c = 0; c < AI; ++c)
+        ao[c] = r0 + c * (T / 8) < irows ? (uint32_t)((r0 + c * (T / 8)) * p.lda + 8 * g0) * 2u : kOOB;
+#pragma unroll
+    for (int c = 0; c < BI; ++c)
+        bo[c] = br0 + c * (T / BG) < jrows ? (uint32_t)((br0 + c * (T / BG)) * p.ldb + (Q ? 16 * bg0 : 8 * bg0)) * (Q ? 1u : 2u) : kOOB;
     const int nst = (int)((len + kTK - 1) / kTK);
-    auto issue = [&](int st) {
+    const int nfull = (int)(len / kTK);
+    // A whole stage costs a load instruction and its scalar offset each (address arithmetic in the vector unit
+    // would run while no wavefront multiplies: the barrier has just lined them up); the last, partial stage
+    // masks the granules past the contraction's end.
+    auto issue = [&](int st) __attribute__((always_inline)) {
         uint8_t* la = lds + (st % NB) * (AS + BS);
         uint8_t* lb = la + AS;
-        const bool ok = (int64_t)st * kTK + 8 * g0 < len;
-        const bool bok = Q ? (int64_t)st * kTK + 16 * bg0 < len : ok;
-        const uint32_t k0 = (uint32_t)st * (kTK * 2), kb0 = Q ? (uint32_t)st * kTK : k0;
-        // (mask arithmetic, so that the compiler keeps one load per slot rather than branching around two)
+        const int ka = st * (kTK * 2), kb = Q ? st * kTK : ka;
+        const uint32_t off_a = st < nfull || st * kTK + 8 * g0 < (int)len ? 0u : kOOB;
+        const uint32_t off_b = st < nfull || st * kTK + (Q ? 16 : 8) * bg0 < (int)len ? 0u : kOOB;
+        if (st < nfull) {
 #pragma unroll
-        for (int c = 0; c < AI; ++c) {
-            const uint32_t bad = 0u - (uint32_t)!(ok && r0 + c * (T / 8) < irows);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr)(la + (c * T + wave * 64) * 16), 16,
-                                                     ((ao + (uint32_t)c * astep + k0) & ~bad) | (kOOB & bad), 0, 0, 0);
-        }
+            for (int c = 0; c < AI; ++c)
+                load_lds(ar, la + (c * T + wave * 64) * 16, ao[c], ka);
 #pragma unroll
-        for (int c = 0; c < BI; ++c) {
-            const uint32_t bad = 0u - (uint32_t)!(bok && br0 + c * (T / BG) < jrows);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_ptr)(lb + (c * T + wave * 64) * 16), 16,
-                                                     ((bo + (uint32_t)c * bstep + kb0) & ~bad) | (kOOB & bad), 0, 0, 0);
+            for (int c = 0; c < BI; ++c)
+                load_lds(br, lb + (c * T + wave * 64) * 16, bo[c], kb);
+        } else {
+#pragma unroll
+            for (int c = 0; c < AI; ++c)
+                load_lds(ar, la + (c * T + wave * 64) * 16, ao[c] | off_a, ka);
+#pragma unroll
+            for (int c = 0; c < BI; ++c)
+                load_lds(br, lb + (c * T + wave * 64) * 16, bo[c] | off_b, kb);
         }
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
@@ -481,7 +499,7 @@ NtKind nt_kind(int per_cu, double stage, double busy)
 }
 // (two 256 x 256 forms: wavefronts of 64 x 128 write longer row pieces, those of 128 x 64 are 3% faster in long
 // contractions; the choice between them is by L)
-const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2>(1, 1.75, 1.70), nt_kind<2, 2, 2, 2, false, 2>(2, 0.85, 0.70), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.33),
+const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2>(2, 0.85, 0.70), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.38),
                       nt_kind<2, 2, 1, 1, false, 4>(2, 0.27, 0.21), nt_kind<1, 4, 4, 1, true, 3>(2, 0.75, 0.62),
                       nt_kind<1, 4, 2, 1, true, 4>(2, 0.35, 0.35)};
 int64_t nt_tiles(const NtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
@@ -542,28 +560,31 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
     const int64_t len = min(p.chunk, p.L - l0);
     const int nst = len > 0 ? (int)((len + 63) / 64) : 0;
     const int ig = (int)min((int64_t)AG, (p.I - i0 + 7) / 8), jg = (int)min((int64_t)BG, (p.J - j0 + 7) / 8);
+    uint32_t ao[AI], bo[BI];     // byte offsets of this thread's loads within a stage; columns past the edge are out of range
+#pragma unroll
+    for (int c = 0; c < AI; ++c) {
+        const int s = c * T + tid, r = s / AG, g = (s % AG) ^ turn<TI>(r);
+        ao[c] = g < ig ? (uint32_t)r * (uint32_t)p.lda * 2u + 16u * g : kOOB;
+    }
+#pragma unroll
+    for (int c = 0; c < BI; ++c) {
+        const int s = c * T + tid, r = s / BG, g = (s % BG) ^ turn<TJ>(r);
+        bo[c] = g < jg ? (uint32_t)r * (uint32_t)p.ldb * 2u + 16u * g : kOOB;
+    }
     auto issue = [&](int st) __attribute__((always_inline)) {
         uint8_t* la = lds + (st & 1) * (AS + BS);
         uint8_t* lb = la + AS;
         const int64_t row = l0 + (int64_t)st * 64;
         const int rows = (int)min((int64_t)64, l0 + len - row);
-        // ranges over this stage's rows; the last row ends with its last used granule
+        // ranges over this stage's rows: the last one ends with its last used granule, rows past it are out of range
         const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + row * p.lda + i0), 0, (int)((rows - 1) * p.lda * 2 + 16 * ig), 0x00020000);
         const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + row * p.ldb + j0), 0, (int)((rows - 1) * p.ldb * 2 + 16 * jg), 0x00020000);
 #pragma unroll
-        for (int c = 0; c < AI; ++c) {
-            const int s = c * T + tid, r = s / AG, g = (s % AG) ^ turn<TI>(r);
-            const uint32_t bad = 0u - (uint32_t)!(r < rows && g < ig);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_ptr)(la + (c * T + wave * 64) * 16), 16,
-                                                     (((uint32_t)r * (uint32_t)p.lda * 2u + 16u * g) & ~bad) | (kOOB & bad), 0, 0, 0);
-        }
+        for (int c = 0; c < AI; ++c)
+            load_lds(ar, la + (c * T + wave * 64) * 16, ao[c], 0);
 #pragma unroll
-        for (int c = 0; c < BI; ++c) {
-            const int s = c * T + tid, r = s / BG, g = (s % BG) ^ turn<TJ>(r);
-            const uint32_t bad = 0u - (uint32_t)!(r < rows && g < jg);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_ptr)(lb + (c * T + wave * 64) * 16), 16,
-                                                     (((uint32_t)r * (uint32_t)p.ldb * 2u + 16u * g) & ~bad) | (kOOB & bad), 0, 0, 0);
-        }
+        for (int c = 0; c < BI; ++c)
+            load_lds(br, lb + (c * T + wave * 64) * 16, bo[c], 0);
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
     const int h = lane >> 5, r32 = lane & 31;

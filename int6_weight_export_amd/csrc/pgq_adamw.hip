@@ -23,6 +23,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
@@ -111,6 +112,53 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t block_max_bits)
 // kinds of stream a launch holds: fp32 weights with fp32 or bf16 gradients in every tensor, or any mix
 enum Streams { S_F32 = 0, S_BF16G = 1, S_ANY = 2 };
 
+// Four elements of a lane as they lie in memory: fp32 streams in four words, 16-bit ones in two, codes in one.
+struct Raw {
+    u32x4 w, g, m, v;
+    uint32_t mb, rb;                              // 8 bits: scale bytes
+};
+
+__device__ __forceinline__ u32x4 load4(const void* p, int64_t i, bool wide)
+{
+    if (wide) return __builtin_nontemporal_load((const GLB u32x4*)((const uint32_t*)p + i));
+    const u32x2 q = __builtin_nontemporal_load((const GLB u32x2*)((const uint16_t*)p + i));
+    return u32x4{q[0], q[1], 0, 0};
+}
+// the same element by element, zeros past `live`
+__device__ __forceinline__ u32x4 load4_edge(const void* p, int64_t i, bool wide, int live)
+{
+    u32x4 r = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < live) {
+            if (wide) r[e] = ((const uint32_t*)p)[i + e];
+            else r[e / 2] |= (uint32_t)((const uint16_t*)p)[i + e] << (16 * (e % 2));
+        }
+    return r;
+}
+__device__ __forceinline__ uint32_t load_codes_edge(const void* p, int64_t i, int live)
+{
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < live) r |= (uint32_t)((const uint8_t*)p)[i + e] << (8 * e);
+    return r;
+}
+// element e of four loaded values of a type
+__device__ __forceinline__ float value(const u32x4& r, int e, int32_t dtype)
+{
+    if (dtype == PGQ_F32) {
+        const uint32_t x = r[e];
+        return __builtin_bit_cast(float, x);
+    }
+    const uint16_t h = (uint16_t)(r[e / 2] >> (16 * (e % 2)));
+    return dtype == PGQ_BF16 ? bf16_to_f32(h) : (float)__builtin_bit_cast(_Float16, h);
+}
+__device__ __forceinline__ u32x2 pack_bf16(const float* w)
+{
+    return u32x2{(uint32_t)f32_to_bf16(w[0]) | ((uint32_t)f32_to_bf16(w[1]) << 16), (uint32_t)f32_to_bf16(w[2]) | ((uint32_t)f32_to_bf16(w[3]) << 16)};
+}
+
 template <int BITS, int S>
 __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grads)
 {
@@ -127,92 +175,32 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
     const float step = lr * h.ib1;
     const float keep = 1.0f - lr * d.weight_decay;
     const uint32_t tseed = mix(0x9E3779B1u * (d.id + 1u) + h.seed);
-    const bool w_bf16 = S == S_ANY && d.w_bf16;
+    const int32_t wt = S == S_ANY && d.w_bf16 ? PGQ_BF16 : PGQ_F32;
     const int32_t gt = S == S_F32 ? PGQ_F32 : S == S_BF16G ? PGQ_BF16 : (int32_t)grads.dtype[di - a.first_desc];
     const int64_t base = (int64_t)(tile - d.first_tile) * kTile;
     const int lane4 = ((int)threadIdx.x & 63) * 4, wave = (int)threadIdx.x >> 6;
+    const int64_t first = base + wave * (kGroups * 256) + lane4;
     const bool vec = d.vec && base + kTile <= d.numel && (S != S_ANY || ((uintptr_t)grad & (gt == PGQ_F32 ? 15 : 7)) == 0);
     bool bad = false;
 
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        const int64_t i0 = base + (wave * kGroups + k) * 256 + lane4;
-        const int live = (int)min((int64_t)4, max((int64_t)0, d.numel - i0));
-        float w[4], g[4], m[4], v[4], r[4];
-        uint32_t mb = 0, rb = 0;
-        // ---- load ----
-        if (vec) {
-            if (w_bf16) {
-                const u16x4 q = *(const GLB u16x4*)((const uint16_t*)d.w + i0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = bf16_to_f32(q[e]);
-            } else {
-                const f32x4 q = *(const GLB f32x4*)((const float*)d.w + i0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = q[e];
-            }
-            if (gt == PGQ_F32) {
-                const f32x4 q = *(const GLB f32x4*)((const float*)grad + i0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[e] = q[e];
-            } else {
-                const u16x4 q = *(const GLB u16x4*)((const uint16_t*)grad + i0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[e] = gt == PGQ_BF16 ? bf16_to_f32(q[e]) : (float)__builtin_bit_cast(_Float16, (uint16_t)q[e]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = g[e] = 0.0f;
-                if (e < live) {
-                    w[e] = w_bf16 ? bf16_to_f32(((const uint16_t*)d.w)[i0 + e]) : ((const float*)d.w)[i0 + e];
-                    g[e] = gt == PGQ_F32 ? ((const float*)grad)[i0 + e]
-                           : gt == PGQ_BF16 ? bf16_to_f32(((const uint16_t*)grad)[i0 + e])
-                                            : (float)((const _Float16*)grad)[i0 + e];
-                }
-            }
-        }
-        if (BITS == 8) {
-            uint32_t mc = 0, rc = 0;
-            if (vec) {
-                mc = *(const GLB uint32_t*)((const uint8_t*)d.m + i0);
-                rc = *(const GLB uint32_t*)((const uint8_t*)d.v + i0);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < live) {
-                        mc |= (uint32_t)((const uint8_t*)d.m)[i0 + e] << (8 * e);
-                        rc |= (uint32_t)((const uint8_t*)d.v)[i0 + e] << (8 * e);
-                    }
-            }
-            if (live > 0) {
-                mb = d.m_scale[i0 >> 6];
-                rb = d.v_scale[i0 >> 6];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t c = (mc >> (8 * e)) & 0xFFu;
-                const float q = decode<3>(c & 0x7Fu, mb);
-                m[e] = (c & 0x80u) ? -q : q;
-                r[e] = decode<4>((rc >> (8 * e)) & 0xFFu, rb);
-                v[e] = r[e] * r[e];
-            }
-        } else if (vec) {
-            const f32x4 p = *(const GLB f32x4*)((const float*)d.m + i0);
-            const f32x4 q = *(const GLB f32x4*)((const float*)d.v + i0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) { m[e] = p[e]; v[e] = q[e]; }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                m[e] = v[e] = 0.0f;
-                if (e < live) { m[e] = ((const float*)d.m)[i0 + e]; v[e] = ((const float*)d.v)[i0 + e]; }
-            }
-        }
-        // ---- update ----
+    // one group of 256 elements: from the loaded values to the stores
+    auto update = [&](int64_t i0, const Raw& q, int live, bool whole) __attribute__((always_inline)) {
+        float w[4], m[4], v[4], r[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float gs = h.grad_scale * g[e];
+            w[e] = value(q.w, e, wt);
+            const float g = value(q.g, e, gt);
+            if (BITS == 8) {
+                const uint32_t c = (q.m[0] >> (8 * e)) & 0xFFu;
+                const float x = decode<3>(c & 0x7Fu, q.mb);
+                m[e] = (c & 0x80u) ? -x : x;
+                r[e] = decode<4>((q.v[0] >> (8 * e)) & 0xFFu, q.rb);
+                v[e] = r[e] * r[e];
+            } else {
+                m[e] = value(q.m, e, PGQ_F32);
+                v[e] = value(q.v, e, PGQ_F32);
+            }
+            const float gs = h.grad_scale * g;
             const float m1 = m[e] * h.beta1 + gs * h.c1;
             const float v1 = v[e] * h.beta2 + (gs * gs) * h.c2;
             const float root = sqrtf(v1);
@@ -224,20 +212,18 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
             if (BITS == 8) r[e] = ok ? root : r[e];
             else v[e] = ok ? v1 : v[e];
         }
-        // ---- store ----
-        if (vec) {
-            if (w_bf16) {
-                *(GLB u16x4*)((uint16_t*)d.w + i0) = u16x4{f32_to_bf16(w[0]), f32_to_bf16(w[1]), f32_to_bf16(w[2]), f32_to_bf16(w[3])};
+        if (whole) {
+            if (wt == PGQ_BF16) {
+                *(GLB u32x2*)((uint16_t*)d.w + i0) = pack_bf16(w);
             } else {
-                *(GLB f32x4*)((float*)d.w + i0) = f32x4{w[0], w[1], w[2], w[3]};
-                if (d.copy)
-                    *(GLB u16x4*)(d.copy + i0) = u16x4{f32_to_bf16(w[0]), f32_to_bf16(w[1]), f32_to_bf16(w[2]), f32_to_bf16(w[3])};
+                __builtin_nontemporal_store(f32x4{w[0], w[1], w[2], w[3]}, (GLB f32x4*)((float*)d.w + i0));
+                if (d.copy) *(GLB u32x2*)(d.copy + i0) = pack_bf16(w);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (e < live) {
-                    if (w_bf16) ((uint16_t*)d.w)[i0 + e] = f32_to_bf16(w[e]);
+                    if (wt == PGQ_BF16) ((uint16_t*)d.w)[i0 + e] = f32_to_bf16(w[e]);
                     else ((float*)d.w)[i0 + e] = w[e];
                     if (d.copy) d.copy[i0 + e] = f32_to_bf16(w[e]);
                 }
@@ -261,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
                 c = r[e] > 0.0f && c == 0 ? 1u : c;
                 rc |= c << (8 * e);
             }
-            if (vec) {
+            if (whole) {
                 *(GLB uint32_t*)((uint8_t*)d.m + i0) = mc;
                 *(GLB uint32_t*)((uint8_t*)d.v + i0) = rc;
             } else {
@@ -276,13 +262,58 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
                 d.m_scale[i0 >> 6] = (uint8_t)bm;
                 d.v_scale[i0 >> 6] = (uint8_t)br;
             }
-        } else if (vec) {
-            *(GLB f32x4*)((float*)d.m + i0) = f32x4{m[0], m[1], m[2], m[3]};
-            *(GLB f32x4*)((float*)d.v + i0) = f32x4{v[0], v[1], v[2], v[3]};
+        } else if (whole) {
+            __builtin_nontemporal_store(f32x4{m[0], m[1], m[2], m[3]}, (GLB f32x4*)((float*)d.m + i0));
+            __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (GLB f32x4*)((float*)d.v + i0));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (e < live) { ((float*)d.m)[i0 + e] = m[e]; ((float*)d.v)[i0 + e] = v[e]; }
+        }
+    };
+
+    if (vec) {
+        // every load of the tile first, so that a lane has kGroups groups of all streams in flight
+        Raw q[kGroups];
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t i0 = first + k * 256;
+            q[k].w = load4(d.w, i0, wt == PGQ_F32);
+            q[k].g = load4(grad, i0, gt == PGQ_F32);
+            if (BITS == 8) {
+                q[k].m[0] = __builtin_nontemporal_load((const GLB uint32_t*)((const uint8_t*)d.m + i0));
+                q[k].v[0] = __builtin_nontemporal_load((const GLB uint32_t*)((const uint8_t*)d.v + i0));
+                q[k].mb = ((const GLB uint8_t*)d.m_scale)[i0 >> 6];
+                q[k].rb = ((const GLB uint8_t*)d.v_scale)[i0 >> 6];
+            } else {
+                q[k].m = load4(d.m, i0, true);
+                q[k].v = load4(d.v, i0, true);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) update(first + k * 256, q[k], 4, true);
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < kGroups; ++k) {
+            const int64_t i0 = first + k * 256;
+            const int live = (int)min((int64_t)4, max((int64_t)0, d.numel - i0));
+            Raw q;
+            q.w = load4_edge(d.w, i0, wt == PGQ_F32, live);
+            q.g = load4_edge(grad, i0, gt == PGQ_F32, live);
+            q.mb = q.rb = 0;
+            if (BITS == 8) {
+                q.m[0] = load_codes_edge(d.m, i0, live);
+                q.v[0] = load_codes_edge(d.v, i0, live);
+                if (live > 0) {
+                    q.mb = d.m_scale[i0 >> 6];
+                    q.rb = d.v_scale[i0 >> 6];
+                }
+            } else {
+                q.m = load4_edge(d.m, i0, true, live);
+                q.v = load4_edge(d.v, i0, true, live);
+            }
+            update(i0, q, live, false);
         }
     }
     if (a.status && __ballot(bad) != 0 && ((int)threadIdx.x & 63) == 0) atomicOr(a.status, PGQ_DEV_NONFINITE);
@@ -329,8 +360,8 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_decode_kernel(AdArgs a, Pt
             qr[e] = f32_to_bf16(decode<4>((rc >> (8 * e)) & 0xFFu, rb));
         }
         if (vec) {
-            *(GLB u16x4*)(mo + i0) = qm;
-            *(GLB u16x4*)(ro + i0) = qr;
+            __builtin_nontemporal_store(qm, (GLB u16x4*)(mo + i0));
+            __builtin_nontemporal_store(qr, (GLB u16x4*)(ro + i0));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)

@@ -124,6 +124,12 @@ __device__ __forceinline__ u32x4 load16(const void* p)
     __builtin_memcpy(&v, p, 16);
     return v;
 }
+// the same for values that this call reads once
+__device__ __forceinline__ u32x4 load16_once(const void* p)
+{
+    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
+    return __builtin_nontemporal_load((const GLB any_u32x4*)p);
+}
 __device__ __forceinline__ uint64_t load8(const void* p)
 {
     uint64_t v;
@@ -138,7 +144,7 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) { return (uint32_t
 // padded to 8 elements with zeros.  What is formed once here instead of in every tile: it is small beside X
 // and Y, and its conversion from codes cost the matrix kernel about a sixth of its time.
 constexpr int kDzCols = 256;                   // columns of a dZ unit
-constexpr int kFlat = 256 * 4;                 // granules (8 elements) of a flat unit
+constexpr int kFlat = 256;                     // granules (8 elements) of a flat unit, one a thread
 
 struct Prep {
     pgq_linear_bwd b;            // the sources (codes, scales, x and their strides also in forward)
@@ -164,7 +170,7 @@ __device__ __forceinline__ void unpack2(uint32_t w, float* f)
 template <int E, typename T>
 __device__ __forceinline__ u32x4 load_cols(const T* row, int64_t n, int64_t N)
 {
-    if (n + E <= N) return load16(row + n);
+    if (n + E <= N) return load16_once(row + n);
     u32x4 v = {};
     if (n >= N) return v;
     if (N >= E) {
@@ -314,41 +320,38 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
     if (!what) unit -= p.n_what;
     const pgq_linear_bwd& b = p.b;
     const int64_t g = p.Kp / 8, rows = what ? b.N : b.M;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-        const int64_t i = unit * kFlat + c * 256 + threadIdx.x;
-        if (i >= rows * g) return;
-        int64_t r, k;
-        if (rows * g <= 0xFFFFFFFFll) {                       // (a 64-bit division costs as much as the rest)
-            r = (uint32_t)i / (uint32_t)g;
-            k = ((uint32_t)i - (uint32_t)r * (uint32_t)g) * 8;
+    const int64_t i = unit * kFlat + threadIdx.x;
+    if (i >= rows * g) return;
+    int64_t r, k;
+    if (rows * g <= 0xFFFFFFFFll) {                       // (a 64-bit division costs as much as the rest)
+        r = (uint32_t)i / (uint32_t)g;
+        k = ((uint32_t)i - (uint32_t)r * (uint32_t)g) * 8;
+    } else {
+        r = i / g;
+        k = i % g * 8;
+    }
+    u32x4 o;
+    if (what) {
+        const float s = f16_to_f32(b.scales[r]);
+        const int8_t* src = b.codes + r * b.ldc + k;
+        int8_t q[8] = {};
+        if (k + 8 <= b.K) {
+            const uint64_t v = load8(src);
+            __builtin_memcpy(q, &v, 8);
         } else {
-            r = i / g;
-            k = i % g * 8;
-        }
-        u32x4 o;
-        if (what) {
-            const float s = f16_to_f32(b.scales[r]);
-            const int8_t* src = b.codes + r * b.ldc + k;
-            int8_t q[8] = {};
-            if (k + 8 <= b.K) {
-                const uint64_t v = load8(src);
-                __builtin_memcpy(q, &v, 8);
-            } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int8_t v = src[min((int64_t)e, b.K - 1 - k)];
-                    q[e] = k + e < b.K ? v : (int8_t)0;
-                }
+            for (int e = 0; e < 8; ++e) {
+                const int8_t v = src[min((int64_t)e, b.K - 1 - k)];
+                q[e] = k + e < b.K ? v : (int8_t)0;
             }
-            // padding is 0 whatever the scale is
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pk_bf16(k + 2 * e < b.K ? (float)q[2 * e] * s : 0.0f, k + 2 * e + 1 < b.K ? (float)q[2 * e + 1] * s : 0.0f);
-            *(GLB u32x4*)(p.what + r * p.Kp + k) = o;
-        } else {
-            o = load_cols<8>(b.x + r * b.ldx, k, b.K);
-            *(GLB u32x4*)(p.xc + r * p.Kp + k) = o;
         }
+        // padding is 0 whatever the scale is
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pk_bf16(k + 2 * e < b.K ? (float)q[2 * e] * s : 0.0f, k + 2 * e + 1 < b.K ? (float)q[2 * e + 1] * s : 0.0f);
+        *(GLB u32x4*)(p.what + r * p.Kp + k) = o;
+    } else {
+        o = load_cols<8>(b.x + r * b.ldx, k, b.K);
+        *(GLB u32x4*)(p.xc + r * p.Kp + k) = o;
     }
 }
 

@@ -354,6 +354,87 @@ def test_large_sampled_rows():
     within(got["dbias"][cols], *want["dbias"], "dbias")
 
 
+def test_contractions_and_strides_past_the_matrix_kernels():
+    """Rows of 2^21 elements and more (32-bit byte offsets within a tile end there), and row strides that
+    long: against 64-bit products on the device, bounds as in linear_ref."""
+    say("linear with K, N or strides of 2^21 and more")
+    big = (1 << 21) + 24
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def rand(*s, std=1.0):
+        return (torch.randn(*s, generator=g, device="cuda") * std).bfloat16()
+
+    def layer(N, K):
+        codes = torch.randint(-31, 32, (N, K), generator=g, device="cuda", dtype=torch.int8)
+        scales = torch.rand(N, generator=g, device="cuda").half() * 0.01 + 0.001
+        return codes, scales, (codes.float() * scales.float()[:, None]).bfloat16().double()
+
+    def near(got, a, b, L, half_step):
+        want, mag = a @ b, a.abs() @ b.abs()
+        bound = (L + 1) * ref.U * mag
+        bound = bound + half_step * (want.abs() + bound) + 2.0 ** -133
+        assert bool(((got.double() - want).abs() <= bound).all())
+
+    for M in (2, 66):                                      # few-token kernel; element-load kernel
+        codes, scales, w = layer(3, big)
+        x = rand(M, big)
+        near(ops.qlinear(x, codes, scales, out_dtype=torch.float32), x.double(), w.t(), big, ref.U)
+        del x
+    x, dy = rand(3, big), rand(3, 3)
+    got = ops.qlinear_backward(dy, codes, scales, x=x, want_dbias=True)
+    near(got["dx"], dy.double(), w, 3, 2.0 ** -8)
+    near(got["dw"], dy.double().t(), x.double(), 3, 2.0 ** -8)
+    codes, scales, w = layer(big, 5)
+    x, dy = rand(2, 5), rand(2, big)
+    got = ops.qlinear_backward(dy, codes, scales, x=x, want_dbias=True)
+    near(got["dx"], dy.double(), w, big, 2.0 ** -8)
+    near(got["dw"], dy.double().t(), x.double(), 2, 2.0 ** -8)
+    assert torch.allclose(got["dbias"], dy.float().sum(0), rtol=1e-6, atol=0)
+    # row strides: X in a buffer of rows 2^21 + 24 apart, 70 rows; codes and dY likewise
+    wide = torch.full((70, big), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x = wide[:, 8:72]
+    x.copy_(rand(70, 64))
+    cwide = torch.zeros((40, big), dtype=torch.int8, device="cuda")
+    codes, scales, w = layer(40, 64)
+    cwide[:, 16:80] = codes
+    y = ops.qlinear(x, cwide[:, 16:80], scales, out_dtype=torch.float32)
+    near(y, x.double(), w.t(), 64, ref.U)
+    dwide = torch.full((70, big), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dy = dwide[:, 64:104]
+    dy.copy_(rand(70, 40))
+    got = ops.qlinear_backward(dy, cwide[:, 16:80], scales, x=x)
+    torch.cuda.synchronize()
+    near(got["dx"], dy.double(), w, 40, 2.0 ** -8)
+    near(got["dw"], dy.double().t(), x.double(), 70, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 96, 4096), (96, 64, 8192), (300, 48, 4160), (640, 4096, 1024), (2048, 1024, 520),
+                                   (4096, 1536, 512), (8192, 264, 96)])
+def test_every_tile_and_its_parts(M, N, K):
+    """Sizes that the plan gives to each tile, from codes and from laid-out weights (K not a multiple of 16), whole
+    and in parts: the outputs sampled, in both types."""
+    say(f"linear tiles {M}x{N}x{K}")
+    codes, scales, w = weights(N, K, M)
+    x = randn((M, K), 5, torch.bfloat16)
+    r = randn((M, N), 6, torch.float32)
+    b = randn((1, N), 7, torch.bfloat16)[0]
+    rows = np.unique(np.r_[0:3, M // 2:M // 2 + 3, M - 3:M, np.arange(0, M, max(1, M // 40))])
+    for y, res in (("f32", r), ("bf16", None)):
+        got, z = ops.qlinear(x, codes, scales, bias=b, act="silu", residual=res, want_z=True, out_dtype=T[y])
+        torch.cuda.synchronize()
+        zr, ez, yr, ey = ref.forward(f64(x)[rows], w, f64(b), "silu", 0.0, None if res is None else f64(res)[rows], y)
+        within(z[rows], zr, ez, "z")
+        within(got[rows], yr, ey, "y")
+    dy = randn((M, N), 8, torch.bfloat16, std=0.1)
+    got = ops.qlinear_backward(dy, codes, scales, x=x, dx_dtype=torch.float32, dw_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want = ref.backward(f64(dy)[rows], None, f64(x)[rows], w, dx="f32", dw="f32")
+    within(got["dx"][rows], *want["dx"], "dx")
+    cols = np.unique(np.r_[0:2, N // 2, N - 2:N, np.arange(0, N, max(1, N // 20))])
+    want = ref.backward(f64(dy)[:, cols], None, f64(x), w[cols], dx="f32", dw="f32")
+    within(got["dw"][cols], *want["dw"], "dw")
+
+
 def test_wrapper_refusals():
     say("linear wrappers refuse wrong operands")
     codes, scales, _ = weights(8, 16, 1)

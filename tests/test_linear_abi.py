@@ -77,3 +77,34 @@ def test_null_descriptors_and_empty_calls():
     nothing = bwd(dx=None, dw=None, dbias=None)
     assert pgq.pgq_linear_backward(ctypes.byref(nothing), None, 0, None) == pgq.PGQ_OK
     assert pgq.pgq_linear_backward_workspace(ctypes.byref(nothing), ctypes.byref(n)) == pgq.PGQ_OK and n.value == 0
+
+
+def test_packed_descriptors_match_the_structs():
+    """The wrappers pack descriptors with struct; the layout has to be the C structs'."""
+    import struct as st
+
+    for fmt, cls in (("15q4ifi", pgq.pgq_linear_fwd), ("18q4ifi", pgq.pgq_linear_bwd)):
+        assert st.calcsize(fmt) == ctypes.sizeof(cls)
+        names = [n for n, _ in cls._fields_]
+        vals = [i + 1 if n != "slope" else 0.5 for i, n in enumerate(names)]
+        p = cls.from_buffer_copy(st.pack(fmt, *vals))
+        for n, v in zip(names, vals):
+            got = getattr(p, n)
+            assert got == v, n
+    src = open(__import__("os").path.join(__import__("os").path.dirname(pgq.LIB_PATH), "ops.py")).read()
+    assert 'struct.Struct("15q4ifi")' in src and 'struct.Struct("18q4ifi")' in src
+
+
+def test_workspace_is_required_when_the_call_needs_one():
+    n = ctypes.c_size_t(0)
+    p = fwd(M=4096, N=1024, K=520, ldx=520, ldc=520, ldy=1024)
+    assert pgq.pgq_linear_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == pgq.PGQ_OK and n.value > 0
+    assert pgq.pgq_linear_forward(ctypes.byref(p), None, 0, None) == pgq.PGQ_ERR_WORKSPACE
+    assert pgq.pgq_linear_forward(ctypes.byref(p), FAKE, n.value - 1, None) == pgq.PGQ_ERR_WORKSPACE
+    assert pgq.pgq_linear_forward(ctypes.byref(p), FAKE + 64, n.value, None) == pgq.PGQ_ERR_ALIGN
+    b = bwd(M=512)
+    assert pgq.pgq_linear_backward_workspace(ctypes.byref(b), ctypes.byref(n)) == pgq.PGQ_OK and n.value > 0
+    assert pgq.pgq_linear_backward(ctypes.byref(b), None, 0, None) == pgq.PGQ_ERR_WORKSPACE
+    assert pgq.pgq_linear_backward(ctypes.byref(b), FAKE + 8, n.value, None) == pgq.PGQ_ERR_ALIGN
+    # few tokens need none
+    assert pgq.pgq_linear_forward_workspace(ctypes.byref(fwd(M=1)), ctypes.byref(n)) == pgq.PGQ_OK and n.value == 0

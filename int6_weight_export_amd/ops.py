@@ -559,6 +559,14 @@ def _same_device(tensors: Sequence[Optional[torch.Tensor]], device) -> None:
             raise ValueError(f"a tensor is on {t.device}, expected {device}")
 
 
+def _separate(tensors: Sequence[Optional[torch.Tensor]]) -> None:
+    """Tensors that one launch writes: dense, and no two of them in the same memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t is not None and t.numel())
+    for (_, end), (start, _) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError("two of the weights, copies and states share memory")
+
+
 def _dense(name: str, t: torch.Tensor, numel: int, dtypes) -> None:
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name}: {numel} dense values expected")
@@ -611,6 +619,7 @@ class AdamW:
                 w.data_ptr(), 0 if c is None else c.data_ptr(), s[0].data_ptr(), s[1].data_ptr(),
                 s[2].data_ptr() if state_bits == 8 else 0, s[3].data_ptr() if state_bits == 8 else 0, k,
                 _dtype_code(w.dtype), pgq.PGQ_F32, per[0][i], per[1][i])
+        _separate([*self.weights, *self.copies, *(t for s in self.states for t in s)])
         need = ctypes.c_size_t(0)
         pgq.check(pgq.pgq_adamw_workspace(self._arr, n, ctypes.byref(need)), "pgq_adamw_workspace")
         self.workspace = torch.empty(max(need.value, 64), dtype=torch.uint8, device=self.device)
@@ -644,10 +653,13 @@ class AdamW:
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
              device_hyper: bool = False) -> None:
-        """One update from the gradients (fp32, bf16 or fp16, dense).  device_hyper: take the constants that load_hyper wrote instead of counting
-        this step here."""
+        """One update from the gradients (fp32, bf16 or fp16, dense).  device_hyper: take the constants that
+        load_hyper wrote instead of counting this step here; a captured step needs it, since a graph would
+        repeat one step's constants."""
         if len(grads) != self.n:
             raise ValueError(f"{len(grads)} gradients for {self.n} weights")
+        if not device_hyper and torch.cuda.is_current_stream_capturing():
+            raise pgq.PgqError(pgq.PGQ_ERR_PARAM, "a captured step takes its constants from the device (device_hyper=True)")
         ptrs, numel, types, index = self._ptrs, self._numel, self._g_dtypes, self._index
         for i, g in enumerate(grads):
             if g.numel() != numel[i] or not g.is_contiguous():

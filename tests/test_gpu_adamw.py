@@ -315,3 +315,22 @@ def test_wrapper_refusals():
                 lambda: opt.step([w], lr=float("nan"))):
         with pytest.raises((ValueError, TypeError, pgq.PgqError)):
             bad()
+
+
+def test_shared_memory_and_captured_constants_refused():
+    say("adamw: the same weight twice, overlapping views, a captured step with host constants")
+    w = torch.zeros(1000, device="cuda")
+    c = torch.zeros(1000, dtype=torch.bfloat16, device="cuda")
+    for weights, copies in (([w, w], None), ([w[:600], w[500:]], None), ([w, w.clone()], [c, c])):
+        with pytest.raises(ValueError, match="share"):
+            ops.AdamW(weights, copies=copies)
+    opt = ops.AdamW([w[:500], w[500:]], lr=0.1)
+    grads = [torch.ones(500, device="cuda") for _ in range(2)]
+    opt.step(grads)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(pgq.PgqError, match="device_hyper"):
+            opt.step(grads)
+        opt.step(grads, device_hyper=True)
+    assert opt.step_count == 1
+    torch.cuda.synchronize()

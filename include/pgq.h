@@ -304,7 +304,8 @@ pgq_status pgq_qgemm_bf16_ybf16(const uint16_t* x, int64_t M, int64_t K, int64_t
 /* same inputs gives the same bits.                                                            */
 /* The gradient of the weights is the straight-through one: of the bf16 weights, zeroed where   */
 /* the fake-quant mask bit is 0 (pgq_fq_tensor.mask); that of the residual is dY itself.       */
-/* NaN and infinities follow the arithmetic; a masked weight's gradient is +0 whatever they are. */
+/* NaN and infinities follow the arithmetic (relu of -infinity with slope 0 is NaN); a masked      */
+/* weight's gradient is +0 whatever they are.                                                  */
 /* ------------------------------------------------------------------------------------------ */
 
 #define PGQ_ACT_NONE  0
@@ -364,7 +365,10 @@ pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* worksp
 /* workspace: device memory of at least that many bytes, 256-byte aligned (NULL when 0); its content
  * is of no account before and after the call, and calls that run at the same time need one each.
  * p is read during the call only.  M = 0 or N = 0 writes no Y; K = 0 makes Z the bias.  In backward
- * an empty sum (N = 0 for dX, M = 0 for dW and db) is +0.  May be recorded into a HIP graph. */
+ * an empty sum (N = 0 for dX, M = 0 for dW and db) is +0.  May be recorded into a HIP graph.
+ * What a call writes may share no memory with its other arguments (y as its own residual apart):
+ * PGQ_ERR_PARAM, also for matrices of different row strides whose ranges of memory meet.  Columns of
+ * one buffer, with its row stride, are distinct memory. */
 pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t workspace_bytes, void* stream);
 pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "pgq_desc.h"
 #include "../../include/pgq.h"
 
 namespace pgq {
@@ -31,6 +32,13 @@ __device__ __forceinline__ float act_slope(int32_t act, float slope, float z)
     }
     const float d = z > 0.0f ? 1.0f : slope;
     return act == PGQ_ACT_RELU ? d : 2.0f * z * d * d;
+}
+
+// One launch of a linear grid; one past the runtime's limits (2^31 - 1 workgroups, 2^32 - 1 threads) is an error.
+inline hipError_t launch_grid(const void* fn, int64_t grid, int block, void** args, void* stream)
+{
+    if (grid > 0x7FFFFFFF || grid * block > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    return launch_plain(fn, dim3((unsigned)grid), dim3((unsigned)block), args, stream);
 }
 
 // What a product does with its sums on the way out: v = act(sum + bias) + residual, Z stored on the side.

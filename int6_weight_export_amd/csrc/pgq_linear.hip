@@ -305,7 +305,7 @@ __device__ __forceinline__ void prep_what_t(const Prep& p, int64_t unit, uint16_
 
 __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
 {
-    __shared__ __align__(16) float lds[8 * kDzCols];           // 8 KB; the transpose needs 9 KB as halves
+    __shared__ __align__(16) float lds[8 * kDzCols];
     __shared__ __align__(16) uint16_t tr[64 * 72];
     int64_t unit = blockIdx.x;
     if (unit < p.n_dz) {
@@ -378,19 +378,18 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
 #pragma unroll
     for (int i = 0; i < MB; ++i) xrow[i] = f.x + min((int64_t)(16 * i + r), f.M - 1) * f.ldx + 16 * q;
     const float s = f.K > 0 ? f16_to_f32(f.scales[n]) : 0.0f;
-    const float s128 = -128.0f * s;                       // exact
     f32x4 acc[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[i] = f32x4{};
-    auto multiply = [&](u32x4 c, const u32x4 (*x)[2]) __attribute__((always_inline)) {
-        // u = code + 128: fma(u, s, -128 s) = code * s exactly (at most 7 + 11 significant bits), then bf16
-        float v[16];
+    auto multiply = [&](u32x4 c, const u32x4 (*x)[2], int left = 16) __attribute__((always_inline)) {
+        float v[16];                                      // code * s exactly (at most 7 + 11 significant bits)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t u = c[w] ^ 0x80808080u;
+        for (int w = 0; w < 4; ++w)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * w + e] = __builtin_fmaf((float)((u >> (8 * e)) & 0xFFu), s, s128);
-        }
+            for (int e = 0; e < 4; ++e) {
+                v[4 * w + e] = (float)(int8_t)(c[w] >> (8 * e)) * s;
+                if (4 * w + e >= left) v[4 * w + e] = 0.0f;        // (0 * s is NaN for an infinite s)
+            }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const u32x4 a = {pk_bf16(v[8 * t], v[8 * t + 1]), pk_bf16(v[8 * t + 2], v[8 * t + 3]),
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
         u32x4 xv[MB][2];
 #pragma unroll
         for (int i = 0; i < MB; ++i) { xv[i][0] = x[i].v[0]; xv[i][1] = x[i].v[1]; }
-        multiply(c.v, xv);
+        multiply(c.v, xv, left);
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i) sums[wave][i][lane] = acc[i];
@@ -470,6 +469,32 @@ bool act_ok(int32_t act, float slope)
     return (act == PGQ_ACT_RELU || act == PGQ_ACT_RELU2) && slope - slope == 0.0f;
 }
 
+// The bytes of a matrix argument.  clash: two of them share a byte, or might: rows of different strides in
+// one range of memory are not told apart.
+struct Span {
+    const void* at;
+    int64_t rows, width, ld;             // width and row stride in bytes
+};
+bool clash(const Span& a, const Span& b)
+{
+    if (!a.at || !b.at || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const uintptr_t a0 = (uintptr_t)a.at, b0 = (uintptr_t)b.at;
+    const uintptr_t a1 = a0 + (uintptr_t)(a.rows - 1) * (uintptr_t)a.ld + (uintptr_t)a.width;
+    const uintptr_t b1 = b0 + (uintptr_t)(b.rows - 1) * (uintptr_t)b.ld + (uintptr_t)b.width;
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.ld != b.ld) return true;
+    const int64_t d = (int64_t)(b0 - a0) % a.ld, at = d < 0 ? d + a.ld : d;       // columns of one buffer
+    return at < a.width || at + b.width > a.ld;
+}
+// one of the outputs (the first n_out spans) shares memory with another span
+bool any_clash(const Span* s, int n_out, int n)
+{
+    for (int i = 0; i < n_out; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (clash(s[i], s[j])) return true;
+    return false;
+}
+
 pgq_status check_fwd(const pgq_linear_fwd* p)
 {
     if (!p) return PGQ_ERR_NULL;
@@ -487,9 +512,16 @@ pgq_status check_fwd(const pgq_linear_fwd* p)
         (p->bias && !is_aligned(p->bias, float_size(p->bias_dtype))) ||
         (p->residual && !is_aligned(p->residual, float_size(p->residual_dtype))))
         return PGQ_ERR_ALIGN;
-    // the residual may be y itself; any other reading of memory that the call writes is refused
-    if (p->residual == p->y && (p->ldr != p->ldy || p->residual_dtype != p->y_dtype)) return PGQ_ERR_PARAM;
-    return PGQ_OK;
+    const int64_t ye = (int64_t)float_size(p->y_dtype), re = (int64_t)float_size(p->residual_dtype);
+    const bool in_place = p->residual == p->y && p->ldr == p->ldy && p->residual_dtype == p->y_dtype;
+    const Span spans[] = {{p->y, M, N * ye, p->ldy * ye},
+                          {p->z, M, N * 2, p->ldz * 2},
+                          {p->x, M, K * 2, p->ldx * 2},
+                          {p->codes, N, K, p->ldc},
+                          {p->scales, K > 0, N * 2, N * 2},
+                          {p->bias, 1, N * (int64_t)float_size(p->bias_dtype), N * 4},
+                          {in_place ? nullptr : p->residual, M, N * re, p->ldr * re}};
+    return any_clash(spans, 2, 7) ? PGQ_ERR_PARAM : PGQ_OK;
 }
 
 pgq_status check_bwd(const pgq_linear_bwd* p)
@@ -513,7 +545,17 @@ pgq_status check_bwd(const pgq_linear_bwd* p)
         (p->dx && !is_aligned(p->dx, float_size(p->dx_dtype))) || (p->dw && !is_aligned(p->dw, float_size(p->dw_dtype))) ||
         (p->dbias && !is_aligned(p->dbias, 4)))
         return PGQ_ERR_ALIGN;
-    return PGQ_OK;
+    const int64_t ge = (int64_t)float_size(p->dy_dtype), xe = (int64_t)float_size(p->dx_dtype), we = (int64_t)float_size(p->dw_dtype);
+    const Span spans[] = {{p->dx, M, K * xe, p->lddx * xe},
+                          {p->dw, N, K * we, p->lddw * we},
+                          {p->dbias, 1, N * 4, N * 4},
+                          {p->dy, M, N * ge, p->lddy * ge},
+                          {act ? p->z : nullptr, M, N * 2, p->ldz * 2},
+                          {p->dw ? p->x : nullptr, M, K * 2, p->ldx * 2},
+                          {p->dx ? p->codes : nullptr, N, K, p->ldc},
+                          {p->dx ? p->scales : nullptr, 1, N * 2, N * 2},
+                          {p->dw ? p->mask : nullptr, N, (K + 7) / 8, (K + 7) / 8}};
+    return any_clash(spans, 3, 9) ? PGQ_ERR_PARAM : PGQ_OK;
 }
 
 int64_t tiles_of(int64_t I, int64_t J) { return ((I + kGT - 1) / kGT) * ((J + kGT - 1) / kGT); }
@@ -635,7 +677,7 @@ struct Launches {
     void go(const void* fn, int64_t grid, int block, void** args)
     {
         if (!next()) return;
-        e = grid > 0x7FFFFFFF ? hipErrorInvalidValue : launch_plain(fn, dim3((unsigned)grid), dim3((unsigned)block), args, stream);
+        e = launch_grid(fn, grid, block, args, stream);
     }
     pgq_status done() const { return e == hipSuccess ? PGQ_OK : (pgq_status)note_hip_error(e); }
 };

@@ -209,17 +209,15 @@ __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 // in registers right before it multiplies: for few tile rows, where laying What out first costs more.
 __device__ __forceinline__ int swz4(int r) { return (((r >> 1) & 1) ^ ((r >> 3) & 1)) | (((r >> 2) & 1) << 1); }
 
-// 16 codes -> two fragments of bf16(code * s): with u = code + 128, fma(u, s, -128 s) = code * s exactly (at
-// most 7 + 11 significant bits), then one rounding
-__device__ __forceinline__ void codes_to_bf16(u32x4 q, float s, float s128, bf16x8& lo, bf16x8& hi)
+// 16 codes -> two fragments of bf16(code * s): the product is exact (at most 7 + 11 significant bits)
+__device__ __forceinline__ void codes_to_bf16(u32x4 q, float s, bf16x8& lo, bf16x8& hi)
 {
     u32x4 a, c;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        const uint32_t u = q[w] ^ 0x80808080u;
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf((float)((u >> (8 * e)) & 0xFFu), s, s128);
+        for (int e = 0; e < 4; ++e) v[e] = (float)(int8_t)(q[w] >> (8 * e)) * s;
         u32x4& to = w < 2 ? a : c;
         to[2 * (w & 1)] = pk_bf16(v[0], v[1]);
         to[2 * (w & 1) + 1] = pk_bf16(v[2], v[3]);
@@ -298,13 +296,12 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
     const int r32 = lane & 31, h = lane >> 5;
-    float sc[Q ? JB : 1], sc128[Q ? JB : 1];                 // the scales of this lane's weight rows
+    float sc[Q ? JB : 1];                                    // the scales of this lane's weight rows
     if constexpr (Q) {
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
             const int64_t n = j0 + wj + 32 * j + r32;
             sc[j] = n < p.J ? f16_to_f32(((const GLB uint16_t*)p.scales)[n]) : 0.0f;
-            sc128[j] = -128.0f * sc[j];                      // exact
         }
     }
     f32x16 acc[IB][JB];
@@ -343,12 +340,12 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
             }
         }
     };
-    auto multiply = [&](const Frag& f) __attribute__((always_inline)) {
+    auto multiply = [&](const Frag& f, int l) __attribute__((always_inline)) {
         bf16x8 b[JB][2];
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
-            if constexpr (Q) {
-                codes_to_bf16(__builtin_bit_cast(u32x4, f.b[j][0]), sc[j], sc128[j], b[j][0], b[j][1]);
+            if constexpr (Q) {                               // past the end 0 * 0, whatever the scale is
+                codes_to_bf16(__builtin_bit_cast(u32x4, f.b[j][0]), l + 16 * h < (int)len ? sc[j] : 0.0f, b[j][0], b[j][1]);
             } else {
                 b[j][0] = f.b[j][0];
                 b[j][1] = f.b[j][1];
@@ -376,12 +373,12 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     }
     for (int st = 0; st < nst; ++st) {
         fetch(f1, st, 1);
-        multiply(f0);
+        multiply(f0, st * kTK);
         if (st + NB - 1 < nst) wait_barrier<(NB - 2) * NL>();
         else wait_barrier<0>();
         if (st + NB < nst) issue(st + NB);
         if (st + 1 < nst) fetch(f0, st + 1, 0);
-        if ((int64_t)st * kTK + 32 < len) multiply(f1);
+        if (st * kTK + 32 < (int)len) multiply(f1, st * kTK + 32);
     }
     if (p.splits > 1) {                                       // the part's sums as they lie in the registers
         f32x4* part_out = reinterpret_cast<f32x4*>(p.partial) +
@@ -804,20 +801,18 @@ hipError_t launch_mm_nt(const MmNt& p, void* stream)
 {
     const NtKind& k = kNt[p.kind];
     const int64_t grid = nt_tiles(k, p.I, p.J) * p.splits;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmNt copy = p;
     void* args[] = {&copy};
-    return launch_plain(p.e.y_dtype == PGQ_F32 ? k.f32 : k.bf16, dim3((unsigned)grid), dim3((unsigned)k.threads), args, stream);
+    return launch_grid(p.e.y_dtype == PGQ_F32 ? k.f32 : k.bf16, grid, k.threads, args, stream);
 }
 
 hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream)
 {
     const NtKind& k = kNt[p.kind];
     const int64_t grid = nt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmNt copy = p;
     void* args[] = {&copy};
-    return launch_plain(k.reduce, dim3((unsigned)grid), dim3(256), args, stream);
+    return launch_grid(k.reduce, grid, 256, args, stream);
 }
 
 // The tile and the number of parts with the least estimated time: stages of a part times the rounds its
@@ -927,20 +922,19 @@ hipError_t launch_mm_both(int both, const MmNt& x, const MmTt& w, const Dbias& d
     const BothKind& b = kBoth[both];
     const int64_t nx = nt_tiles(kNt[x.kind], x.I, x.J) * x.splits, nw = tt_tiles(kTt[w.kind], w.I, w.J) * w.splits;
     const int64_t grid = nx + nw + (d.out ? (d.N + 63) / 64 : 0);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmNt cx = x;
     MmTt cw = w;
     Dbias cd = d;
     uint32_t ux = (uint32_t)nx, uw = (uint32_t)nw;
     void* args[] = {&cx, &cw, &cd, &ux, &uw};
-    return launch_plain(x.e.y_dtype == PGQ_F32 ? b.f32 : b.bf16, dim3((unsigned)grid), dim3((unsigned)kNt[x.kind].threads), args, stream);
+    return launch_grid(x.e.y_dtype == PGQ_F32 ? b.f32 : b.bf16, grid, kNt[x.kind].threads, args, stream);
 }
 
 hipError_t launch_mm_dbias(const Dbias& d, void* stream)
 {
     Dbias copy = d;
     void* args[] = {&copy};
-    return launch_plain(reinterpret_cast<const void*>(&pgq_mm_dbias_kernel), dim3((unsigned)((d.N + 63) / 64)), dim3(1024), args, stream);
+    return launch_grid(reinterpret_cast<const void*>(&pgq_mm_dbias_kernel), (d.N + 63) / 64, 1024, args, stream);
 }
 
 size_t mm_tt_partial_bytes(const MmTt& p)
@@ -953,20 +947,18 @@ hipError_t launch_mm_tt(const MmTt& p, void* stream)
 {
     const TtKind& k = kTt[p.kind];
     const int64_t grid = tt_tiles(k, p.I, p.J) * p.splits;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmTt copy = p;
     void* args[] = {&copy};
-    return launch_plain(k.kernel, dim3((unsigned)grid), dim3((unsigned)k.threads), args, stream);
+    return launch_grid(k.kernel, grid, k.threads, args, stream);
 }
 
 hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream)
 {
     const TtKind& k = kTt[p.kind];
     const int64_t grid = tt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4;      // a wavefront: 8 rows of 32 columns
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     MmTt copy = p;
     void* args[] = {&copy};
-    return launch_plain(k.reduce, dim3((unsigned)grid), dim3(256), args, stream);
+    return launch_grid(k.reduce, grid, 256, args, stream);
 }
 
 }  // namespace pgq

@@ -435,6 +435,45 @@ def test_every_tile_and_its_parts(M, N, K):
     within(got["dw"][cols], *want["dw"], "dw")
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 40, 128), (40, 24, 200), (96, 64, 1024), (96, 64, 1040), (700, 264, 152), (64, 96, 2048)])
+def test_infinite_and_nan_scales(M, N, K):
+    """code * infinity is an infinity of the code's sign, NaN for code 0, on every path; a row's neighbours
+    are untouched.  Codes and x of one sign, so that no sum mixes infinities."""
+    say(f"linear infinite scales {M}x{N}x{K}")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(1, 32, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    codes[5] *= -1
+    codes[7, 3] = 0
+    scales = torch.full((N,), 0.01, device="cuda", dtype=torch.float16)
+    clean = (torch.rand(M, K, generator=g, device="cuda") + 0.5).bfloat16()
+    base = ops.qlinear(clean, codes, scales, out_dtype=torch.float32)
+    scales[4], scales[5], scales[6], scales[7] = float("inf"), float("inf"), float("nan"), float("inf")
+    y = ops.qlinear(clean, codes, scales, out_dtype=torch.float32)
+    dx = ops.qlinear_backward(torch.ones(M, N, device="cuda"), codes[:, :16].contiguous(), scales, want_dw=False)["dx"]
+    torch.cuda.synchronize()
+    assert bool((y[:, 4] == float("inf")).all()) and bool((y[:, 5] == -float("inf")).all())
+    assert bool(y[:, 6:8].isnan().all()) and bool(dx.isnan().all())
+    rest = [n for n in range(N) if n not in (4, 5, 6, 7)]
+    assert torch.equal(y[:, rest], base[:, rest])
+
+
+def test_in_place_and_shared_memory():
+    """Y over X is refused; Y and X, and Y and Z, as columns of one buffer are not."""
+    say("linear shared memory")
+    codes, scales, w = weights(64, 64, 2)
+    buf = torch.zeros(100, 192, dtype=torch.bfloat16, device="cuda")
+    x = buf[:, :64]
+    x.copy_(randn((100, 64), 1, torch.bfloat16))
+    with pytest.raises(pgq.PgqError):
+        ops.qlinear(x, codes, scales, out=x)
+    with pytest.raises(pgq.PgqError):
+        ops.qlinear(x, codes, scales, out=buf[:, 63:127])
+    want = ops.qlinear(x.contiguous(), codes, scales)
+    ops.qlinear(x, codes, scales, out=buf[:, 64:128])
+    torch.cuda.synchronize()
+    assert torch.equal(buf[:, 64:128], want) and not bool(buf[:, 128:].any())
+
+
 def test_wrapper_refusals():
     say("linear wrappers refuse wrong operands")
     codes, scales, _ = weights(8, 16, 1)

@@ -97,14 +97,62 @@ def test_packed_descriptors_match_the_structs():
 
 def test_workspace_is_required_when_the_call_needs_one():
     n = ctypes.c_size_t(0)
-    p = fwd(M=4096, N=1024, K=520, ldx=520, ldc=520, ldy=1024)
+    at = {n: FAKE + (i << 32) for i, n in enumerate(("x", "codes", "scales", "y", "dy", "dx", "dw", "dbias"))}
+    p = fwd(M=4096, N=1024, K=520, ldx=520, ldc=520, ldy=1024, **{k: at[k] for k in ("x", "codes", "scales", "y")})
     assert pgq.pgq_linear_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == pgq.PGQ_OK and n.value > 0
     assert pgq.pgq_linear_forward(ctypes.byref(p), None, 0, None) == pgq.PGQ_ERR_WORKSPACE
     assert pgq.pgq_linear_forward(ctypes.byref(p), FAKE, n.value - 1, None) == pgq.PGQ_ERR_WORKSPACE
     assert pgq.pgq_linear_forward(ctypes.byref(p), FAKE + 64, n.value, None) == pgq.PGQ_ERR_ALIGN
-    b = bwd(M=512)
+    b = bwd(M=512, **{k: at[k] for k in at if k != "y"})
     assert pgq.pgq_linear_backward_workspace(ctypes.byref(b), ctypes.byref(n)) == pgq.PGQ_OK and n.value > 0
     assert pgq.pgq_linear_backward(ctypes.byref(b), None, 0, None) == pgq.PGQ_ERR_WORKSPACE
     assert pgq.pgq_linear_backward(ctypes.byref(b), FAKE + 8, n.value, None) == pgq.PGQ_ERR_ALIGN
     # few tokens need none
-    assert pgq.pgq_linear_forward_workspace(ctypes.byref(fwd(M=1)), ctypes.byref(n)) == pgq.PGQ_OK and n.value == 0
+    assert pgq.pgq_linear_forward_workspace(ctypes.byref(fwd(M=1, **{k: at[k] for k in ("x", "codes", "scales", "y")})),
+                                            ctypes.byref(n)) == pgq.PGQ_OK and n.value == 0
+
+
+def _status(p):
+    size = pgq.pgq_linear_forward_workspace if isinstance(p, pgq.pgq_linear_fwd) else pgq.pgq_linear_backward_workspace
+    return size(ctypes.byref(p), ctypes.byref(ctypes.c_size_t(0)))
+
+
+def test_outputs_share_no_memory_with_other_arguments():
+    """4 tokens, 8 outputs, 16 inputs; an output whose bytes meet another argument's is refused."""
+    names = ("x", "codes", "scales", "y", "z", "bias", "residual", "dy", "dx", "dw", "dbias", "mask")
+    at = {n: FAKE + (i << 16) for i, n in enumerate(names)}
+
+    def f(**kw):
+        a = {k: at[k] for k in ("x", "codes", "scales", "y", "z", "bias", "residual")}
+        a.update(ldz=8, ldr=8, bias_dtype=pgq.PGQ_F32, residual_dtype=pgq.PGQ_F32)
+        a.update(kw)
+        return _status(fwd(**a))
+
+    def b(**kw):
+        a = {k: at[k] for k in ("x", "codes", "scales", "z", "dy", "dx", "dw", "dbias", "mask")}
+        a.update(ldz=8, act=pgq.PGQ_ACT_SILU)
+        a.update(kw)
+        return _status(bwd(**a))
+
+    assert f() == pgq.PGQ_OK and b() == pgq.PGQ_OK
+    for k in ("x", "codes", "scales", "z", "bias", "residual"):
+        assert f(y=at[k]) == pgq.PGQ_ERR_PARAM, k
+        if k != "z":
+            assert f(z=at[k]) == pgq.PGQ_ERR_PARAM, k
+    for o in ("dx", "dw", "dbias"):
+        for k in ("x", "codes", "scales", "z", "dy", "dx", "dw", "mask"):
+            if k != o:
+                assert b(**{o: at[k]}) == pgq.PGQ_ERR_PARAM, (o, k)
+    # the last byte of x and the one behind it
+    assert f(y=at["x"] + 4 * 16 * 2 - 2) == pgq.PGQ_ERR_PARAM and f(y=at["x"] + 4 * 16 * 2) == pgq.PGQ_OK
+    # Y in place of its residual; columns of one buffer; the same with one column shared; another stride
+    assert f(residual=at["y"], residual_dtype=pgq.PGQ_BF16) == pgq.PGQ_OK
+    assert f(y=at["x"] + 32, ldx=24, ldy=24) == pgq.PGQ_OK
+    assert f(y=at["x"], x=at["x"] + 16, ldx=24, ldy=24) == pgq.PGQ_OK
+    assert f(y=at["x"] + 30, ldx=24, ldy=24) == pgq.PGQ_ERR_PARAM
+    assert f(y=at["x"], x=at["x"] + 14, ldx=24, ldy=24) == pgq.PGQ_ERR_PARAM
+    assert f(y=at["x"] + 32, ldx=24, ldy=28) == pgq.PGQ_ERR_PARAM
+    # an argument that the call does not use may lie anywhere
+    assert b(dw=None, x=at["dx"], mask=at["dx"]) == pgq.PGQ_OK and b(dx=None, codes=at["dw"], scales=at["dw"]) == pgq.PGQ_OK
+    assert b(act=pgq.PGQ_ACT_NONE, z=at["dx"]) == pgq.PGQ_OK
+    assert _status(fwd(M=0)) == pgq.PGQ_OK

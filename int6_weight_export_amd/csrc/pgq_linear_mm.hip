@@ -226,12 +226,72 @@ __device__ __forceinline__ void codes_to_bf16(u32x4 q, float s, bf16x8& lo, bf16
     hi = __builtin_bit_cast(bf16x8, c);
 }
 
+// In the large tiles the R LDS reads of a half stage go between the M matrix instructions of the half before it: a
+// wavefront issues in order, and reads issued in one piece kept it from multiplying while the LDS worked them off
+// (16384 x 528 x 6336 155 -> 144 us, 8192 x 8448 x 4096 554 -> 535; the small tiles, bound by latency, lose
+// 1 us to the longer code and go without).
+template <int IB, int JB>
+constexpr bool kSpread = IB * JB >= 6;
+template <int R, int M>
+__device__ __forceinline__ void spread()
+{
+    static_assert(R <= 2 * M, "at most two reads to an instruction");
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                          // a matrix instruction
+        const int reads = R * (m + 1) / M - R * m / M;
+        if (reads == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);          // then LDS reads
+        if (reads == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+}
+
+constexpr int kWayOut = 64 + 4;                // floats of a row on its way out, at most
+
 template <int WR, int WC, int IB, int JB, bool Q, int NB>
 constexpr int nt_lds()
 {
     constexpr int stages = NB * (32 * IB * WR * 8 + 32 * JB * WC * (Q ? 4 : 8)) * 16;
-    constexpr int out = WR * WC * 32 * (((JB & (JB - 1)) == 0 ? 32 * JB : 32) + 4) * 4;
+    constexpr int out = WR * WC * 32 * kWayOut * 4;
     return stages > out ? stages : out;
+}
+
+// A wavefront's way out of NJ of its blocks of 32 columns, from block J0 on: row i0.., column j0.. of Y.
+template <int IB, int JB, int J0, int NJ, typename YT>
+__device__ __forceinline__ void way_out(const MmNt& p, const f32x16 (&acc)[IB][JB], float* tl, int64_t i0, int64_t j0, int lane)
+{
+    constexpr int V = sizeof(YT) == 4 ? 4 : 8;
+    constexpr int EP = 32 * NJ + 4;                           // row pitch in LDS, floats
+    static_assert(EP <= kWayOut, "the scratch of a wavefront");
+    constexpr int LPR = 32 * NJ / V;                          // lanes per row
+    constexpr int STEP = 64 / LPR;                            // rows a wavefront covers at once
+    constexpr int G = sizeof(YT) == 4 && STEP <= 8 ? 4 : 2;   // and a lane takes G of those at a time (more spill)
+    static_assert(64 % LPR == 0 && 32 % (STEP * G) == 0, "whole groups");
+    const int h = lane >> 5, r32 = lane & 31;
+    const Out<V, YT> out(p.e, j0 + 32 * J0 + lane % LPR * V, p.J);
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) tl[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + r32] = acc[i][J0 + j][r];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+        for (int q = 0; q < 32; q += STEP * G) {
+            const int rr = q + lane / LPR;
+            float v[G][V];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int u = 0; u < V / 4; ++u) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(tl + (rr + g * STEP) * EP + lane % LPR * V + 4 * u);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) v[g][4 * u + w] = x[w];
+                }
+            const int64_t row = i0 + 32 * i + rr;
+            if (row < p.I && out.col < p.J) out.template rows<G>(row, STEP, p.I, v);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
 }
 
 template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
@@ -242,8 +302,6 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     constexpr int AI = TI * 8 / T, BI = TJ * BG / T;         // load instructions per thread per stage
     constexpr int AS = TI * kTK * 2, BS = TJ * BG * 16;      // bytes per stage
     static_assert(TI * 8 % T == 0 && TJ * BG % T == 0, "whole load instructions");
-    constexpr int CW = (JB & (JB - 1)) == 0 ? 32 * JB : 32;  // columns a wavefront's way out takes at a time
-    constexpr int EP = CW + 4;                               // its row pitch in floats
     const int tid = (int)threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t gi = (uint32_t)((p.I + TI - 1) / TI), gj = (uint32_t)((p.J + TJ - 1) / TJ);
@@ -371,7 +429,21 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
         else wait_barrier<0>();
         fetch(f0, 0, 0);
     }
-    for (int st = 0; st < nst; ++st) {
+    int st = 0;
+    if constexpr (kSpread<IB, JB>) {
+        for (; st + 1 < nst; ++st) {                          // all but the last stage
+            fetch(f1, st, 1);
+            multiply(f0, st * kTK);
+            spread<2 * (IB + JB), 2 * IB * JB>();
+            if (st + NB - 1 < nst) wait_barrier<(NB - 2) * NL>();
+            else wait_barrier<0>();
+            if (st + NB < nst) issue(st + NB);
+            fetch(f0, st + 1, 0);
+            multiply(f1, st * kTK + 32);
+            spread<2 * (IB + JB), 2 * IB * JB>();
+        }
+    }
+    for (; st < nst; ++st) {
         fetch(f1, st, 1);
         multiply(f0, st * kTK);
         if (st + NB - 1 < nst) wait_barrier<(NB - 2) * NL>();
@@ -392,42 +464,11 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
                     part_out[((i * JB + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         return;
     }
-    // out through LDS, 32 rows of CW columns at a time, so that a lane holds consecutive columns
-    constexpr int V = sizeof(YT) == 4 ? 4 : 8;
-    constexpr int LPR = CW / V;                               // lanes per row
-    constexpr int STEP = 64 / LPR;                            // rows a wavefront covers at once
-    constexpr int G = sizeof(YT) == 4 && STEP <= 8 ? 4 : 2;   // and a lane takes G of those at a time (more spill)
-    static_assert(64 % LPR == 0 && 32 % (STEP * G) == 0, "whole groups");
-    float* tl = reinterpret_cast<float*>(lds) + wave * (32 * EP);
+    // out through LDS, 32 rows at a time, so that a lane holds consecutive columns
+    float* tl = reinterpret_cast<float*>(lds) + wave * (32 * kWayOut);
     lds_barrier();
-#pragma unroll
-    for (int jc = 0; jc < 32 * JB / CW; ++jc) {
-        const Out<V, YT> out(p.e, j0 + wj + jc * CW + lane % LPR * V, p.J);
-#pragma unroll
-        for (int i = 0; i < IB; ++i) {
-#pragma unroll
-            for (int j = 0; j < CW / 32; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) tl[(8 * (r >> 2) + 4 * h + (r & 3)) * EP + 32 * j + r32] = acc[i][jc * (CW / 32) + j][r];
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 1
-            for (int q = 0; q < 32; q += STEP * G) {
-                const int rr = q + lane / LPR;
-                float v[G][V];
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int u = 0; u < V / 4; ++u) {
-                        const f32x4 x = *reinterpret_cast<const f32x4*>(tl + (rr + g * STEP) * EP + lane % LPR * V + 4 * u);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) v[g][4 * u + w] = x[w];
-                    }
-                const int64_t row = i0 + wi + 32 * i + rr;
-                if (row < p.I && out.col < p.J) out.template rows<G>(row, STEP, p.I, v);
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        }
-    }
+    way_out<IB, JB, 0, JB == 3 ? 2 : JB, YT>(p, acc, tl, i0 + wi, j0 + wj, lane);
+    if constexpr (JB == 3) way_out<IB, JB, 2, 1, YT>(p, acc, tl, i0 + wi, j0 + wj, lane);
 }
 
 template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
@@ -494,11 +535,11 @@ NtKind nt_kind(int per_cu, double stage, double busy)
             reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, uint16_t>),
             reinterpret_cast<const void*>(&pgq_mm_nt_reduce_kernel<WR, WC, IB, JB>), Q};
 }
-// (two 256 x 256 forms: wavefronts of 64 x 128 write longer row pieces, those of 128 x 64 are 3% faster in long
-// contractions; the choice between them is by L)
+// (256 x 192 beside 256 x 256 for outputs that end shortly behind a multiple of 256: 16384 x 528 x 1584 runs in
+// 41.0 us with it against 46.9, 16384 x 1584 x 528 in 71.3 against 50.1)
 const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2>(2, 0.85, 0.70), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.38),
                       nt_kind<2, 2, 1, 1, false, 4>(2, 0.27, 0.21), nt_kind<1, 4, 4, 1, true, 3>(2, 0.75, 0.62),
-                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.35, 0.35)};
+                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.35, 0.35), nt_kind<4, 2, 2, 3, false, 2>(1, 1.35, 1.27)};
 int64_t nt_tiles(const NtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 // ---- A columns times B columns ----------------------------------------------------------------------
@@ -629,7 +670,20 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
         if (nst > 1) issue(1);
         fetch(f0, 0, 0);
     }
-    for (int st = 0; st < nst; ++st) {
+    int st = 0;
+    if constexpr (kSpread<IB, JB>) {
+        for (; st + 1 < nst; ++st) {                          // all but the last stage
+            fetch(f1, st, 1);
+            multiply(f0);
+            spread<4 * (IB + JB), 2 * IB * JB>();
+            wait_barrier<0>();
+            if (st + 2 < nst) issue(st + 2);
+            fetch(f0, st + 1, 0);
+            multiply(f1);
+            spread<4 * (IB + JB), 2 * IB * JB>();
+        }
+    }
+    for (; st < nst; ++st) {
         fetch(f1, st, 1);
         multiply(f0);
         wait_barrier<0>();
@@ -856,7 +910,8 @@ BothKind both_kind(int nt, int tt, int per_cu, double nt_stage, double tt_stage)
             reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, B0, B1, B2, B3, uint16_t>)};
 }
 const BothKind kBoth[] = {both_kind<2, 4, 4, 2, 2, 4, 2, 2, 4>(0, 0, 1, 1.75, 1.9), both_kind<2, 4, 4, 2, 2, 4, 2, 2, 3>(0, 1, 1, 1.75, 1.5),
-                          both_kind<2, 2, 2, 2, 2, 2, 2, 2, 2>(1, 2, 2, 1.4, 1.1), both_kind<2, 2, 1, 1, 4, 2, 2, 1, 1>(3, 3, 2, 0.45, 0.5)};
+                          both_kind<2, 2, 2, 2, 2, 2, 2, 2, 2>(1, 2, 2, 1.4, 1.1), both_kind<2, 2, 1, 1, 4, 2, 2, 1, 1>(3, 3, 2, 0.45, 0.5),
+                          both_kind<4, 2, 2, 3, 2, 4, 2, 2, 3>(6, 1, 1, 1.40, 1.5)};
 
 // When `first` workgroups of one_first microseconds and then `second` of one_second each, taken in that order by
 // `slots` places, are done: the places free after the first kind's last whole round start at t0, the others at

@@ -362,16 +362,36 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
 // (row lane % 16, k = 8 (lane / 16) .. + 7) and the tokens as B (column lane % 16): lane quarter q supplies
 // k = 16 q + 8 t .. + 7 of a block in instruction t, so that a lane's 16 codes are one load.  Lanes past M
 // or N repeat the last row, whose sums they do not store.
+//
+// A compute unit takes 0.3 us (one token) to 1.9 us (64) for eight blocks, so few weight rows with long K are cut
+// into parts of K: their sums go to scratch and a second launch adds them in order (16 x 256 x 8192 13.2 -> 8.4 us,
+// 19 x 224 x 6176 with rows at odd addresses 29 -> 10).
 constexpr int kSkinnyMost = 64;
 constexpr int kSkinnyWaves = 8;
 
+struct Parts {
+    float* sums;                 // n > 1: n x M x N
+    int64_t blocks;              // 64-wide blocks of K in a part
+    int32_t n;
+};
+
+__device__ __forceinline__ void finish(const pgq_linear_fwd& f, int64_t m, int64_t n, float z)
+{
+    if (f.bias) z += load_any(f.bias, f.bias_dtype, n);
+    if (f.z) f.z[m * f.ldz + n] = f32_to_bf16(z);
+    float y = act_value(f.act, f.slope, z);
+    if (f.residual) y += load_any(f.residual, f.residual_dtype, m * f.ldr + n);
+    store_any(f.y, f.y_dtype, m * f.ldy + n, y);
+}
+
 template <int MB>
-__global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pgq_linear_fwd f)
+__global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pgq_linear_fwd f, Parts parts)
 {
     __shared__ f32x4 sums[kSkinnyWaves][MB][64];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int r = lane & 15, q = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const uint32_t part = blockIdx.x % (uint32_t)parts.n;
+    const int64_t n0 = (int64_t)(blockIdx.x / (uint32_t)parts.n) * 16;
     const int64_t n = min(n0 + r, f.N - 1);
     const int8_t* crow = f.codes + n * f.ldc + 16 * q;
     const uint16_t* xrow[MB];
@@ -399,9 +419,10 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
                 acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, x[i][t]), acc[i], 0, 0, 0);
         }
     };
-    const int64_t full = f.K / 64;
+    const bool last = part + 1 == (uint32_t)parts.n;
+    const int64_t full = last ? f.K / 64 : (part + 1) * parts.blocks;       // one past this part's whole blocks
     constexpr int U = MB == 1 ? 8 : MB == 2 ? 4 : 2;      // blocks whose loads are in flight together
-    int64_t kb = wave;
+    int64_t kb = part * parts.blocks + wave;
     for (; kb + (int64_t)(U - 1) * kSkinnyWaves < full; kb += (int64_t)U * kSkinnyWaves) {
         u32x4 c[U], x[U][MB][2];
 #pragma unroll
@@ -423,7 +444,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
         for (int i = 0; i < MB; ++i) { x[i][0] = load16(xrow[i] + k); x[i][1] = load16(xrow[i] + k + 8); }
         multiply(c, x);
     }
-    if (f.K % 64 && kb == full) {                         // the last block, element by element past K
+    if (last && f.K % 64 && kb == full) {                 // the last block, element by element past K
         const int64_t k = full * 64;
         const int left = (int)max((int64_t)0, min((int64_t)16, f.K - k - 16 * q));
         union { u32x4 v; uint8_t b[16]; } c = {};
@@ -451,12 +472,20 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) pgq_linear_skinny_kernel(pg
         float z = sums[0][i][l][e];
 #pragma unroll
         for (int w = 1; w < kSkinnyWaves; ++w) z += sums[w][i][l][e];
-        if (f.bias) z += load_any(f.bias, f.bias_dtype, nn);
-        if (f.z) f.z[m * f.ldz + nn] = f32_to_bf16(z);
-        float y = act_value(f.act, f.slope, z);
-        if (f.residual) y += load_any(f.residual, f.residual_dtype, m * f.ldr + nn);
-        store_any(f.y, f.y_dtype, m * f.ldy + nn, y);
+        if (parts.n > 1) parts.sums[(part * f.M + m) * f.N + nn] = z;
+        else finish(f, m, nn, z);
     }
+}
+
+__global__ void __launch_bounds__(256) pgq_linear_join_kernel(pgq_linear_fwd f, Parts parts)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, mn = f.M * f.N;
+    if (at >= mn) return;
+    const GLB float* src = (const GLB float*)parts.sums + at;
+    float z = src[0];
+#pragma unroll 8
+    for (int i = 1; i < parts.n; ++i) z += src[i * mn];
+    finish(f, at / f.N, at % f.N, z);
 }
 
 constexpr int64_t kMaxSize = ((int64_t)1 << 31) - 1;
@@ -576,16 +605,45 @@ struct FwdPlan {
     bool skinny, tile;           // few tokens; the element-load kernel; else the matrix kernels
     bool copy_x;
     MmNt nt;                     // sizes, tile and parts
+    Parts parts;                 // of the few-token kernel
     size_t what, xc, part, bytes;
 };
+// The few-token kernel's parts and estimated microseconds: eight blocks a time (above), a tile's reads of X and the codes
+// unaligned three times that; 5.5 for the second launch.  Parts for at most two workgroups a compute unit.
+double skinny_plan(const pgq_linear_fwd& p, Parts& parts)
+{
+    const int64_t tiles = (p.N + 15) / 16, blocks = (p.K + 63) / 64;
+    double block = p.M <= 16 ? 0.3 + 0.02 * (double)p.M : p.M <= 32 ? 0.75 : 1.9;
+    if (p.M > 1 && (p.ldx % 8 || p.ldc % 16 || !is_aligned(p.x, 16) || !is_aligned(p.codes, 16))) block *= 3.0;
+    double best = 0;
+    for (int64_t n = 1; n <= 64; n *= 2) {
+        const int64_t per = (blocks + n - 1) / n;
+        if (n > 1 && (tiles * n > 512 || per < kSkinnyWaves || (n - 1) * per >= blocks)) break;
+        const double rounds = std::max(1.0, (double)(tiles * n) / 256.0);
+        const double t = 3.0 + (double)((per + kSkinnyWaves - 1) / kSkinnyWaves) * block * rounds + (n > 1 ? 5.5 : 0.0);
+        if (best == 0 || t < best) {
+            best = t;
+            parts.n = (int32_t)n;
+            parts.blocks = per;
+        }
+    }
+    return best;
+}
 FwdPlan plan_fwd(const pgq_linear_fwd& p)
 {
     FwdPlan q;
     memset(&q, 0, sizeof(q));
     if (p.M == 0 || p.N == 0) return q;
-    q.skinny = p.M <= 16 || (p.M <= kSkinnyMost && (p.K >= kLong || p.K == 0));
-    q.tile = !q.skinny && (p.K >= kLong || p.K == 0);
-    if (q.skinny || q.tile) return q;
+    auto few = [&] {
+        q.skinny = true;
+        q.copy_x = false;
+        q.bytes = q.parts.n > 1 ? up256((size_t)q.parts.n * p.M * p.N * 4) : 0;
+        return q;
+    };
+    const double skinny = p.M <= kSkinnyMost ? skinny_plan(p, q.parts) : 0.0;
+    if (p.M <= 16 || (p.M <= kSkinnyMost && (p.K >= kLong || p.K == 0))) return few();
+    q.tile = p.K >= kLong || p.K == 0;
+    if (q.tile) return q;
     q.copy_x = !direct(p.x, p.ldx, p.K);
     q.nt.I = p.M;
     q.nt.J = p.N;
@@ -593,15 +651,10 @@ FwdPlan plan_fwd(const pgq_linear_fwd& p)
     double mm = mm_nt_plan(q.nt, p.K % 16 == 0 && p.ldc % 16 == 0 && p.ldc < kLong && is_aligned(p.codes, 16),
                            (double)float_size(p.y_dtype) + (p.z ? 2.0 : 0.0) + (p.residual ? (double)float_size(p.residual_dtype) : 0.0));
     if (p.M <= kSkinnyMost) {
-        // 17 to 64 tokens: the few-token kernel reads all of X again for every 16 weight rows (about 8 MB a
-        // microsecond; at 64 x 4096 x 4096 19.7 us against 13.6 for the tiles, at 64 x 1584 x 528 5.9 against 8.4)
-        const double x = (double)((p.M + 15) / 16 * 16) * (double)p.K * 2.0 * (double)((p.N + 15) / 16);
+        // 17 to 64 tokens: the few-token kernel reads all of X again for every 16 weight rows (at 64 x 4096 x 4096 19.7
+        // us against 13.6 for the tiles, at 64 x 1584 x 528 5.9 against 8.4)
         if (q.copy_x || !q.nt.from_codes) mm += 5.0;
-        if (4.0 + x / 8e6 <= mm) {
-            q.skinny = true;
-            q.copy_x = false;
-            return q;
-        }
+        if (skinny <= mm) return few();
     }
     if (!q.nt.from_codes) q.bytes = up256((size_t)p.N * up8(p.K) * 2);
     q.xc = q.bytes;
@@ -719,12 +772,15 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     pgq_linear_bwd b;
     memset(&b, 0, sizeof(b));
     if (q.skinny) {
-        Launches l(1, stream);
-        void* args[] = {&f};
+        Parts parts = q.parts;
+        parts.sums = reinterpret_cast<float*>(ws);
+        Launches l(parts.n > 1 ? 2 : 1, stream);
+        void* args[] = {&f, &parts};
         const void* k = f.M <= 16   ? reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<1>)
                         : f.M <= 32 ? reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<2>)
                                     : reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<4>);
-        l.go(k, (f.N + 15) / 16, 64 * kSkinnyWaves, args);
+        l.go(k, (f.N + 15) / 16 * parts.n, 64 * kSkinnyWaves, args);
+        if (parts.n > 1) l.go(reinterpret_cast<const void*>(&pgq_linear_join_kernel), (f.M * f.N + 255) / 256, 256, args);
         return l.done();
     }
     if (q.tile) {

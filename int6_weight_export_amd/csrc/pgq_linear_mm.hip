@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(256) pgq_mm_nt_reduce_kernel(MmNt p)
     const GLB f32x4* src = (const GLB f32x4*)p.partial + (size_t)unit * 64 + lane;
     const size_t step = (size_t)tiles * (WR * WC * IB * JB * 4 * 64);
     f32x4 v = *src;
-    for (int s = 1; s < p.splits; ++s) {
+#pragma unroll 8
+    for (int s = 1; s < p.splits; ++s) {                      // (loads of several parts in flight together)
         src += step;
         const f32x4 x = *src;
 #pragma unroll
@@ -775,7 +776,8 @@ __global__ void __launch_bounds__(256) pgq_mm_tt_reduce_kernel(MmTt p)
     const GLB f32x4* src = (const GLB f32x4*)p.partial + (size_t)unit * 64 + lane;
     const size_t step = (size_t)tiles * (WR * WC * IB * JB * 4 * 64);
     f32x4 v = *src;
-    for (int s = 1; s < p.splits; ++s) {
+#pragma unroll 8
+    for (int s = 1; s < p.splits; ++s) {                      // (loads of several parts in flight together)
         src += step;
         const f32x4 x = *src;
 #pragma unroll

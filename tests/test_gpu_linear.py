@@ -457,6 +457,29 @@ def test_infinite_and_nan_scales(M, N, K):
     assert torch.equal(y[:, rest], base[:, rest])
 
 
+@pytest.mark.parametrize("M,N,K,pad", [(1, 7, 40000, 0), (5, 40, 8192, 0), (16, 64, 6176, 3), (33, 20, 8200, 1), (19, 224, 6176, 1),
+                                       (2, 100, 4160, 16), (64, 16, 16384, 8)])
+@pytest.mark.parametrize("act,y,res", [("none", "f32", None), ("relu2", "bf16", "f32"), ("silu", "f32", "bf16")])
+def test_few_tokens_long_rows(M, N, K, pad, act, y, res):
+    """Few weight rows of long K go in parts; padding around the rows holds NaN and codes that must not count."""
+    say(f"linear few tokens in parts {M}x{N}x{K} pad {pad} {act} {y}")
+    codes, scales, w = weights(N, K, M)
+    cw = torch.full((N, K + pad), 77, dtype=torch.int8, device="cuda")
+    cw[:, :K] = codes
+    xw = torch.full((M, K + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xw[:, :K] = randn((M, K), 5, torch.bfloat16)
+    x = xw[:, :K]
+    b = randn((1, N), 7, torch.float32)[0]
+    r = None if res is None else randn((M, N), 6, T[res])
+    got, z = ops.qlinear(x, cw[:, :K], scales, bias=b, act=act, slope=0.5, residual=r, want_z=True, out_dtype=T[y])
+    again, _ = ops.qlinear(x, cw[:, :K], scales, bias=b, act=act, slope=0.5, residual=r, want_z=True, out_dtype=T[y])
+    torch.cuda.synchronize()
+    zr, ez, yr, ey = ref.forward(f64(x), w, f64(b), act, 0.5, None if r is None else f64(r), y)
+    within(z, zr, ez, "z")
+    within(got, yr, ey, "y")
+    assert torch.equal(got, again)
+
+
 def test_in_place_and_shared_memory():
     """Y over X is refused; Y and X, and Y and Z, as columns of one buffer are not."""
     say("linear shared memory")

@@ -199,7 +199,9 @@ struct Out {
 // A workgroup of WR x WC wavefronts computes a tile of 32 IB WR x 32 JB WC, each wavefront IB x JB blocks
 // of 32 x 32.  Each 64-wide stage of both operands goes from global memory straight into LDS (buffer
 // loads with the LDS destination), double-buffered, so the next stage's loads are in flight while the
-// matrix cores work on this one; a lane past I, J or L gets zeros from the buffer range check.
+// matrix cores work on this one; a lane past I, J or L gets zeros from the buffer range check.  Where the LDS has room
+// A, which comes from memory, is three stages deep and B, which stays in the caches, two (16384 x 528 x 1584 52.6 ->
+// 46.9 us, 8192 x 8192 x 4096 483 -> 465).
 //
 // LDS slots are 16-byte granules, 8 to a row; granule g of row r sits in slot g ^ swz(r), so that the
 // rows a fragment read touches spread over distinct banks in every group of 8 and of 16 lanes.
@@ -247,10 +249,10 @@ __device__ __forceinline__ void spread()
 
 constexpr int kWayOut = 64 + 4;                // floats of a row on its way out, at most
 
-template <int WR, int WC, int IB, int JB, bool Q, int NB>
+template <int WR, int WC, int IB, int JB, bool Q, int NB, int NA>
 constexpr int nt_lds()
 {
-    constexpr int stages = NB * (32 * IB * WR * 8 + 32 * JB * WC * (Q ? 4 : 8)) * 16;
+    constexpr int stages = (NA * 32 * IB * WR * 8 + NB * 32 * JB * WC * (Q ? 4 : 8)) * 16;
     constexpr int out = WR * WC * 32 * kWayOut * 4;
     return stages > out ? stages : out;
 }
@@ -294,7 +296,7 @@ __device__ __forceinline__ void way_out(const MmNt& p, const f32x16 (&acc)[IB][J
     }
 }
 
-template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
+template <int WR, int WC, int IB, int JB, bool Q, int NB, int NA, typename YT>
 __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t total, uint8_t* lds)
 {
     constexpr int T = 64 * WR * WC, TI = 32 * IB * WR, TJ = 32 * JB * WC;
@@ -330,26 +332,27 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     // A whole stage costs a load instruction and its scalar offset each (address arithmetic in the vector unit
     // would run while no wavefront multiplies: the barrier has just lined them up); the last, partial stage
     // masks the granules past the contraction's end.
-    auto issue = [&](int st) __attribute__((always_inline)) {
-        uint8_t* la = lds + (st % NB) * (AS + BS);
-        uint8_t* lb = la + AS;
-        const int ka = st * (kTK * 2), kb = Q ? st * kTK : ka;
-        const uint32_t off_a = st < nfull || st * kTK + 8 * g0 < (int)len ? 0u : kOOB;
-        const uint32_t off_b = st < nfull || st * kTK + (Q ? 16 : 8) * bg0 < (int)len ? 0u : kOOB;
+    auto issue_a = [&](int st) __attribute__((always_inline)) {
+        uint8_t* la = lds + (st % NA) * AS;
+        const uint32_t off = st < nfull || st * kTK + 8 * g0 < (int)len ? 0u : kOOB;
         if (st < nfull) {
 #pragma unroll
-            for (int c = 0; c < AI; ++c)
-                load_lds(ar, la + (c * T + wave * 64) * 16, ao[c], ka);
-#pragma unroll
-            for (int c = 0; c < BI; ++c)
-                load_lds(br, lb + (c * T + wave * 64) * 16, bo[c], kb);
+            for (int c = 0; c < AI; ++c) load_lds(ar, la + (c * T + wave * 64) * 16, ao[c], st * (kTK * 2));
         } else {
 #pragma unroll
-            for (int c = 0; c < AI; ++c)
-                load_lds(ar, la + (c * T + wave * 64) * 16, ao[c] | off_a, ka);
+            for (int c = 0; c < AI; ++c) load_lds(ar, la + (c * T + wave * 64) * 16, ao[c] | off, st * (kTK * 2));
+        }
+    };
+    auto issue_b = [&](int st) __attribute__((always_inline)) {
+        uint8_t* lb = lds + NA * AS + (st % NB) * BS;
+        const int kb = st * (Q ? kTK : kTK * 2);
+        const uint32_t off = st < nfull || st * kTK + (Q ? 16 : 8) * bg0 < (int)len ? 0u : kOOB;
+        if (st < nfull) {
 #pragma unroll
-            for (int c = 0; c < BI; ++c)
-                load_lds(br, lb + (c * T + wave * 64) * 16, bo[c] | off_b, kb);
+            for (int c = 0; c < BI; ++c) load_lds(br, lb + (c * T + wave * 64) * 16, bo[c], kb);
+        } else {
+#pragma unroll
+            for (int c = 0; c < BI; ++c) load_lds(br, lb + (c * T + wave * 64) * 16, bo[c] | off, kb);
         }
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
@@ -373,8 +376,8 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
         bf16x8 a[IB][2], b[JB][Q ? 1 : 2];
     } f0, f1;
     auto fetch = [&](Frag& f, int st, int kb) __attribute__((always_inline)) {
-        const uint8_t* la = lds + (st % NB) * (AS + BS);
-        const uint8_t* lb = la + AS;
+        const uint8_t* la = lds + (st % NA) * AS;
+        const uint8_t* lb = lds + NA * AS + (st % NB) * BS;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -418,14 +421,18 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i][t], b[j][t], acc[i][j], 0, 0, 0);
     };
     // Two sets of fragments: while the matrix cores work on one half stage, the next half is read from LDS.
-    // The barrier sits between the halves: there every wave has read all of stage st, so the loads of stage
-    // st + NB may overwrite it, and those of st + 1 have arrived (the younger stages' loads may still be out).
-    constexpr int NL = AI + BI;
+    // The barrier sits between the halves: there every wave has read all of stage st, so the loads of B's stage
+    // st + NB and A's stage st + NA may overwrite it, and those of st + 1 have arrived (younger ones may still be out:
+    // loads are counted in the order B(st + NB), A(st + NA)).
+    constexpr int NL = AI + BI, EL = (NA - NB) * AI;
     if (nst > 0) {
 #pragma unroll
-        for (int s = 0; s < NB; ++s)
-            if (s < nst) issue(s);
-        if (nst >= NB) wait_barrier<(NB - 1) * NL>();
+        for (int s = 0; s < NA; ++s)
+            if (s < nst) {
+                if (s < NB) issue_b(s);
+                issue_a(s);
+            }
+        if (nst >= NA) wait_barrier<(NB - 1) * NL + EL>();
         else wait_barrier<0>();
         fetch(f0, 0, 0);
     }
@@ -435,9 +442,10 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
             fetch(f1, st, 1);
             multiply(f0, st * kTK);
             spread<2 * (IB + JB), 2 * IB * JB>();
-            if (st + NB - 1 < nst) wait_barrier<(NB - 2) * NL>();
+            if (st + NA - 1 < nst) wait_barrier<(NB - 2) * NL + EL>();
             else wait_barrier<0>();
-            if (st + NB < nst) issue(st + NB);
+            if (st + NB < nst) issue_b(st + NB);
+            if (st + NA < nst) issue_a(st + NA);
             fetch(f0, st + 1, 0);
             multiply(f1, st * kTK + 32);
             spread<2 * (IB + JB), 2 * IB * JB>();
@@ -446,9 +454,10 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     for (; st < nst; ++st) {
         fetch(f1, st, 1);
         multiply(f0, st * kTK);
-        if (st + NB - 1 < nst) wait_barrier<(NB - 2) * NL>();
+        if (st + NA - 1 < nst) wait_barrier<(NB - 2) * NL + EL>();
         else wait_barrier<0>();
-        if (st + NB < nst) issue(st + NB);
+        if (st + NB < nst) issue_b(st + NB);
+        if (st + NA < nst) issue_a(st + NA);
         if (st + 1 < nst) fetch(f0, st + 1, 0);
         if (st * kTK + 32 < (int)len) multiply(f1, st * kTK + 32);
     }
@@ -471,12 +480,12 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     if constexpr (JB == 3) way_out<IB, JB, 2, 1, YT>(p, acc, tl, i0 + wi, j0 + wj, lane);
 }
 
-template <int WR, int WC, int IB, int JB, bool Q, int NB, typename YT>
+template <int WR, int WC, int IB, int JB, bool Q, int NB, int NA, typename YT>
 __global__ void __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2)))
 pgq_mm_nt_kernel(MmNt p)
 {
-    __shared__ __align__(16) uint8_t lds[nt_lds<WR, WC, IB, JB, Q, NB>()];
-    nt_body<WR, WC, IB, JB, Q, NB, YT>(p, blockIdx.x, gridDim.x, lds);
+    __shared__ __align__(16) uint8_t lds[nt_lds<WR, WC, IB, JB, Q, NB, NA>()];
+    nt_body<WR, WC, IB, JB, Q, NB, NA, YT>(p, blockIdx.x, gridDim.x, lds);
 }
 
 // the sums of the parts, in their order, through the epilogue: one wavefront takes 8 rows of 32 columns
@@ -520,27 +529,27 @@ __global__ void __launch_bounds__(256) pgq_mm_nt_reduce_kernel(MmNt p)
 }
 
 // The tiles a product can be cut into.  stage: microseconds of one 64-wide stage of a workgroup that has its
-// compute unit alone; busy: a stage's share of a compute unit that several keep busy; per_cu: how many fit.
-// Measured at 1024 x 1024 x 1024 and 8192 x 4096 x 4096.
+// compute unit alone; busy: a stage's share of a compute unit that several keep busy; per_cu: how many fit; start:
+// the launch, the first loads and the last stores.  Fitted to the clock over the sizes at mm_nt_plan.
 struct NtKind {
     int ti, tj, threads, per_cu;
-    double stage, busy;
+    double stage, busy, start;
     const void *f32, *bf16, *reduce;
     bool codes;                                   // B as codes
 };
-template <int WR, int WC, int IB, int JB, bool Q, int NB>
-NtKind nt_kind(int per_cu, double stage, double busy)
+template <int WR, int WC, int IB, int JB, bool Q, int NB, int NA = NB>
+NtKind nt_kind(int per_cu, double stage, double busy, double start = 4.0)
 {
-    return {32 * IB * WR, 32 * JB * WC, 64 * WR * WC, per_cu, stage, busy,
-            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, float>),
-            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, uint16_t>),
+    return {32 * IB * WR, 32 * JB * WC, 64 * WR * WC, per_cu, stage, busy, start,
+            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, NA, float>),
+            reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, NA, uint16_t>),
             reinterpret_cast<const void*>(&pgq_mm_nt_reduce_kernel<WR, WC, IB, JB>), Q};
 }
 // (256 x 192 beside 256 x 256 for outputs that end shortly behind a multiple of 256: 16384 x 528 x 1584 runs in
 // 41.0 us with it against 46.9, 16384 x 1584 x 528 in 71.3 against 50.1)
-const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2>(2, 0.85, 0.70), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.38),
-                      nt_kind<2, 2, 1, 1, false, 4>(2, 0.27, 0.21), nt_kind<1, 4, 4, 1, true, 3>(2, 0.75, 0.62),
-                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.35, 0.35), nt_kind<4, 2, 2, 3, false, 2>(1, 1.35, 1.27)};
+const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2, 3>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2, 3>(2, 0.50, 0.55), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.38),
+                      nt_kind<2, 2, 1, 1, false, 4>(2, 0.27, 0.21), nt_kind<1, 4, 4, 1, true, 3>(2, 0.50, 0.62, 6.0),
+                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.55, 0.40), nt_kind<4, 2, 2, 3, false, 2, 3>(1, 1.35, 1.27)};
 int64_t nt_tiles(const NtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 // ---- A columns times B columns ----------------------------------------------------------------------
@@ -749,14 +758,14 @@ __global__ void __launch_bounds__(1024) pgq_mm_dbias_kernel(Dbias p)
 // A whole backward pass after its operands are laid out: the tiles of dX, those of dW and the sums of db are
 // independent, so one launch holds them all and the second product fills the compute units that the first
 // leaves idle in its last round.
-template <int A0, int A1, int A2, int A3, int NB, int B0, int B1, int B2, int B3, typename YT>
+template <int A0, int A1, int A2, int A3, int NB, int NA, int B0, int B1, int B2, int B3, typename YT>
 __global__ void __launch_bounds__(64 * A0 * A1) __attribute__((amdgpu_waves_per_eu(2)))
 pgq_mm_both_kernel(MmNt x, MmTt w, Dbias d, uint32_t nx, uint32_t nw)
 {
     static_assert(A0 * A1 == B0 * B1, "one block size");
-    constexpr int LX = nt_lds<A0, A1, A2, A3, false, NB>(), LW = tt_lds<B0, B1, B2, B3>();
+    constexpr int LX = nt_lds<A0, A1, A2, A3, false, NB, NA>(), LW = tt_lds<B0, B1, B2, B3>();
     __shared__ __align__(16) uint8_t lds[LX > LW ? LX : LW];
-    if (blockIdx.x < nx) nt_body<A0, A1, A2, A3, false, NB, YT>(x, blockIdx.x, nx, lds);
+    if (blockIdx.x < nx) nt_body<A0, A1, A2, A3, false, NB, NA, YT>(x, blockIdx.x, nx, lds);
     else if (blockIdx.x < nx + nw) tt_body<B0, B1, B2, B3>(w, blockIdx.x - nx, nw, lds);
     else dbias_body(d, blockIdx.x - nx - nw, lds);
 }
@@ -809,8 +818,8 @@ int64_t tt_tiles(const TtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1)
 // The tile and the number of parts with the least estimated time.  A tile that has its compute unit to itself
 // goes in rounds of 256; smaller ones keep several on a unit and flow.  To that the trip of the outputs (5.3 MB a
 // microsecond: the stores of a tile hardly overlap its stages), a start a round, and, for parts, their sums'
-// trip and a launch.  Measured against the clock at 16384 x 1584 x 528, 16384 x 528 x 1584, 8192 x 8192 x
-// 4096, 4096 x 1536 x 512 and 1009 x 717 x 1032: within 15%, and the tile chosen within 5% of the best.
+// trip and a launch.  Every tile timed against the choice at 25 sizes from 96 x 1584 x 528 to 8192 x 8192 x 1024 (X from
+// memory): the tile chosen is within 7% of the best.
 double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes)
 {
     double best = 0;
@@ -831,7 +840,7 @@ double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes)
                 t += (double)rounds * ((double)per * kind.busy + 2.0) + 2.0;
             } else {
                 const double share = (double)std::min<int64_t>(kind.per_cu, rounds);
-                t += (double)per * std::max(std::max(kind.stage, kind.busy * share), kind.busy * (double)wgs / 256.0) + 4.0;
+                t += (double)per * std::max(std::max(kind.stage, kind.busy * share), kind.busy * (double)wgs / 256.0) + kind.start;
             }
             if (parts > 1) t += 4.0 + (double)wgs * kind.ti * kind.tj * 8.0 / 5e6;
             if (!kind.codes) t += layout;
@@ -904,16 +913,16 @@ struct BothKind {
     double nt_stage, tt_stage;                    // microseconds of a stage when every unit is busy, times per_cu
     const void *f32, *bf16;
 };
-template <int A0, int A1, int A2, int A3, int NB, int B0, int B1, int B2, int B3>
+template <int A0, int A1, int A2, int A3, int NB, int NA, int B0, int B1, int B2, int B3>
 BothKind both_kind(int nt, int tt, int per_cu, double nt_stage, double tt_stage)
 {
     return {nt, tt, per_cu, nt_stage, tt_stage,
-            reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, B0, B1, B2, B3, float>),
-            reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, B0, B1, B2, B3, uint16_t>)};
+            reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, NA, B0, B1, B2, B3, float>),
+            reinterpret_cast<const void*>(&pgq_mm_both_kernel<A0, A1, A2, A3, NB, NA, B0, B1, B2, B3, uint16_t>)};
 }
-const BothKind kBoth[] = {both_kind<2, 4, 4, 2, 2, 4, 2, 2, 4>(0, 0, 1, 1.75, 1.9), both_kind<2, 4, 4, 2, 2, 4, 2, 2, 3>(0, 1, 1, 1.75, 1.5),
-                          both_kind<2, 2, 2, 2, 2, 2, 2, 2, 2>(1, 2, 2, 1.4, 1.1), both_kind<2, 2, 1, 1, 4, 2, 2, 1, 1>(3, 3, 2, 0.45, 0.5),
-                          both_kind<4, 2, 2, 3, 2, 4, 2, 2, 3>(6, 1, 1, 1.40, 1.5)};
+const BothKind kBoth[] = {both_kind<2, 4, 4, 2, 2, 3, 4, 2, 2, 4>(0, 0, 1, 1.75, 1.9), both_kind<2, 4, 4, 2, 2, 3, 4, 2, 2, 3>(0, 1, 1, 1.75, 1.5),
+                          both_kind<2, 2, 2, 2, 2, 3, 2, 2, 2, 2>(1, 2, 2, 1.4, 1.1), both_kind<2, 2, 1, 1, 4, 4, 2, 2, 1, 1>(3, 3, 2, 0.45, 0.5),
+                          both_kind<4, 2, 2, 3, 2, 3, 4, 2, 2, 3>(6, 1, 1, 1.40, 1.5)};
 
 // When `first` workgroups of one_first microseconds and then `second` of one_second each, taken in that order by
 // `slots` places, are done: the places free after the first kind's last whole round start at t0, the others at

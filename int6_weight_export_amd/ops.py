@@ -201,11 +201,6 @@ class Exporter:
             self.dq_ptrs = (ctypes.c_void_p * n)(*[d.data_ptr() for d in self.dq])
         self.status = new_status(dev)
         self._uploaded = False
-        self._index = _gpu_of("weight", self.weights[0])
-        self._numel = [w.numel() for w in self.weights]
-        self._ptrs = (ctypes.c_void_p * n)()
-        self._g_dtypes = [torch.float32] * n
-        self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
     def run(self, reuse_table: bool = True):
         flags = pgq.PGQ_TABLE_RESIDENT if (reuse_table and self._uploaded) else 0

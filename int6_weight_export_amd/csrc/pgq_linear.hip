@@ -141,20 +141,20 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) { return (uint32_t
 // ---- operands laid out for the matrix products --------------------------------------------------------
 // One launch prepares everything the products of a call read: dZ (and the partial sums of db), What as bf16
 // rows (forward) or transposed (dX), and a copy of X with 16-byte aligned rows where X has none.  Rows are
-// padded to 8 elements with zeros.  What is formed once here instead of in every tile: it is small beside X
+// padded to 8 elements with zeros, their strides to whole cache lines.  What is formed once here instead of in every tile: it is small beside X
 // and Y, and its conversion from codes cost the matrix kernel about a sixth of its time.
 constexpr int kDzCols = 256;                   // columns of a dZ unit
 constexpr int kFlat = 256;                     // granules (8 elements) of a flat unit, one a thread
 
 struct Prep {
     pgq_linear_bwd b;            // the sources (codes, scales, x and their strides also in forward)
-    uint16_t* dz;                // M x ldz_out, or NULL: only the partial sums
+    uint16_t* dz;                // M x Np, row stride ldn, or NULL: only the partial sums
     float* dbias_part;           // ceil(M / dz_rows) x N, or NULL
     int32_t dz_rows;             // rows of a dZ unit
-    uint16_t* what;              // N x Kp
-    uint16_t* what_t;            // K x Np
-    uint16_t* xc;                // M x Kp
-    int64_t Kp, Np;
+    uint16_t* what;              // N x Kp, row stride ldk
+    uint16_t* what_t;            // K x Np, row stride ldn
+    uint16_t* xc;                // M x Kp, row stride ldk
+    int64_t Kp, Np, ldk, ldn;
     int64_t n_dz, n_what, n_what_t, n_x;      // units of each kind, in this order
 };
 
@@ -250,7 +250,7 @@ __device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums
                 }
                 if (m < b.M) {
                     if (p.dz)
-                        *(GLB u32x4*)(p.dz + m * p.Np + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
+                        *(GLB u32x4*)(p.dz + m * p.ldn + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) t[e] += d[e];
                 }
@@ -299,7 +299,7 @@ __device__ __forceinline__ void prep_what_t(const Prep& p, int64_t unit, uint16_
     for (int c = 0; c < 2; ++c) {
         const int r = (tid >> 3) + 32 * c, g = tid & 7;
         const int64_t k = k0 + r, n = n0 + 8 * g;
-        if (k < b.K && n < p.Np) *(GLB u32x4*)(p.what_t + k * p.Np + n) = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
+        if (k < b.K && n < p.Np) *(GLB u32x4*)(p.what_t + k * p.ldn + n) = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
     }
 }
 
@@ -348,10 +348,10 @@ __global__ void __launch_bounds__(256) pgq_linear_prep_kernel(Prep p)
         // padding is 0 whatever the scale is
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = pk_bf16(k + 2 * e < b.K ? (float)q[2 * e] * s : 0.0f, k + 2 * e + 1 < b.K ? (float)q[2 * e + 1] * s : 0.0f);
-        *(GLB u32x4*)(p.what + r * p.Kp + k) = o;
+        *(GLB u32x4*)(p.what + r * p.ldk + k) = o;
     } else {
         o = load_cols<8>(b.x + r * b.ldx, k, b.K);
-        *(GLB u32x4*)(p.xc + r * p.Kp + k) = o;
+        *(GLB u32x4*)(p.xc + r * p.ldk + k) = o;
     }
 }
 
@@ -589,6 +589,9 @@ pgq_status check_bwd(const pgq_linear_bwd* p)
 
 int64_t tiles_of(int64_t I, int64_t J) { return ((I + kGT - 1) / kGT) * ((J + kGT - 1) / kGT); }
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+// Row stride of a laid-out operand: whole 128-byte lines, so that a stage's 128 bytes of a row are one line, not
+// two (16384 x 1584 x 528 50.1 -> 48.2 us, 4899 x 947 x 4656 114 -> 107); short rows stay dense.
+int64_t pitch(int64_t x) { return x >= 256 ? (x + 63) / 64 * 64 : up8(x); }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Contractions and rows this long go through the 64 x 64 element-load kernel: the matrix kernels address
@@ -656,9 +659,9 @@ FwdPlan plan_fwd(const pgq_linear_fwd& p)
         if (q.copy_x || !q.nt.from_codes) mm += 5.0;
         if (skinny <= mm) return few();
     }
-    if (!q.nt.from_codes) q.bytes = up256((size_t)p.N * up8(p.K) * 2);
+    if (!q.nt.from_codes) q.bytes = up256((size_t)p.N * pitch(p.K) * 2);
     q.xc = q.bytes;
-    if (q.copy_x) q.bytes += up256((size_t)p.M * up8(p.K) * 2);
+    if (q.copy_x) q.bytes += up256((size_t)p.M * pitch(p.K) * 2);
     q.part = q.bytes;
     q.bytes += up256(mm_nt_partial_bytes(q.nt));
     return q;
@@ -691,17 +694,17 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     if (q.tile || p.N == 0 || p.M == 0) return q;
     if (q.dx || q.dw) {
         q.dz = p.act != PGQ_ACT_NONE || p.dy_dtype != PGQ_BF16 || !direct(p.dy, p.lddy, p.N);
-        if (q.dz) q.o_dz = take((size_t)p.M * up8(p.N) * 2);
+        if (q.dz) q.o_dz = take((size_t)p.M * pitch(p.N) * 2);
     }
     if (q.dx) {
-        q.o_what_t = take((size_t)p.K * up8(p.N) * 2);
+        q.o_what_t = take((size_t)p.K * pitch(p.N) * 2);
         q.nt.I = p.M;
         q.nt.J = p.K;
         q.nt.L = up8(p.N);
     }
     if (q.dw) {
         q.copy_x = !direct(p.x, p.ldx, p.K);
-        if (q.copy_x) q.o_x = take((size_t)p.M * up8(p.K) * 2);
+        if (q.copy_x) q.o_x = take((size_t)p.M * pitch(p.K) * 2);
         q.tt.I = p.N;
         q.tt.J = p.K;
         q.tt.L = p.M;
@@ -803,6 +806,7 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     pr.b.x = f.x;
     pr.b.ldx = f.ldx;
     pr.Kp = up8(f.K);
+    pr.ldk = pitch(f.K);
     if (!q.nt.from_codes) {
         pr.what = reinterpret_cast<uint16_t*>(ws + q.what);
         pr.n_what = (f.N * (pr.Kp / 8) + kFlat - 1) / kFlat;
@@ -815,11 +819,11 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     if (prep) l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), pr.n_what + pr.n_x, 256, args);
     MmNt mm = q.nt;
     mm.a = q.copy_x ? pr.xc : f.x;
-    mm.lda = q.copy_x ? pr.Kp : f.ldx;
+    mm.lda = q.copy_x ? pr.ldk : f.ldx;
     mm.b = pr.what;
     mm.codes = f.codes;
     mm.scales = f.scales;
-    mm.ldb = q.nt.from_codes ? f.ldc : pr.Kp;
+    mm.ldb = q.nt.from_codes ? f.ldc : pr.ldk;
     mm.partial = reinterpret_cast<float*>(ws + q.part);
     mm.e.bias = f.bias;
     mm.e.residual = f.residual;
@@ -857,6 +861,8 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     pr.b = b;
     pr.Kp = up8(b.K);
     pr.Np = up8(b.N);
+    pr.ldk = pitch(b.K);
+    pr.ldn = pitch(b.N);
     pr.dz = q.dz ? reinterpret_cast<uint16_t*>(ws + q.o_dz) : nullptr;
     pr.dz_rows = q.dz_rows;
     pr.dbias_part = q.db ? reinterpret_cast<float*>(ws + q.o_db) : nullptr;
@@ -888,16 +894,16 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     MmNt x = q.nt;
     MmTt w = q.tt;
     x.a = w.a = q.dz ? pr.dz : static_cast<const uint16_t*>(b.dy);
-    x.lda = w.lda = q.dz ? pr.Np : b.lddy;
+    x.lda = w.lda = q.dz ? pr.ldn : b.lddy;
     x.b = pr.what_t;
-    x.ldb = pr.Np;
+    x.ldb = pr.ldn;
     x.partial = reinterpret_cast<float*>(ws + q.o_part_dx);
     x.e.y = b.dx;
     x.e.ldy = b.lddx;
     x.e.y_dtype = b.dx_dtype;
     x.e.vec = rows16(b.dx, b.dx_dtype, b.lddx);
     w.b = q.copy_x ? pr.xc : b.x;
-    w.ldb = q.copy_x ? pr.Kp : b.ldx;
+    w.ldb = q.copy_x ? pr.ldk : b.ldx;
     w.c = b.dw;
     w.ldc = b.lddw;
     w.c_dtype = b.dw_dtype;

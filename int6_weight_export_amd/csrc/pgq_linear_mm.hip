@@ -547,9 +547,9 @@ NtKind nt_kind(int per_cu, double stage, double busy, double start = 4.0)
 }
 // (256 x 192 beside 256 x 256 for outputs that end shortly behind a multiple of 256: 16384 x 528 x 1584 runs in
 // 41.0 us with it against 46.9, 16384 x 1584 x 528 in 71.3 against 50.1)
-const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2, 3>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2, 3>(2, 0.50, 0.55), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.38),
-                      nt_kind<2, 2, 1, 1, false, 4>(2, 0.27, 0.21), nt_kind<1, 4, 4, 1, true, 3>(2, 0.50, 0.62, 6.0),
-                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.55, 0.40), nt_kind<4, 2, 2, 3, false, 2, 3>(1, 1.35, 1.27)};
+const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2, 3>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2, 3>(2, 0.50, 0.55), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.36),
+                      nt_kind<2, 2, 1, 1, false, 4>(2, 0.33, 0.24), nt_kind<1, 4, 4, 1, true, 3>(2, 0.50, 0.62, 6.0),
+                      nt_kind<1, 4, 2, 1, true, 4>(2, 0.55, 0.40), nt_kind<4, 2, 2, 3, false, 2, 3>(1, 1.35, 1.35)};
 int64_t nt_tiles(const NtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1) / k.ti) * ((J + k.tj - 1) / k.tj); }
 
 // ---- A columns times B columns ----------------------------------------------------------------------
@@ -824,11 +824,25 @@ int64_t tt_tiles(const TtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1)
 
 }  // namespace
 
-// The tile and the number of parts with the least estimated time.  A tile that has its compute unit to itself
-// goes in rounds of 256; smaller ones keep several on a unit and flow.  To that the trip of the outputs (5.3 MB a
-// microsecond: the stores of a tile hardly overlap its stages), a start a round, and, for parts, their sums'
-// trip and a launch.  Every tile timed against the choice at 25 sizes from 96 x 1584 x 528 to 8192 x 8192 x 1024 (X from
-// memory): the tile chosen is within 7% of the best.
+// Microseconds that workgroups of `per` stages each take: whole rounds over the places, then the rest.  A rest of at most
+// one workgroup a compute unit runs at the lone workgroup's pace, more at a pace between the two; a tile that has
+// its unit to itself runs a stage faster the fewer units share the memory (1.6 us with all of them, 1.3 with half).
+static double rounds_of_stages(const NtKind& kind, int64_t wgs, double per)
+{
+    const int64_t places = 256 * kind.per_cu, full = wgs / places, rest = wgs % places;
+    if (kind.per_cu == 1) {
+        const double last = kind.busy * (0.8 + 0.2 * (double)rest / 256.0);
+        return (double)full * (per * kind.busy + 2.0) + (rest ? per * last + 2.0 : 0.0) + 2.0;
+    }
+    const double both = kind.busy * (double)kind.per_cu;
+    const double last = rest <= 256 ? kind.stage : kind.stage + (both - kind.stage) * (double)(rest - 256) / (double)(places - 256);
+    return (double)full * per * both + (rest ? per * last : 0.0) + kind.start;
+}
+
+// The tile and the number of parts with the least estimated time: the stages, the trip of the outputs (5.3 MB a
+// microsecond: the stores of a tile hardly overlap its stages) and, for parts, their sums' trip and a launch.  Every tile
+// timed against the choice at 31 sizes from 96 x 1584 x 528 to 8192 x 8192 x 1024 (X from memory): the tile chosen is
+// within 7% of the best at 30 of them; at 4899 x 947 x 4656, whose rows of X straddle cache lines, it is 26% off.
 double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes)
 {
     double best = 0;
@@ -843,14 +857,8 @@ double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes)
         for (int64_t s = 1; s <= 16; s *= 2) {
             const int64_t per = (stages + s - 1) / s, parts = (stages + per - 1) / per;
             if (s > 1 && (parts != s || per < 4 || tiles * parts > 512)) break;
-            const int64_t wgs = tiles * parts, rounds = (wgs + 255) / 256;
-            double t = out;
-            if (kind.per_cu == 1) {
-                t += (double)rounds * ((double)per * kind.busy + 2.0) + 2.0;
-            } else {
-                const double share = (double)std::min<int64_t>(kind.per_cu, rounds);
-                t += (double)per * std::max(std::max(kind.stage, kind.busy * share), kind.busy * (double)wgs / 256.0) + kind.start;
-            }
+            const int64_t wgs = tiles * parts;
+            double t = out + rounds_of_stages(kind, wgs, (double)per);
             if (parts > 1) t += 4.0 + (double)wgs * kind.ti * kind.tj * 8.0 / 5e6;
             if (!kind.codes) t += layout;
             if (best == 0 || t < best) {

@@ -299,9 +299,11 @@ pgq_status pgq_qgemm_bf16_ybf16(const uint16_t* x, int64_t M, int64_t K, int64_t
 /*   act        none; relu: z > 0 ? z : slope * z; relu2: the square of relu; silu: z / (1 + e^-z) */
 /* Products of bf16 values are exact in fp32 and every sum, bias, activation and residual is    */
 /* formed in fp32; Y, Z, dX and dW are rounded to their type once, at the store.  In backward   */
-/* dZ is rounded to bf16 before the two products (the matrix cores' input type; exact when act  */
-/* is none and dY is bf16); db sums the unrounded dZ.  Sums run in a fixed order: a call on the */
-/* same inputs gives the same bits.                                                            */
+/* dZ, an fp32 value, enters the two products as a sum of bf16 values (the matrix cores' input  */
+/* type): one where it is one (bf16 dY times 1, 0 or powers of two), else two for a bf16 output */
+/* (at most 2^-14 of dZ is lost) and three for an fp32 one (nothing is).  Each is a product of  */
+/* its own: a caller content with a bf16 dZ forms it and passes it as dY with PGQ_ACT_NONE.      */
+/* db sums dZ itself.  Sums run in a fixed order: a call on the same inputs gives the same bits. */
 /* The gradient of the weights is the straight-through one: of the bf16 weights, zeroed where   */
 /* the fake-quant mask bit is 0 (pgq_fq_tensor.mask); that of the residual is dY itself.       */
 /* NaN and infinities follow the arithmetic (relu of -infinity with slope 0 is NaN); a masked      */

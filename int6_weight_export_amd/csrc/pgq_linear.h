@@ -75,7 +75,7 @@ hipError_t launch_mm_nt(const MmNt& p, void* stream);
 // splits > 1: the sums of the parts, in their order, through the epilogue
 hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream);
 
-// C[i][j] = sum_l A[l][i] B[l][j]: bf16 operands, 16-byte aligned rows of at least I and J elements rounded
+// C[i][j] = sum_l sum_p A[l][p part_cols + i] B[l][j], p below parts: bf16 operands, 16-byte aligned rows of at least I and J elements rounded
 // up to 8, row strides below 2^23.  C goes out as dw_dtype, zero where the mask bit of (i, j) is 0.
 struct MmTt {
     const uint16_t* a;
@@ -84,12 +84,14 @@ struct MmTt {
     void* c;
     int64_t ldc;
     int32_t c_dtype;
-    int32_t kind, splits;        // tile, and parts the sum over l is cut into (mm_tt_plan)
-    int64_t chunk;               // l per part, a multiple of 64
+    int32_t parts;               // bf16 values whose sum stands for an element of A, part_cols columns apart
+    int64_t part_cols;
+    int32_t kind, splits;        // tile, and pieces the sum is cut into (mm_tt_plan)
+    int64_t chunk;               // stages (64 l of one part) per piece
     const uint8_t* mask;         // NULL or I x ceil(J / 8) bytes
     float* partial;              // splits > 1: mm_tt_partial_bytes() of scratch
 };
-void mm_tt_plan(MmTt& p);        // kind, splits and chunk from I, J and L
+void mm_tt_plan(MmTt& p);        // kind, splits and chunk from I, J, L and parts
 size_t mm_tt_partial_bytes(const MmTt& p);
 hipError_t launch_mm_tt(const MmTt& p, void* stream);
 // splits > 1: the sum of the parts, in their order

@@ -3,9 +3,13 @@
 // What[n][k] = bf16(fp32(code[n][k] * s_n)), the STE forward's weight ("SubSixteen v2" card, PR #69,
 // section Other).  Three products:
 //     Z [m][n] = sum_k X[m][k]  What[n][k]          (forward)
-//     dX[m][k] = sum_n dZ[m][n] What[n][k]          dZ = bf16(dY * act'(Z))
+//     dX[m][k] = sum_n dZ[m][n] What[n][k]          dZ = dY * act'(Z)
 //     dW[n][k] = sum_m dZ[m][n] X[m][k]
 // Products of two bf16 values are exact in fp32; every sum is held in fp32.
+//
+// dZ is a binary32 value, the matrix cores take bf16: it enters the products as the sum of one to three bf16 parts,
+// as many as keep what is lost of it far below the outputs' own rounding (dz_parts), each part a product of its
+// own on the same sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -39,7 +43,27 @@ __device__ __forceinline__ void store_any(void* p, int32_t dtype, int64_t i, flo
 
 enum Product { P_FWD, P_DX, P_DW };
 
-// dZ in fp32 (m, n), rounded to bf16 where it enters a product
+// One part of a value, and what is left of it for the next: 8 bits cut off (so that the rest keeps the value's sign
+// and nothing overflows), the last part rounded to nearest.  Where the value ends before its last part the rest
+// goes on as 2^-40 of the value: a part of 0 would make NaN of an infinite weight or input, one of the other sign
+// would take its infinity away.
+__device__ __forceinline__ uint16_t next_part(float value, float& rest, bool last)
+{
+    const uint32_t bits = __builtin_bit_cast(uint32_t, rest);
+    const uint16_t part = last || rest != rest ? f32_to_bf16(rest) : (uint16_t)(bits >> 16);
+    rest = fabsf(value) < INFINITY ? rest - bf16_to_f32(part) : value;
+    if (rest == 0.0f) rest = value * 0x1p-40f;
+    return part;
+}
+__device__ __forceinline__ uint16_t part_of(float value, int part, int parts)
+{
+    float rest = value;
+    uint16_t h = 0;
+    for (int i = 0; i <= part; ++i) h = next_part(value, rest, i + 1 == parts);
+    return h;
+}
+
+// dZ in fp32 (m, n)
 __device__ __forceinline__ float dz_at(const pgq_linear_bwd& b, int64_t m, int64_t n)
 {
     const float g = load_any(b.dy, b.dy_dtype, m * b.lddy + n);
@@ -51,7 +75,7 @@ __device__ __forceinline__ float dz_at(const pgq_linear_bwd& b, int64_t m, int64
 constexpr int kGT = 64, kGK = 32, kGPad = kGK + 8;
 
 template <int P>
-__global__ void __launch_bounds__(256) pgq_linear_tile_kernel(pgq_linear_fwd f, pgq_linear_bwd b)
+__global__ void __launch_bounds__(256) pgq_linear_tile_kernel(pgq_linear_fwd f, pgq_linear_bwd b, int32_t parts)
 {
     __shared__ __align__(16) uint16_t As[kGT][kGPad];
     __shared__ __align__(16) uint16_t Bs[kGT][kGPad];
@@ -65,10 +89,10 @@ __global__ void __launch_bounds__(256) pgq_linear_tile_kernel(pgq_linear_fwd f, 
     auto what = [&](const int8_t* codes, int64_t ldc, const uint16_t* scales, int64_t n, int64_t k) {
         return f32_to_bf16((float)codes[n * ldc + k] * f16_to_f32(scales[n]));
     };
-    auto load_a = [&](int64_t i, int64_t l) -> uint16_t {
+    auto load_a = [&](int64_t i, int64_t l, int part) -> uint16_t {
         if (i >= I || l >= L) return 0;
         if (P == P_FWD) return f.x[i * f.ldx + l];
-        return P == P_DX ? f32_to_bf16(dz_at(b, i, l)) : f32_to_bf16(dz_at(b, l, i));
+        return part_of(P == P_DX ? dz_at(b, i, l) : dz_at(b, l, i), part, parts);
     };
     auto load_b = [&](int64_t j, int64_t l) -> uint16_t {
         if (j >= J || l >= L) return 0;
@@ -76,12 +100,12 @@ __global__ void __launch_bounds__(256) pgq_linear_tile_kernel(pgq_linear_fwd f, 
         return P == P_DX ? what(b.codes, b.ldc, b.scales, l, j) : b.x[l * b.ldx + j];
     };
     f32x16 acc = {};
-    for (int64_t l0 = 0; l0 < L; l0 += kGK) {
+    for (int64_t l0 = 0, part = 0; l0 < L; part + 1 < parts ? ++part : (part = 0, l0 += kGK)) {
         __syncthreads();
         for (int e = tid; e < kGT * kGK; e += 256) {
             // the thread order follows the contiguous index of each operand
             const int r = P == P_DW ? e % kGT : e / kGK, l = P == P_DW ? e / kGT : e % kGK;
-            As[r][l] = load_a(i0 + r, l0 + l);
+            As[r][l] = load_a(i0 + r, l0 + l, (int)part);
         }
         for (int e = tid; e < kGT * kGK; e += 256) {
             const int r = P == P_FWD ? e / kGK : e % kGT, l = P == P_FWD ? e % kGK : e / kGT;
@@ -148,11 +172,12 @@ constexpr int kFlat = 256;                     // granules (8 elements) of a fla
 
 struct Prep {
     pgq_linear_bwd b;            // the sources (codes, scales, x and their strides also in forward)
-    uint16_t* dz;                // M x Np, row stride ldn, or NULL: only the partial sums
+    uint16_t* dz;                // M x (parts x Np), row stride ldn, or NULL: only the partial sums
+    int32_t parts, what_parts;   // of dZ; copies of a row of what_t, one for each part that dX multiplies
     float* dbias_part;           // ceil(M / dz_rows) x N, or NULL
     int32_t dz_rows;             // rows of a dZ unit
     uint16_t* what;              // N x Kp, row stride ldk
-    uint16_t* what_t;            // K x Np, row stride ldn
+    uint16_t* what_t;            // K x (what_parts x Np), row stride ldn
     uint16_t* xc;                // M x Kp, row stride ldk
     int64_t Kp, Np, ldk, ldn;
     int64_t n_dz, n_what, n_what_t, n_x;      // units of each kind, in this order
@@ -249,10 +274,22 @@ __device__ __forceinline__ void prep_dz(const Prep& p, int64_t unit, float* sums
                     }
                 }
                 if (m < b.M) {
-                    if (p.dz)
-                        *(GLB u32x4*)(p.dz + m * p.ldn + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) t[e] += d[e];
+                    if (p.dz && p.parts == 1) {
+                        *(GLB u32x4*)(p.dz + m * p.ldn + n) = u32x4{pk_bf16(d[0], d[1]), pk_bf16(d[2], d[3]), pk_bf16(d[4], d[5]), pk_bf16(d[6], d[7])};
+                    } else if (p.dz) {
+                        float rest[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) rest[e] = d[e];
+#pragma unroll 1
+                        for (int part = 0; part < p.parts; ++part) {
+                            uint32_t h[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] = next_part(d[e], rest[e], part + 1 == p.parts);
+                            *(GLB u32x4*)(p.dz + m * p.ldn + part * p.Np + n) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+                        }
+                    }
                 }
             }
         }
@@ -299,7 +336,10 @@ __device__ __forceinline__ void prep_what_t(const Prep& p, int64_t unit, uint16_
     for (int c = 0; c < 2; ++c) {
         const int r = (tid >> 3) + 32 * c, g = tid & 7;
         const int64_t k = k0 + r, n = n0 + 8 * g;
-        if (k < b.K && n < p.Np) *(GLB u32x4*)(p.what_t + k * p.ldn + n) = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
+        if (k < b.K && n < p.Np) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
+            for (int part = 0; part < p.what_parts; ++part) *(GLB u32x4*)(p.what_t + k * p.ldn + part * p.Np + n) = v;
+        }
     }
 }
 
@@ -670,6 +710,7 @@ FwdPlan plan_fwd(const pgq_linear_fwd& p)
 struct BwdPlan {
     bool dx, dw, db;             // what there is to compute
     bool tile;                   // by the element-load kernel
+    int32_t parts, parts_dx, parts_dw;       // bf16 values that stand for a dZ: in scratch, in each product
     bool dz, copy_x;             // dZ and X go through scratch
     MmNt nt;                     // dX, dW: sizes, tiles and parts
     MmTt tt;
@@ -678,6 +719,20 @@ struct BwdPlan {
     int64_t blocks;              // row blocks of dZ units (and of the db partial sums)
     size_t o_dz, o_db, o_what_t, o_x, o_part, o_part_dx, bytes;
 };
+// The bf16 parts of dZ that a product with outputs of this type takes.  One is dZ where nothing multiplies a bf16
+// dY but 0 or powers of two; two are where a bf16 Z does (8 and 8 bits).  Otherwise two leave 2^-14 of dZ, a 64th of a
+// bf16 output's own rounding (one left 2^-8, and bf16 gradients 0.0024 off where their own rounding is 0.0017), and
+// three leave nothing: 24 bits.
+int32_t dz_parts(const pgq_linear_bwd& p, int32_t out_dtype)
+{
+    uint32_t slope;
+    memcpy(&slope, &p.slope, 4);
+    if (p.dy_dtype == PGQ_BF16) {
+        if (p.act == PGQ_ACT_NONE) return 1;
+        if (p.act != PGQ_ACT_SILU && (slope & 0x7FFFFFu) == 0) return p.act == PGQ_ACT_RELU ? 1 : 2;
+    }
+    return out_dtype == PGQ_F32 ? 3 : 2;
+}
 BwdPlan plan_bwd(const pgq_linear_bwd& p)
 {
     BwdPlan q;
@@ -685,7 +740,11 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     q.dx = p.dx && p.M > 0 && p.K > 0;
     q.dw = p.dw && p.N > 0 && p.K > 0;
     q.db = p.dbias && p.N > 0;
-    q.tile = p.N >= kLong || p.K >= kLong;
+    q.parts_dx = q.dx ? dz_parts(p, p.dx_dtype) : 1;
+    q.parts_dw = q.dw ? dz_parts(p, p.dw_dtype) : 1;
+    q.parts = std::max(q.parts_dx, q.parts_dw);
+    const int64_t Np = up8(p.N), ldn = pitch(q.parts * Np);
+    q.tile = ldn >= kLong || p.K >= kLong;
     auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += up256(n); return at; };
     // long units for few partial sums, short ones where there are not enough of them to fill the machine
     q.dz_rows = p.M * p.N >= (int64_t)4 << 20 ? 64 : 16;
@@ -693,14 +752,14 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     if (q.db) q.o_db = take((size_t)q.blocks * p.N * 4);
     if (q.tile || p.N == 0 || p.M == 0) return q;
     if (q.dx || q.dw) {
-        q.dz = p.act != PGQ_ACT_NONE || p.dy_dtype != PGQ_BF16 || !direct(p.dy, p.lddy, p.N);
-        if (q.dz) q.o_dz = take((size_t)p.M * pitch(p.N) * 2);
+        q.dz = p.act != PGQ_ACT_NONE || p.dy_dtype != PGQ_BF16 || !direct(p.dy, p.lddy, p.N);    // (else one part)
+        if (q.dz) q.o_dz = take((size_t)p.M * ldn * 2);
     }
     if (q.dx) {
-        q.o_what_t = take((size_t)p.K * pitch(p.N) * 2);
+        q.o_what_t = take((size_t)p.K * ldn * 2);
         q.nt.I = p.M;
         q.nt.J = p.K;
-        q.nt.L = up8(p.N);
+        q.nt.L = q.parts_dx * Np;
     }
     if (q.dw) {
         q.copy_x = !direct(p.x, p.ldx, p.K);
@@ -708,6 +767,8 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
         q.tt.I = p.N;
         q.tt.J = p.K;
         q.tt.L = p.M;
+        q.tt.parts = q.parts_dw;
+        q.tt.part_cols = Np;
     }
     if (q.dx && q.dw) q.both = mm_both_plan(q.nt, q.tt, (double)float_size(p.dx_dtype));
     else if (q.dx) mm_nt_plan(q.nt, false, (double)float_size(p.dx_dtype));
@@ -788,7 +849,8 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     }
     if (q.tile) {
         Launches l(1, stream);
-        void* args[] = {&f, &b};
+        int32_t parts = 1;
+        void* args[] = {&f, &b, &parts};
         l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_FWD>), tiles_of(f.M, f.N), 256, args);
         return l.done();
     }
@@ -862,7 +924,9 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     pr.Kp = up8(b.K);
     pr.Np = up8(b.N);
     pr.ldk = pitch(b.K);
-    pr.ldn = pitch(b.N);
+    pr.ldn = pitch(q.parts * pr.Np);
+    pr.parts = q.parts;
+    pr.what_parts = q.parts_dx;
     pr.dz = q.dz ? reinterpret_cast<uint16_t*>(ws + q.o_dz) : nullptr;
     pr.dz_rows = q.dz_rows;
     pr.dbias_part = q.db ? reinterpret_cast<float*>(ws + q.o_db) : nullptr;
@@ -886,9 +950,10 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     if (!mm) {
         pgq_linear_fwd f;
         memset(&f, 0, sizeof(f));
-        void* args[] = {&f, &b};
-        if (q.dx) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DX>), tiles_of(b.M, b.K), 256, args);
-        if (q.dw) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DW>), tiles_of(b.N, b.K), 256, args);
+        int32_t pdx = q.parts_dx, pdw = q.parts_dw;
+        void *xargs[] = {&f, &b, &pdx}, *wargs[] = {&f, &b, &pdw};
+        if (q.dx) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DX>), tiles_of(b.M, b.K), 256, xargs);
+        if (q.dw) l.go(reinterpret_cast<const void*>(&pgq_linear_tile_kernel<P_DW>), tiles_of(b.N, b.K), 256, wargs);
         return l.done();
     }
     MmNt x = q.nt;

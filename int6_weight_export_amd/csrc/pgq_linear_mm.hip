@@ -586,6 +586,8 @@ __device__ __forceinline__ void put4(const MmTt& p, int64_t i, int64_t j, f32x4 
         }
 }
 
+__host__ __device__ inline int64_t tt_stages(const MmTt& p) { return (p.L + 63) / 64 * p.parts; }
+
 template <int WR, int WC, int IB, int JB>
 constexpr int tt_lds() { return 2 * 64 * 2 * (32 * IB * WR + 32 * JB * WC); }
 
@@ -604,9 +606,12 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
     tile_of(wid, total, gi, gj, ti, tj, part);
     const uint32_t tile = ti * gj + tj;
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
-    const int64_t l0 = (int64_t)part * p.chunk;
-    const int64_t len = min(p.chunk, p.L - l0);
-    const int nst = len > 0 ? (int)((len + 63) / 64) : 0;
+    // this piece's stages: 64 rows of each part of A in turn, with the same rows of B (the second read of them is served
+    // by the cache)
+    const int64_t first = (int64_t)part * p.chunk;
+    const int nst = (int)min(p.chunk, tt_stages(p) - first);
+    int64_t row = first / p.parts * 64;          // of the stage that is issued next, and its part
+    int which = (int)(first % p.parts);
     const int ig = (int)min((int64_t)AG, (p.I - i0 + 7) / 8), jg = (int)min((int64_t)BG, (p.J - j0 + 7) / 8);
     uint32_t ao[AI], bo[BI];     // byte offsets of this thread's loads within a stage; columns past the edge are out of range
 #pragma unroll
@@ -622,10 +627,9 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
     auto issue = [&](int st) __attribute__((always_inline)) {
         uint8_t* la = lds + (st & 1) * (AS + BS);
         uint8_t* lb = la + AS;
-        const int64_t row = l0 + (int64_t)st * 64;
-        const int rows = (int)min((int64_t)64, l0 + len - row);
+        const int rows = (int)min((int64_t)64, p.L - row);
         // ranges over this stage's rows: the last one ends with its last used granule, rows past it are out of range
-        const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + row * p.lda + i0), 0, (int)((rows - 1) * p.lda * 2 + 16 * ig), 0x00020000);
+        const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + row * p.lda + which * p.part_cols + i0), 0, (int)((rows - 1) * p.lda * 2 + 16 * ig), 0x00020000);
         const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + row * p.ldb + j0), 0, (int)((rows - 1) * p.ldb * 2 + 16 * jg), 0x00020000);
 #pragma unroll
         for (int c = 0; c < AI; ++c)
@@ -633,6 +637,10 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
 #pragma unroll
         for (int c = 0; c < BI; ++c)
             load_lds(br, lb + (c * T + wave * 64) * 16, bo[c], 0);
+        if (++which == p.parts) {
+            which = 0;
+            row += 64;
+        }
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
     const int h = lane >> 5, r32 = lane & 31;
@@ -903,7 +911,7 @@ constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 32, 48
 void mm_tt_plan(MmTt& p)
 {
     double best = 0;
-    const int64_t stages = std::max<int64_t>(1, (p.L + 63) / 64);
+    const int64_t stages = std::max<int64_t>(1, tt_stages(p));
     for (int k = 0; k < (int)(sizeof(kTt) / sizeof(kTt[0])); ++k) {
         const TtKind& kind = kTt[k];
         const int64_t tiles = tt_tiles(kind, p.I, p.J);
@@ -917,7 +925,7 @@ void mm_tt_plan(MmTt& p)
                 best = t;
                 p.kind = k;
                 p.splits = (int32_t)parts;
-                p.chunk = per * 64;
+                p.chunk = per;
             }
         }
     }
@@ -965,7 +973,7 @@ int mm_both_plan(MmNt& x, MmTt& w, double out_bytes)
 {
     double best = 0;
     int chosen = 0;
-    const int64_t sx = std::max<int64_t>(1, (x.L + 63) / 64), sw = std::max<int64_t>(1, (w.L + 63) / 64);
+    const int64_t sx = std::max<int64_t>(1, (x.L + 63) / 64), sw = std::max<int64_t>(1, tt_stages(w));
     const double out = (double)x.I * (double)x.J * out_bytes / 5.3e6;
     for (int k = 0; k < (int)(sizeof(kBoth) / sizeof(kBoth[0])); ++k) {
         const BothKind& b = kBoth[k];
@@ -989,7 +997,7 @@ int mm_both_plan(MmNt& x, MmTt& w, double out_bytes)
                     x.splits = (int32_t)partx;
                     x.chunk = perx * 64;
                     w.splits = (int32_t)partw;
-                    w.chunk = perw * 64;
+                    w.chunk = perw;
                 }
             }
         }

@@ -505,7 +505,10 @@ def qlinear_backward(dy: torch.Tensor, codes: Optional[torch.Tensor], scales: Op
     mask bit is 0) and "dbias" fp32 [N], each when wanted; the residual's gradient is dy itself.
 
     dy: bf16 or fp32 [M, N]; z: the bf16 pre-activation of the forward call (not for act "none"); x:
-    bf16 [M, K] (for dw); codes, scales: as in qlinear (for dx); mask: uint8 [N, ceil(K / 8)]."""
+    bf16 [M, K] (for dw); codes, scales: as in qlinear (for dx); mask: uint8 [N, ceil(K / 8)].  dZ = dy act'(z)
+    is an fp32 value that enters the products in two bf16 parts (at most 2^-14 of it is lost) for a bf16 gradient and
+    in three (nothing is) for an fp32 one; one is enough, and takes about half as long, where it is a bf16 value:
+    a bf16 dy with act "none", or with "relu" and a slope of 0 or a power of two."""
     if dy.dim() != 2:
         raise ValueError("dy must be a matrix")
     (M, N), dev = dy.shape, _gpu_of("dy", dy)

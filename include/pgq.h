@@ -75,6 +75,7 @@ typedef enum {
 #define PGQ_DEV_F16_OVF     4u   /* an fp16 passthrough value rounded to infinity */
 #define PGQ_DEV_BAD_AWQ     8u   /* an AWQ activation scale is <= 0 or not finite */
 #define PGQ_DEV_STALE_TABLE 16u  /* PGQ_TABLE_RESIDENT given but the workspace holds another table; nothing was written */
+#define PGQ_DEV_NO_HYPER    32u  /* AdamW constants in device memory that no step number makes (zeros); nothing was written */
 
 /* Element types.  Weight inputs may be any of the three; dequantized outputs PGQ_F32 or
  * PGQ_BF16.  fp16 weights are widened to binary32 exactly before every step. */
@@ -460,7 +461,8 @@ pgq_status pgq_adamw_workspace(const pgq_adamw_tensor* t, int32_t n, size_t* wor
 /* state_bits: 32 or 8.  grad: host array of n device pointers (numel dense values of g_dtype).  They and
  * g_dtype may change from call to call: they are kernel arguments, not part of the table.  h: host, read during the
  * call -- or, when h_dev is not NULL, h is ignored and the kernel reads the constants from device memory,
- * so that a recorded graph can be replayed with those of each step.  workspace: 64-byte aligned; flags: 0
+ * so that a recorded graph can be replayed with those of each step.  Constants whose ib1 or ib2 is not positive
+ * (memory that none were written to) are PGQ_ERR_PARAM from the host, PGQ_DEV_NO_HYPER on the device.  workspace: 64-byte aligned; flags: 0
  * or PGQ_TABLE_RESIDENT as for the other grouped calls.  While the stream is being captured only a resident
  * table is accepted (PGQ_ERR_PARAM otherwise): its upload would be replayed from freed host memory.  No
  * two tensors may overlap. */

@@ -64,6 +64,9 @@ struct AdArgs {
     uint32_t first_desc;                          // tensors before its pointers
 };
 
+// Constants of a step have ib1, ib2 >= 1; zeros (never written) would make every weight 0 / 0 and clear the states.
+__host__ __device__ inline bool is_step(const pgq_adamw_hyper& h) { return h.ib1 > 0.0f && h.ib2 > 0.0f; }
+
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
@@ -171,6 +174,10 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
     const AdDesc d = a.table[di];
     const void* grad = grads.p[di - a.first_desc];
     const pgq_adamw_hyper h = a.h_dev ? *a.h_dev : a.h;
+    if (!is_step(h)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, PGQ_DEV_NO_HYPER);
+        return;
+    }
     const float lr = d.lr_scale * h.lr;
     const float step = lr * h.ib1;
     const float keep = 1.0f - lr * d.weight_decay;
@@ -457,6 +464,7 @@ pgq_status run(const pgq_adamw_tensor* t, int32_t n, int32_t bits, uint64_t tile
 {
     if (!workspace || workspace_bytes < table_size(n, tiles)) return PGQ_ERR_WORKSPACE;
     if (!is_aligned(workspace, 64)) return PGQ_ERR_ALIGN;
+    if (h && !is_step(*h)) return PGQ_ERR_PARAM;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint64_t sum;
     if (flags & PGQ_TABLE_RESIDENT) {

@@ -623,7 +623,7 @@ class AdamW:
         self.workspace = torch.empty(max(need.value, 64), dtype=torch.uint8, device=self.device)
         self.status = new_status(self.device)
         self.hyper = torch.zeros(10, dtype=torch.int32, device=self.device)
-        self._uploaded = False
+        self._uploaded = self._loaded = False
         self._index = _gpu_of("weight", self.weights[0])
         self._numel = [w.numel() for w in self.weights]
         self._ptrs = (ctypes.c_void_p * n)()
@@ -635,19 +635,22 @@ class AdamW:
             return tuple(torch.zeros(k, dtype=torch.float32, device=self.device) for _ in range(2))
         return tuple(torch.zeros(m, dtype=torch.uint8, device=self.device) for m in (k, k, (k + 63) // 64, (k + 63) // 64))
 
-    def _hyper(self, lr, grad_scale: float) -> pgq.pgq_adamw_hyper:
+    def _hyper(self, lr, grad_scale: float, count: int) -> pgq.pgq_adamw_hyper:
+        """The constants of step number `count`."""
         h = pgq.pgq_adamw_hyper()
         pgq.check(pgq.pgq_adamw_hyper_at(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
-                                         self.step_count, grad_scale, (self.seed + self.step_count) & 0xFFFFFFFF,
+                                         count, grad_scale, (self.seed + count) & 0xFFFFFFFF,
                                          ctypes.byref(h)), "pgq_adamw_hyper_at")
         return h
 
     def load_hyper(self, lr: Optional[float] = None, grad_scale: float = 1.0) -> None:
         """Count a step and write its constants to device memory, for a step that reads them there
-        (device_hyper=True): before each replay of a graph that holds such a step."""
+        (device_hyper=True): before each replay of a graph that holds such a step.  A replay before the first
+        load_hyper changes nothing and sets PGQ_DEV_NO_HYPER in `status`."""
+        h = self._hyper(lr, grad_scale, self.step_count + 1)
+        self.hyper.copy_(torch.frombuffer(bytearray(bytes(h)), dtype=torch.int32))
         self.step_count += 1
-        host = torch.frombuffer(bytearray(bytes(self._hyper(lr, grad_scale))), dtype=torch.int32)
-        self.hyper.copy_(host)
+        self._loaded = True
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
              device_hyper: bool = False) -> None:
@@ -658,6 +661,8 @@ class AdamW:
             raise ValueError(f"{len(grads)} gradients for {self.n} weights")
         if not device_hyper and torch.cuda.is_current_stream_capturing():
             raise pgq.PgqError(pgq.PGQ_ERR_PARAM, "a captured step takes its constants from the device (device_hyper=True)")
+        if device_hyper and not self._loaded and not torch.cuda.is_current_stream_capturing():
+            raise pgq.PgqError(pgq.PGQ_ERR_PARAM, "device_hyper: load_hyper has not written any constants")
         ptrs, numel, types, index = self._ptrs, self._numel, self._g_dtypes, self._index
         for i, g in enumerate(grads):
             if g.numel() != numel[i] or not g.is_contiguous():
@@ -668,15 +673,10 @@ class AdamW:
             if g.dtype is not types[i]:
                 self._arr[i].g_dtype = _dtype_code(g.dtype)
                 types[i] = g.dtype
+        h = None if device_hyper else self._hyper(lr, grad_scale, self.step_count + 1)
+        self._on_device(self._enqueue_step, h, ptrs)
         if not device_hyper:
             self.step_count += 1
-        try:
-            h = None if device_hyper else self._hyper(lr, grad_scale)
-            self._on_device(self._enqueue_step, h, ptrs)
-        except pgq.PgqError:
-            if not device_hyper:
-                self.step_count -= 1
-            raise
         self._uploaded = True
 
     def _enqueue_step(self, h, ptrs) -> None:

@@ -27,6 +27,7 @@ PGQ_DEV_SCALE_OVF = 2
 PGQ_DEV_F16_OVF = 4
 PGQ_DEV_BAD_AWQ = 8
 PGQ_DEV_STALE_TABLE = 16
+PGQ_DEV_NO_HYPER = 32
 
 PGQ_F32 = 0
 PGQ_BF16 = 1

@@ -451,7 +451,7 @@ typedef struct {
     uint32_t seed;           /* of the stochastic rounding; another one each step */
 } pgq_adamw_hyper;
 
-/* Host only: the constants of step number `step` (1-based).  0 <= beta < 1, lr, eps >= 0 and finite. */
+/* Host only: the constants of step number `step` (1-based).  0 <= beta < 1; lr, eps >= 0 and finite in binary32. */
 pgq_status pgq_adamw_hyper_at(double lr, double beta1, double beta2, double eps, int64_t step, float grad_scale,
                               uint32_t seed, pgq_adamw_hyper* out);
 

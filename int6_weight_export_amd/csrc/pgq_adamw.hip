@@ -539,7 +539,7 @@ pgq_status pgq_adamw_hyper_at(double lr, double beta1, double beta2, double eps,
                               uint32_t seed, pgq_adamw_hyper* out)
 {
     if (!out) return PGQ_ERR_NULL;
-    if (!(lr >= 0 && lr < INFINITY) || !(eps >= 0 && eps < INFINITY) || !(beta1 >= 0 && beta1 < 1) ||
+    if (!(lr >= 0 && (float)lr < INFINITY) || !(eps >= 0 && (float)eps < INFINITY) || !(beta1 >= 0 && beta1 < 1) ||
         !(beta2 >= 0 && beta2 < 1) || step < 1)
         return PGQ_ERR_PARAM;
     memset(out, 0, sizeof(*out));

@@ -19,3 +19,13 @@ def step(h):
 def test_constants_of_no_step_are_refused(kw):
     """Zeroed constants would make every weight 0 / 0 and clear the states."""
     assert step(pgq.pgq_adamw_hyper(lr=0.1, **kw)) == pgq.PGQ_ERR_PARAM
+
+
+@pytest.mark.parametrize("kw", [dict(lr=3.5e38), dict(lr=1e300), dict(eps=1e39)])
+def test_constants_that_binary32_cannot_hold_are_refused(kw):
+    """Finite numbers that round to a binary32 infinity would make every weight NaN."""
+    a = dict(lr=1e-3, eps=1e-8)
+    a.update(kw)
+    h = pgq.pgq_adamw_hyper()
+    assert pgq.pgq_adamw_hyper_at(a["lr"], 0.9, 0.999, a["eps"], 1, 1.0, 0, ctypes.byref(h)) == pgq.PGQ_ERR_PARAM
+    assert pgq.pgq_adamw_hyper_at(3.4e38, 0.9, 0.999, 1e-8, 1, 1.0, 0, ctypes.byref(h)) == pgq.PGQ_OK

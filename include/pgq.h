@@ -367,7 +367,8 @@ pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* worksp
 
 /* workspace: device memory of at least that many bytes, 256-byte aligned (NULL when 0); its content
  * is of no account before and after the call, and calls that run at the same time need one each.
- * p is read during the call only.  M = 0 or N = 0 writes no Y; K = 0 makes Z the bias.  In backward
+ * p is read during the call only.  A call one of whose launches would pass 2^32 threads is PGQ_ERR_SHAPE (N of 2^27
+ * and more for up to 16 tokens; operands of more than 2^34 elements), from both functions.  M = 0 or N = 0 writes no Y; K = 0 makes Z the bias.  In backward
  * an empty sum (N = 0 for dX, M = 0 for dW and db) is +0.  May be recorded into a HIP graph.
  * What a call writes may share no memory with its other arguments (y as its own residual apart):
  * PGQ_ERR_PARAM, also for matrices of different row strides whose ranges of memory meet.  Columns of
@@ -465,7 +466,7 @@ pgq_status pgq_adamw_workspace(const pgq_adamw_tensor* t, int32_t n, size_t* wor
  * (memory that none were written to) are PGQ_ERR_PARAM from the host, PGQ_DEV_NO_HYPER on the device.  workspace: 64-byte aligned; flags: 0
  * or PGQ_TABLE_RESIDENT as for the other grouped calls.  While the stream is being captured only a resident
  * table is accepted (PGQ_ERR_PARAM otherwise): its upload would be replayed from freed host memory.  No
- * two tensors may overlap. */
+ * two tensors may overlap, and no gradient any of them.  PGQ_ERR_SHAPE past 2^36 elements in all. */
 pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bits, const void* const* grad,
                           const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, void* workspace,
                           size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream);

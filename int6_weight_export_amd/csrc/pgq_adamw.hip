@@ -393,7 +393,7 @@ pgq_status check_tensors(const pgq_adamw_tensor* t, int32_t n, int32_t bits, uin
         if (x.copy && x.w_dtype != PGQ_F32) return PGQ_ERR_DTYPE;
         if (!(x.lr_scale - x.lr_scale == 0.0f) || !(x.weight_decay - x.weight_decay == 0.0f)) return PGQ_ERR_PARAM;
         *tiles += (uint64_t)((x.numel + kTile - 1) / kTile);
-        if (*tiles > 0x7FFFFFFFull) return PGQ_ERR_SHAPE;
+        if (*tiles * kThreads > 0xFFFFFFFFull) return PGQ_ERR_SHAPE;       // a launch's limit: 2^32 - 1 threads
         if (x.numel == 0) continue;
         if (!x.w || !x.m || !x.v || (bits == 8 && (!x.m_scale || !x.v_scale))) return PGQ_ERR_NULL;
         if (!is_aligned(x.w, x.w_dtype == PGQ_F32 ? 4 : 2) || (x.copy && !is_aligned(x.copy, 2)) ||
@@ -565,7 +565,7 @@ pgq_status pgq_adamw_workspace(const pgq_adamw_tensor* t, int32_t n, size_t* wor
     for (int32_t i = 0; i < n; ++i) {
         if (t[i].numel < 0 || t[i].numel > kMaxNumel) return PGQ_ERR_SHAPE;
         tiles += (uint64_t)((t[i].numel + kTile - 1) / kTile);
-        if (tiles > 0x7FFFFFFFull) return PGQ_ERR_SHAPE;
+        if (tiles * kThreads > 0xFFFFFFFFull) return PGQ_ERR_SHAPE;
     }
     *workspace_bytes = table_size(n, tiles);
     return PGQ_OK;

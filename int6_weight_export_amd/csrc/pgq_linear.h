@@ -34,10 +34,17 @@ __device__ __forceinline__ float act_slope(int32_t act, float slope, float z)
     return act == PGQ_ACT_RELU ? d : 2.0f * z * d * d;
 }
 
-// One launch of a linear grid; one past the runtime's limits (2^31 - 1 workgroups, 2^32 - 1 threads) is an error.
+// The runtime's limits: 2^31 - 1 workgroups, 2^32 - 1 threads.  A call one of whose launches would pass them is
+// refused before the first.
+inline bool grid_fits(int64_t grid, int block) { return grid <= 0x7FFFFFFF && grid * block <= 0xFFFFFFFFll; }
+// One launch of a linear grid; a refused one leaves no timing events for the thread's next call.
 inline hipError_t launch_grid(const void* fn, int64_t grid, int block, void** args, void* stream)
 {
-    if (grid > 0x7FFFFFFF || grid * block > 0xFFFFFFFFll) return hipErrorInvalidValue;
+    if (!grid_fits(grid, block)) {
+        void *start, *stop;
+        take_timing_events(&start, &stop);
+        return hipErrorInvalidValue;
+    }
     return launch_plain(fn, dim3((unsigned)grid), dim3((unsigned)block), args, stream);
 }
 
@@ -71,6 +78,7 @@ struct MmNt {
 // of Y; returns the estimated microseconds
 double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes);
 size_t mm_nt_partial_bytes(const MmNt& p);
+bool mm_nt_fits(const MmNt& p);          // its launches are within the runtime's limits
 hipError_t launch_mm_nt(const MmNt& p, void* stream);
 // splits > 1: the sums of the parts, in their order, through the epilogue
 hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream);
@@ -93,6 +101,7 @@ struct MmTt {
 };
 void mm_tt_plan(MmTt& p);        // kind, splits and chunk from I, J, L and parts
 size_t mm_tt_partial_bytes(const MmTt& p);
+bool mm_tt_fits(const MmTt& p);
 hipError_t launch_mm_tt(const MmTt& p, void* stream);
 // splits > 1: the sum of the parts, in their order
 hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream);
@@ -103,9 +112,11 @@ struct Dbias {
     int64_t blocks, N;
     float* out;                  // NULL: nothing to do
 };
+bool mm_dbias_fits(int64_t N);
 hipError_t launch_mm_dbias(const Dbias& d, void* stream);
 // dX, dW and db in one launch: the pair of tiles, with kind, splits and chunk of both products.
 int mm_both_plan(MmNt& x, MmTt& w, double out_bytes);
+bool mm_both_fits(const MmNt& x, const MmTt& w, int64_t db_cols);
 hipError_t launch_mm_both(int both, const MmNt& x, const MmTt& w, const Dbias& d, void* stream);
 
 }  // namespace pgq

@@ -778,6 +778,39 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     return q;
 }
 
+// Workgroups of the preparation, the element-load kernel and the few-token kernel
+int64_t flat_units(int64_t rows, int64_t cols) { return (rows * (up8(cols) / 8) + kFlat - 1) / kFlat; }
+int64_t dz_units(const pgq_linear_bwd& p, const BwdPlan& q) { return q.dz || q.db ? q.blocks * ((up8(p.N) + kDzCols - 1) / kDzCols) : 0; }
+int64_t what_t_units(const pgq_linear_bwd& p) { return ((up8(p.N) + 63) / 64) * ((p.K + 63) / 64); }
+int64_t skinny_grid(const pgq_linear_fwd& p, const Parts& parts) { return (p.N + 15) / 16 * parts.n; }
+int64_t join_grid(const pgq_linear_fwd& p) { return (p.M * p.N + 255) / 256; }
+int64_t prep_units(const pgq_linear_fwd& p, const FwdPlan& q)
+{
+    return (q.nt.from_codes ? 0 : flat_units(p.N, p.K)) + (q.copy_x ? flat_units(p.M, p.K) : 0);
+}
+int64_t prep_units(const pgq_linear_bwd& p, const BwdPlan& q)
+{
+    const bool mm = !q.tile && p.M > 0 && p.N > 0;
+    return dz_units(p, q) + (mm && q.dx ? what_t_units(p) : 0) + (mm && q.copy_x ? flat_units(p.M, p.K) : 0);
+}
+// Every launch of the call is within the runtime's limits.
+bool launches_fit(const pgq_linear_fwd& p, const FwdPlan& q)
+{
+    if (p.M == 0 || p.N == 0) return true;
+    if (q.skinny) return grid_fits(skinny_grid(p, q.parts), 64 * kSkinnyWaves) && (q.parts.n == 1 || grid_fits(join_grid(p), 256));
+    if (q.tile) return grid_fits(tiles_of(p.M, p.N), 256);
+    return grid_fits(prep_units(p, q), 256) && mm_nt_fits(q.nt);
+}
+bool launches_fit(const pgq_linear_bwd& p, const BwdPlan& q)
+{
+    const bool mm = !q.tile && p.M > 0 && p.N > 0;
+    if (!grid_fits(prep_units(p, q), 256)) return false;
+    if (mm && q.dx && q.dw) return mm_both_fits(q.nt, q.tt, q.db ? p.N : 0);
+    if (q.db && !mm_dbias_fits(p.N)) return false;
+    if (!mm) return (!q.dx || grid_fits(tiles_of(p.M, p.K), 256)) && (!q.dw || grid_fits(tiles_of(p.N, p.K), 256));
+    return (!q.dx || mm_nt_fits(q.nt)) && (!q.dw || mm_tt_fits(q.tt));
+}
+
 // The launches of one call: the first takes a pending start event, the last the stop event.
 struct Launches {
     void *start = nullptr, *stop = nullptr, *stream;
@@ -812,16 +845,22 @@ pgq_status pgq_linear_forward_workspace(const pgq_linear_fwd* p, size_t* workspa
 {
     if (!workspace_bytes) return PGQ_ERR_NULL;
     const pgq_status st = check_fwd(p);
-    if (st == PGQ_OK) *workspace_bytes = plan_fwd(*p).bytes;
-    return st;
+    if (st != PGQ_OK) return st;
+    const FwdPlan q = plan_fwd(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
+    *workspace_bytes = q.bytes;
+    return PGQ_OK;
 }
 
 pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* workspace_bytes)
 {
     if (!workspace_bytes) return PGQ_ERR_NULL;
     const pgq_status st = check_bwd(p);
-    if (st == PGQ_OK) *workspace_bytes = plan_bwd(*p).bytes;
-    return st;
+    if (st != PGQ_OK) return st;
+    const BwdPlan q = plan_bwd(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
+    *workspace_bytes = q.bytes;
+    return PGQ_OK;
 }
 
 pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t workspace_bytes, void* stream)
@@ -829,6 +868,7 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     const pgq_status st = check_fwd(p);
     if (st != PGQ_OK || p->M == 0 || p->N == 0) return st;
     const FwdPlan q = plan_fwd(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
     if (q.bytes && (!workspace || workspace_bytes < q.bytes)) return PGQ_ERR_WORKSPACE;
     if (q.bytes && !is_aligned(workspace, 256)) return PGQ_ERR_ALIGN;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -843,8 +883,8 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
         const void* k = f.M <= 16   ? reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<1>)
                         : f.M <= 32 ? reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<2>)
                                     : reinterpret_cast<const void*>(&pgq_linear_skinny_kernel<4>);
-        l.go(k, (f.N + 15) / 16 * parts.n, 64 * kSkinnyWaves, args);
-        if (parts.n > 1) l.go(reinterpret_cast<const void*>(&pgq_linear_join_kernel), (f.M * f.N + 255) / 256, 256, args);
+        l.go(k, skinny_grid(f, parts), 64 * kSkinnyWaves, args);
+        if (parts.n > 1) l.go(reinterpret_cast<const void*>(&pgq_linear_join_kernel), join_grid(f), 256, args);
         return l.done();
     }
     if (q.tile) {
@@ -871,11 +911,11 @@ pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t w
     pr.ldk = pitch(f.K);
     if (!q.nt.from_codes) {
         pr.what = reinterpret_cast<uint16_t*>(ws + q.what);
-        pr.n_what = (f.N * (pr.Kp / 8) + kFlat - 1) / kFlat;
+        pr.n_what = flat_units(f.N, f.K);
     }
     if (q.copy_x) {
         pr.xc = reinterpret_cast<uint16_t*>(ws + q.xc);
-        pr.n_x = (f.M * (pr.Kp / 8) + kFlat - 1) / kFlat;
+        pr.n_x = flat_units(f.M, f.K);
     }
     void* args[] = {&pr};
     if (prep) l.go(reinterpret_cast<const void*>(&pgq_linear_prep_kernel), pr.n_what + pr.n_x, 256, args);
@@ -912,6 +952,7 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     if (st != PGQ_OK) return st;
     const BwdPlan q = plan_bwd(*p);
     if (!q.dx && !q.dw && !q.db) return PGQ_OK;
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
     if (q.bytes && (!workspace || workspace_bytes < q.bytes)) return PGQ_ERR_WORKSPACE;
     if (q.bytes && !is_aligned(workspace, 256)) return PGQ_ERR_ALIGN;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -930,14 +971,14 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     pr.dz = q.dz ? reinterpret_cast<uint16_t*>(ws + q.o_dz) : nullptr;
     pr.dz_rows = q.dz_rows;
     pr.dbias_part = q.db ? reinterpret_cast<float*>(ws + q.o_db) : nullptr;
-    if (q.dz || q.db) pr.n_dz = q.blocks * ((pr.Np + kDzCols - 1) / kDzCols);
+    pr.n_dz = dz_units(b, q);
     if (mm && q.dx) {
         pr.what_t = reinterpret_cast<uint16_t*>(ws + q.o_what_t);
-        pr.n_what_t = ((pr.Np + 63) / 64) * ((b.K + 63) / 64);
+        pr.n_what_t = what_t_units(b);
     }
     if (mm && q.copy_x) {
         pr.xc = reinterpret_cast<uint16_t*>(ws + q.o_x);
-        pr.n_x = (b.M * (pr.Kp / 8) + kFlat - 1) / kFlat;
+        pr.n_x = flat_units(b.M, b.K);
     }
     const int64_t units = pr.n_dz + pr.n_what_t + pr.n_x;
     const bool reduce = mm && q.dw && q.tt.splits > 1, reduce_dx = mm && q.dx && q.nt.splits > 1;

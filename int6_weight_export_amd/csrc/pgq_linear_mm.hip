@@ -887,10 +887,18 @@ size_t mm_nt_partial_bytes(const MmNt& p)
     return p.splits > 1 ? (size_t)p.splits * (size_t)nt_tiles(k, p.I, p.J) * k.ti * k.tj * 4 : 0;
 }
 
+static int64_t nt_grid(const MmNt& p) { return nt_tiles(kNt[p.kind], p.I, p.J) * p.splits; }
+static int64_t nt_reduce_grid(const MmNt& p)
+{
+    const NtKind& k = kNt[p.kind];
+    return p.splits > 1 ? nt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4 : 0;
+}
+bool mm_nt_fits(const MmNt& p) { return grid_fits(nt_grid(p), kNt[p.kind].threads) && grid_fits(nt_reduce_grid(p), 256); }
+
 hipError_t launch_mm_nt(const MmNt& p, void* stream)
 {
     const NtKind& k = kNt[p.kind];
-    const int64_t grid = nt_tiles(k, p.I, p.J) * p.splits;
+    const int64_t grid = nt_grid(p);
     MmNt copy = p;
     void* args[] = {&copy};
     return launch_grid(p.e.y_dtype == PGQ_F32 ? k.f32 : k.bf16, grid, k.threads, args, stream);
@@ -899,7 +907,7 @@ hipError_t launch_mm_nt(const MmNt& p, void* stream)
 hipError_t launch_mm_nt_reduce(const MmNt& p, void* stream)
 {
     const NtKind& k = kNt[p.kind];
-    const int64_t grid = nt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4;
+    const int64_t grid = nt_reduce_grid(p);
     MmNt copy = p;
     void* args[] = {&copy};
     return launch_grid(k.reduce, grid, 256, args, stream);
@@ -1008,11 +1016,26 @@ int mm_both_plan(MmNt& x, MmTt& w, double out_bytes)
     return chosen;
 }
 
+static int64_t tt_grid(const MmTt& p) { return tt_tiles(kTt[p.kind], p.I, p.J) * p.splits; }
+static int64_t tt_reduce_grid(const MmTt& p)               // a wavefront: 8 rows of 32 columns
+{
+    const TtKind& k = kTt[p.kind];
+    return p.splits > 1 ? tt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4 : 0;
+}
+static int64_t dbias_grid(int64_t N) { return (N + 63) / 64; }
+bool mm_tt_fits(const MmTt& p) { return grid_fits(tt_grid(p), kTt[p.kind].threads) && grid_fits(tt_reduce_grid(p), 256); }
+bool mm_dbias_fits(int64_t N) { return grid_fits(dbias_grid(N), 1024); }
+bool mm_both_fits(const MmNt& x, const MmTt& w, int64_t db_cols)
+{
+    return grid_fits(nt_grid(x) + tt_grid(w) + dbias_grid(db_cols), kNt[x.kind].threads) && grid_fits(nt_reduce_grid(x), 256) &&
+           grid_fits(tt_reduce_grid(w), 256);
+}
+
 hipError_t launch_mm_both(int both, const MmNt& x, const MmTt& w, const Dbias& d, void* stream)
 {
     const BothKind& b = kBoth[both];
-    const int64_t nx = nt_tiles(kNt[x.kind], x.I, x.J) * x.splits, nw = tt_tiles(kTt[w.kind], w.I, w.J) * w.splits;
-    const int64_t grid = nx + nw + (d.out ? (d.N + 63) / 64 : 0);
+    const int64_t nx = nt_grid(x), nw = tt_grid(w);
+    const int64_t grid = nx + nw + (d.out ? dbias_grid(d.N) : 0);
     MmNt cx = x;
     MmTt cw = w;
     Dbias cd = d;
@@ -1025,7 +1048,7 @@ hipError_t launch_mm_dbias(const Dbias& d, void* stream)
 {
     Dbias copy = d;
     void* args[] = {&copy};
-    return launch_grid(reinterpret_cast<const void*>(&pgq_mm_dbias_kernel), (d.N + 63) / 64, 1024, args, stream);
+    return launch_grid(reinterpret_cast<const void*>(&pgq_mm_dbias_kernel), dbias_grid(d.N), 1024, args, stream);
 }
 
 size_t mm_tt_partial_bytes(const MmTt& p)
@@ -1037,7 +1060,7 @@ size_t mm_tt_partial_bytes(const MmTt& p)
 hipError_t launch_mm_tt(const MmTt& p, void* stream)
 {
     const TtKind& k = kTt[p.kind];
-    const int64_t grid = tt_tiles(k, p.I, p.J) * p.splits;
+    const int64_t grid = tt_grid(p);
     MmTt copy = p;
     void* args[] = {&copy};
     return launch_grid(k.kernel, grid, k.threads, args, stream);
@@ -1046,7 +1069,7 @@ hipError_t launch_mm_tt(const MmTt& p, void* stream)
 hipError_t launch_mm_tt_reduce(const MmTt& p, void* stream)
 {
     const TtKind& k = kTt[p.kind];
-    const int64_t grid = tt_tiles(k, p.I, p.J) * (k.ti * k.tj / 256) / 4;      // a wavefront: 8 rows of 32 columns
+    const int64_t grid = tt_reduce_grid(p);
     MmTt copy = p;
     void* args[] = {&copy};
     return launch_grid(k.reduce, grid, 256, args, stream);

@@ -376,6 +376,24 @@ pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* worksp
 pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t workspace_bytes, void* stream);
 pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Planning aid, host only: how the calls above would run.  No part of the method: the choices follow measured   */
+/* costs and change with the kernels, so use it to see or to test which one a size gets, not to rely on it. */
+#define PGQ_LINEAR_EMPTY    0   /* no product */
+#define PGQ_LINEAR_FEW      1   /* few tokens: 16 weight rows a workgroup */
+#define PGQ_LINEAR_ELEMENTS 2   /* the kernel for every size and stride */
+#define PGQ_LINEAR_TILES    3   /* the matrix kernels */
+typedef struct {
+    int32_t path;                        /* PGQ_LINEAR_* */
+    int32_t tile_rows, tile_cols, parts; /* of Y (forward) or dX, 0 where there is none; parts the sum is cut into */
+    int32_t from_codes;                  /* 1: tiles read the codes, no laid-out weights */
+    int32_t copies_x;                    /* 1: X is laid out first */
+    int32_t dw_rows, dw_cols, dw_parts;  /* of dW */
+    int32_t joint;                       /* 1: dX, dW and db in one launch */
+    int32_t dz_dx, dz_dw;                /* bf16 values that stand for a dZ in each product */
+} pgq_linear_plan;
+pgq_status pgq_linear_forward_plan(const pgq_linear_fwd* p, pgq_linear_plan* out);
+pgq_status pgq_linear_backward_plan(const pgq_linear_bwd* p, pgq_linear_plan* out);
+
 /* ------------------------------------------------------------------------------------------ */
 /* Weight averaging without quantization, grouped over n tensors in one launch.               */
 /* w[i]: the weights (fp32 or bf16, rows x cols, row stride ld; awq_s must be NULL; name is    */

@@ -78,6 +78,7 @@ struct MmNt {
 // of Y; returns the estimated microseconds
 double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes);
 size_t mm_nt_partial_bytes(const MmNt& p);
+void mm_nt_tile(const MmNt& p, int32_t* rows, int32_t* cols);
 bool mm_nt_fits(const MmNt& p);          // its launches are within the runtime's limits
 hipError_t launch_mm_nt(const MmNt& p, void* stream);
 // splits > 1: the sums of the parts, in their order, through the epilogue
@@ -101,6 +102,7 @@ struct MmTt {
 };
 void mm_tt_plan(MmTt& p);        // kind, splits and chunk from I, J, L and parts
 size_t mm_tt_partial_bytes(const MmTt& p);
+void mm_tt_tile(const MmTt& p, int32_t* rows, int32_t* cols);
 bool mm_tt_fits(const MmTt& p);
 hipError_t launch_mm_tt(const MmTt& p, void* stream);
 // splits > 1: the sum of the parts, in their order

@@ -863,6 +863,52 @@ pgq_status pgq_linear_backward_workspace(const pgq_linear_bwd* p, size_t* worksp
     return PGQ_OK;
 }
 
+pgq_status pgq_linear_forward_plan(const pgq_linear_fwd* p, pgq_linear_plan* out)
+{
+    if (!out) return PGQ_ERR_NULL;
+    const pgq_status st = check_fwd(p);
+    if (st != PGQ_OK) return st;
+    const FwdPlan q = plan_fwd(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
+    memset(out, 0, sizeof(*out));
+    if (p->M == 0 || p->N == 0) return PGQ_OK;
+    out->path = q.skinny ? PGQ_LINEAR_FEW : q.tile ? PGQ_LINEAR_ELEMENTS : PGQ_LINEAR_TILES;
+    out->parts = q.skinny ? q.parts.n : 1;
+    if (out->path == PGQ_LINEAR_TILES) {
+        mm_nt_tile(q.nt, &out->tile_rows, &out->tile_cols);
+        out->parts = q.nt.splits;
+        out->from_codes = q.nt.from_codes;
+        out->copies_x = q.copy_x;
+    }
+    return PGQ_OK;
+}
+
+pgq_status pgq_linear_backward_plan(const pgq_linear_bwd* p, pgq_linear_plan* out)
+{
+    if (!out) return PGQ_ERR_NULL;
+    const pgq_status st = check_bwd(p);
+    if (st != PGQ_OK) return st;
+    const BwdPlan q = plan_bwd(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
+    memset(out, 0, sizeof(*out));
+    if (!q.dx && !q.dw) return PGQ_OK;
+    out->path = q.tile || p->M == 0 || p->N == 0 ? PGQ_LINEAR_ELEMENTS : PGQ_LINEAR_TILES;
+    out->dz_dx = q.dx ? q.parts_dx : 0;
+    out->dz_dw = q.dw ? q.parts_dw : 0;
+    if (out->path != PGQ_LINEAR_TILES) return PGQ_OK;
+    if (q.dx) {
+        mm_nt_tile(q.nt, &out->tile_rows, &out->tile_cols);
+        out->parts = q.nt.splits;
+    }
+    if (q.dw) {
+        mm_tt_tile(q.tt, &out->dw_rows, &out->dw_cols);
+        out->dw_parts = q.tt.splits;
+    }
+    out->copies_x = q.copy_x;
+    out->joint = q.dx && q.dw;
+    return PGQ_OK;
+}
+
 pgq_status pgq_linear_forward(const pgq_linear_fwd* p, void* workspace, size_t workspace_bytes, void* stream)
 {
     const pgq_status st = check_fwd(p);

@@ -887,6 +887,16 @@ size_t mm_nt_partial_bytes(const MmNt& p)
     return p.splits > 1 ? (size_t)p.splits * (size_t)nt_tiles(k, p.I, p.J) * k.ti * k.tj * 4 : 0;
 }
 
+void mm_nt_tile(const MmNt& p, int32_t* rows, int32_t* cols)
+{
+    *rows = kNt[p.kind].ti;
+    *cols = kNt[p.kind].tj;
+}
+void mm_tt_tile(const MmTt& p, int32_t* rows, int32_t* cols)
+{
+    *rows = kTt[p.kind].ti;
+    *cols = kTt[p.kind].tj;
+}
 static int64_t nt_grid(const MmNt& p) { return nt_tiles(kNt[p.kind], p.I, p.J) * p.splits; }
 static int64_t nt_reduce_grid(const MmNt& p)
 {

@@ -44,6 +44,11 @@ PGQ_ACT_RELU = 1
 PGQ_ACT_RELU2 = 2
 PGQ_ACT_SILU = 3
 
+PGQ_LINEAR_EMPTY = 0
+PGQ_LINEAR_FEW = 1
+PGQ_LINEAR_ELEMENTS = 2
+PGQ_LINEAR_TILES = 3
+
 
 class PgqError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
@@ -104,6 +109,11 @@ class pgq_linear_bwd(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class pgq_linear_plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("path", "tile_rows", "tile_cols", "parts", "from_codes", "copies_x", "dw_rows",
+                                              "dw_cols", "dw_parts", "joint", "dz_dx", "dz_dw")]
+
+
 class pgq_adamw_tensor(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("numel", ctypes.c_int64),
@@ -146,6 +156,8 @@ SIGNATURES = {
     "pgq_linear_backward_workspace": (_I32, [_P, ctypes.POINTER(_SZ)]),
     "pgq_linear_forward": (_I32, [_P, _P, _SZ, _P]),
     "pgq_linear_backward": (_I32, [_P, _P, _SZ, _P]),
+    "pgq_linear_forward_plan": (_I32, [_P, ctypes.POINTER(pgq_linear_plan)]),
+    "pgq_linear_backward_plan": (_I32, [_P, ctypes.POINTER(pgq_linear_plan)]),
     "pgq_average_workspace": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_SZ)]),
     "pgq_ema_update": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_P), ctypes.c_float, _I32, _P,
                               _SZ, _U32, _P, _P]),
@@ -250,6 +262,14 @@ def pgq_linear_forward(p, workspace, workspace_bytes, stream):
 
 def pgq_linear_backward(p, workspace, workspace_bytes, stream):
     return _lib.pgq_linear_backward(p, workspace, workspace_bytes, stream)
+
+
+def pgq_linear_forward_plan(p, out):
+    return _lib.pgq_linear_forward_plan(p, out)
+
+
+def pgq_linear_backward_plan(p, out):
+    return _lib.pgq_linear_backward_plan(p, out)
 
 
 def pgq_average_workspace(w, n, workspace_bytes):

@@ -60,17 +60,19 @@ struct Epilogue {
     int32_t vec;                 // rows of y, z and residual take 16-byte accesses of 8 (bf16) or 4 (fp32) columns
 };
 
-// Y[i][j] = epilogue(sum_l A[i][l] B[j][l]): 16-byte aligned rows, row strides below 2^21 elements.  B in bf16 and
-// L a multiple of 8, or B as int8 codes with a scale per row (bf16(code * s)) and L a multiple of 16.
+// Y[i][j] = epilogue(sum_l A[i][l] B[j][l]): 16-byte aligned rows, row strides below 2^22 elements.  B in bf16 and
+// L a multiple of 8, or B as int8 codes with a scale per row (bf16(code * s)) and L a multiple of 16.  With parts > 1
+// an element of A is the sum of that many bf16 values L columns apart, L a multiple of 64 and B in bf16.
 struct MmNt {
     const uint16_t* a;
     const uint16_t* b;
     const int8_t* codes;         // in place of b where from_codes
     const uint16_t* scales;
     int64_t lda, ldb, I, J, L;
-    int32_t kind, splits;        // tile, and parts the contraction is cut into (mm_nt_plan)
+    int32_t parts;
+    int32_t kind, splits;        // tile, and pieces the contraction is cut into (mm_nt_plan)
     int32_t from_codes;
-    int64_t chunk;               // l per part, a multiple of 64
+    int64_t chunk;               // l per piece, those of one part after the other's, a multiple of 64
     float* partial;              // splits > 1: mm_nt_partial_bytes() of scratch
     Epilogue e;
 };

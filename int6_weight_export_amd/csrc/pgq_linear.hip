@@ -173,13 +173,13 @@ constexpr int kFlat = 256;                     // granules (8 elements) of a fla
 struct Prep {
     pgq_linear_bwd b;            // the sources (codes, scales, x and their strides also in forward)
     uint16_t* dz;                // M x (parts x Np), row stride ldn, or NULL: only the partial sums
-    int32_t parts, what_parts;   // of dZ; copies of a row of what_t, one for each part that dX multiplies
+    int32_t parts;               // of dZ
     float* dbias_part;           // ceil(M / dz_rows) x N, or NULL
     int32_t dz_rows;             // rows of a dZ unit
     uint16_t* what;              // N x Kp, row stride ldk
-    uint16_t* what_t;            // K x (what_parts x Np), row stride ldn
+    uint16_t* what_t;            // K x Np, row stride ldt
     uint16_t* xc;                // M x Kp, row stride ldk
-    int64_t Kp, Np, ldk, ldn;
+    int64_t Kp, Np, ldk, ldn, ldt;
     int64_t n_dz, n_what, n_what_t, n_x;      // units of each kind, in this order
 };
 
@@ -336,10 +336,7 @@ __device__ __forceinline__ void prep_what_t(const Prep& p, int64_t unit, uint16_
     for (int c = 0; c < 2; ++c) {
         const int r = (tid >> 3) + 32 * c, g = tid & 7;
         const int64_t k = k0 + r, n = n0 + 8 * g;
-        if (k < b.K && n < p.Np) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
-            for (int part = 0; part < p.what_parts; ++part) *(GLB u32x4*)(p.what_t + k * p.ldn + part * p.Np + n) = v;
-        }
+        if (k < b.K && n < p.Np) *(GLB u32x4*)(p.what_t + k * p.ldt + n) = *reinterpret_cast<const u32x4*>(t + r * kPitch + 8 * g);
     }
 }
 
@@ -691,6 +688,7 @@ FwdPlan plan_fwd(const pgq_linear_fwd& p)
     q.nt.I = p.M;
     q.nt.J = p.N;
     q.nt.L = up8(p.K);
+    q.nt.parts = 1;
     double mm = mm_nt_plan(q.nt, p.K % 16 == 0 && p.ldc % 16 == 0 && p.ldc < kLong && is_aligned(p.codes, 16),
                            (double)float_size(p.y_dtype) + (p.z ? 2.0 : 0.0) + (p.residual ? (double)float_size(p.residual_dtype) : 0.0));
     if (p.M <= kSkinnyMost) {
@@ -711,6 +709,7 @@ struct BwdPlan {
     bool dx, dw, db;             // what there is to compute
     bool tile;                   // by the element-load kernel
     int32_t parts, parts_dx, parts_dw;       // bf16 values that stand for a dZ: in scratch, in each product
+    int64_t Np, ldn, ldt;        // columns of a part, row strides of dZ and of the transposed weights
     bool dz, copy_x;             // dZ and X go through scratch
     MmNt nt;                     // dX, dW: sizes, tiles and parts
     MmTt tt;
@@ -743,8 +742,11 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     q.parts_dx = q.dx ? dz_parts(p, p.dx_dtype) : 1;
     q.parts_dw = q.dw ? dz_parts(p, p.dw_dtype) : 1;
     q.parts = std::max(q.parts_dx, q.parts_dw);
-    const int64_t Np = up8(p.N), ldn = pitch(q.parts * Np);
-    q.tile = ldn >= kLong || p.K >= kLong;
+    // several parts of a row of dZ lie one behind the other, each padded with zeros to whole stages
+    q.Np = q.parts > 1 ? (p.N + 63) / 64 * 64 : up8(p.N);
+    q.ldn = q.parts > 1 ? q.parts * q.Np : pitch(p.N);
+    q.ldt = q.parts > 1 ? q.Np : pitch(p.N);
+    q.tile = q.ldn >= kLong || p.K >= kLong;
     auto take = [&](size_t n) { const size_t at = q.bytes; q.bytes += up256(n); return at; };
     // long units for few partial sums, short ones where there are not enough of them to fill the machine
     q.dz_rows = p.M * p.N >= (int64_t)4 << 20 ? 64 : 16;
@@ -753,13 +755,14 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
     if (q.tile || p.N == 0 || p.M == 0) return q;
     if (q.dx || q.dw) {
         q.dz = p.act != PGQ_ACT_NONE || p.dy_dtype != PGQ_BF16 || !direct(p.dy, p.lddy, p.N);    // (else one part)
-        if (q.dz) q.o_dz = take((size_t)p.M * ldn * 2);
+        if (q.dz) q.o_dz = take((size_t)p.M * q.ldn * 2);
     }
     if (q.dx) {
-        q.o_what_t = take((size_t)p.K * ldn * 2);
+        q.o_what_t = take((size_t)p.K * q.ldt * 2);
         q.nt.I = p.M;
         q.nt.J = p.K;
-        q.nt.L = q.parts_dx * Np;
+        q.nt.L = q.Np;
+        q.nt.parts = q.parts_dx;
     }
     if (q.dw) {
         q.copy_x = !direct(p.x, p.ldx, p.K);
@@ -768,7 +771,7 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
         q.tt.J = p.K;
         q.tt.L = p.M;
         q.tt.parts = q.parts_dw;
-        q.tt.part_cols = Np;
+        q.tt.part_cols = q.Np;
     }
     if (q.dx && q.dw) q.both = mm_both_plan(q.nt, q.tt, (double)float_size(p.dx_dtype));
     else if (q.dx) mm_nt_plan(q.nt, false, (double)float_size(p.dx_dtype));
@@ -780,8 +783,8 @@ BwdPlan plan_bwd(const pgq_linear_bwd& p)
 
 // Workgroups of the preparation, the element-load kernel and the few-token kernel
 int64_t flat_units(int64_t rows, int64_t cols) { return (rows * (up8(cols) / 8) + kFlat - 1) / kFlat; }
-int64_t dz_units(const pgq_linear_bwd& p, const BwdPlan& q) { return q.dz || q.db ? q.blocks * ((up8(p.N) + kDzCols - 1) / kDzCols) : 0; }
-int64_t what_t_units(const pgq_linear_bwd& p) { return ((up8(p.N) + 63) / 64) * ((p.K + 63) / 64); }
+int64_t dz_units(const pgq_linear_bwd& p, const BwdPlan& q) { return q.dz || q.db ? q.blocks * ((q.Np + kDzCols - 1) / kDzCols) : 0; }
+int64_t what_t_units(const pgq_linear_bwd& p) { return ((p.N + 63) / 64) * ((p.K + 63) / 64); }
 int64_t skinny_grid(const pgq_linear_fwd& p, const Parts& parts) { return (p.N + 15) / 16 * parts.n; }
 int64_t join_grid(const pgq_linear_fwd& p) { return (p.M * p.N + 255) / 256; }
 int64_t prep_units(const pgq_linear_fwd& p, const FwdPlan& q)
@@ -1009,11 +1012,11 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     memset(&pr, 0, sizeof(pr));
     pr.b = b;
     pr.Kp = up8(b.K);
-    pr.Np = up8(b.N);
+    pr.Np = q.Np;
     pr.ldk = pitch(b.K);
-    pr.ldn = pitch(q.parts * pr.Np);
+    pr.ldn = q.ldn;
+    pr.ldt = q.ldt;
     pr.parts = q.parts;
-    pr.what_parts = q.parts_dx;
     pr.dz = q.dz ? reinterpret_cast<uint16_t*>(ws + q.o_dz) : nullptr;
     pr.dz_rows = q.dz_rows;
     pr.dbias_part = q.db ? reinterpret_cast<float*>(ws + q.o_db) : nullptr;
@@ -1048,7 +1051,7 @@ pgq_status pgq_linear_backward(const pgq_linear_bwd* p, void* workspace, size_t 
     x.a = w.a = q.dz ? pr.dz : static_cast<const uint16_t*>(b.dy);
     x.lda = w.lda = q.dz ? pr.ldn : b.lddy;
     x.b = pr.what_t;
-    x.ldb = pr.ldn;
+    x.ldb = pr.ldt;
     x.partial = reinterpret_cast<float*>(ws + q.o_part_dx);
     x.e.y = b.dx;
     x.e.ldy = b.lddx;

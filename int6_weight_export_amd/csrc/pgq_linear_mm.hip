@@ -247,6 +247,8 @@ __device__ __forceinline__ void spread()
     }
 }
 
+__host__ __device__ inline int64_t nt_stages(const MmNt& p) { return (p.L + kTK - 1) / kTK * p.parts; }
+
 constexpr int kWayOut = 64 + 4;                // floats of a row on its way out, at most
 
 template <int WR, int WC, int IB, int JB, bool Q, int NB, int NA>
@@ -310,12 +312,12 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     uint32_t ti, tj, part;
     tile_of(wid, total, gi, gj, ti, tj, part);
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
-    const int64_t l0 = (int64_t)part * p.chunk, len = min(p.chunk, p.L - l0);      // this part of the contraction
+    const int64_t l0 = (int64_t)part * p.chunk, len = min(p.chunk, p.parts * p.L - l0);      // this piece of the contraction
     const int irows = (int)min((int64_t)TI, p.I - i0), jrows = (int)min((int64_t)TJ, p.J - j0);
     const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + i0 * p.lda + l0), 0, (int)(((int64_t)(irows - 1) * p.lda + len) * 2), 0x00020000);
     const __amdgpu_buffer_rsrc_t br =
         Q ? __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + j0 * p.ldb + l0), 0, (int)((int64_t)(jrows - 1) * p.ldb + len), 0x00020000)
-          : __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb + l0), 0, (int)(((int64_t)(jrows - 1) * p.ldb + len) * 2), 0x00020000);
+          : __builtin_amdgcn_make_buffer_rsrc((void*)(p.b + j0 * p.ldb), 0, (int)(((int64_t)(jrows - 1) * p.ldb + p.L) * 2), 0x00020000);
     // load slot of instruction c: row c T / 8 + tid / 8, slot tid % 8 (its granule is the same for every c)
     const int r0 = tid >> 3, g0 = (tid & 7) ^ swz(r0);
     const int br0 = tid / BG, bg0 = Q ? (tid & 3) ^ swz4(br0) : g0;
@@ -329,6 +331,9 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
         bo[c] = br0 + c * (T / BG) < jrows ? (uint32_t)((br0 + c * (T / BG)) * p.ldb + (Q ? 16 * bg0 : 8 * bg0)) * (Q ? 1u : 2u) : kOOB;
     const int nst = (int)((len + kTK - 1) / kTK);
     const int nfull = (int)(len / kTK);
+    // A part's columns start those of B again: their byte offset for the stage that is issued next
+    const int b_end = p.parts > 1 ? (int)p.L * 2 : 0x7FFFFFFF;
+    int b_off = (int)(l0 >= 2 * p.L ? l0 - 2 * p.L : l0 >= p.L ? l0 - p.L : l0) * 2;      // (at most three parts)
     // A whole stage costs a load instruction and its scalar offset each (address arithmetic in the vector unit
     // would run while no wavefront multiplies: the barrier has just lined them up); the last, partial stage
     // masks the granules past the contraction's end.
@@ -345,7 +350,7 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
     };
     auto issue_b = [&](int st) __attribute__((always_inline)) {
         uint8_t* lb = lds + NA * AS + (st % NB) * BS;
-        const int kb = st * (Q ? kTK : kTK * 2);
+        const int kb = Q ? st * kTK : b_off;
         const uint32_t off = st < nfull || st * kTK + (Q ? 16 : 8) * bg0 < (int)len ? 0u : kOOB;
         if (st < nfull) {
 #pragma unroll
@@ -353,6 +358,10 @@ __device__ __forceinline__ void nt_body(const MmNt& p, uint32_t wid, uint32_t to
         } else {
 #pragma unroll
             for (int c = 0; c < BI; ++c) load_lds(br, lb + (c * T + wave * 64) * 16, bo[c] | off, kb);
+        }
+        if constexpr (!Q) {
+            b_off += kTK * 2;
+            b_off = b_off == b_end ? 0 : b_off;
         }
     };
     const int wi = (wave / WC) * (32 * IB), wj = (wave % WC) * (32 * JB);
@@ -610,8 +619,9 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
     // by the cache)
     const int64_t first = (int64_t)part * p.chunk;
     const int nst = (int)min(p.chunk, tt_stages(p) - first);
-    int64_t row = first / p.parts * 64;          // of the stage that is issued next, and its part
-    int which = (int)(first % p.parts);
+    const uint32_t block = (uint32_t)first / (uint32_t)p.parts;
+    int64_t row = (int64_t)block * 64;           // of the stage that is issued next, and its part
+    int which = (int)((uint32_t)first - block * (uint32_t)p.parts);
     const int ig = (int)min((int64_t)AG, (p.I - i0 + 7) / 8), jg = (int)min((int64_t)BG, (p.J - j0 + 7) / 8);
     uint32_t ao[AI], bo[BI];     // byte offsets of this thread's loads within a stage; columns past the edge are out of range
 #pragma unroll
@@ -857,7 +867,7 @@ double mm_nt_plan(MmNt& p, bool codes_ok, double out_bytes)
     // laying What out: codes in, bf16 out, and a launch
     const double layout = codes_ok ? 4.0 + (double)p.J * (double)p.L * 3.0 / 4e6 : 0.0;
     const double out = (double)p.I * (double)p.J * out_bytes / 5.3e6;
-    const int64_t stages = std::max<int64_t>(1, (p.L + 63) / 64);
+    const int64_t stages = std::max<int64_t>(1, nt_stages(p));
     for (int k = 0; k < (int)(sizeof(kNt) / sizeof(kNt[0])); ++k) {
         const NtKind& kind = kNt[k];
         if (kind.codes && !codes_ok) continue;
@@ -991,7 +1001,7 @@ int mm_both_plan(MmNt& x, MmTt& w, double out_bytes)
 {
     double best = 0;
     int chosen = 0;
-    const int64_t sx = std::max<int64_t>(1, (x.L + 63) / 64), sw = std::max<int64_t>(1, tt_stages(w));
+    const int64_t sx = std::max<int64_t>(1, nt_stages(x)), sw = std::max<int64_t>(1, tt_stages(w));
     const double out = (double)x.I * (double)x.J * out_bytes / 5.3e6;
     for (int k = 0; k < (int)(sizeof(kBoth) / sizeof(kBoth[0])); ++k) {
         const BothKind& b = kBoth[k];

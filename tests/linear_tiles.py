@@ -90,7 +90,7 @@ BACKWARD = [
     ((204, 16, 6976, "dx dw dbias", "bf16", "none"), ("dx dw dbias", 128, 128, False, 128, 128, False, "bf16")),
     ((277, 16, 5616, "dx dw dbias", "f32", "none"), ("dx dw dbias", 128, 128, False, 128, 128, False, "f32")),
     ((669, 16, 2320, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 128, 128, False, 128, 128, True, "bf16")),
-    ((709, 16, 2112, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 128, 128, False, 128, 128, True, "f32")),
+    ((330, 16, 4688, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 128, 128, False, 128, 128, True, "f32")),
     ((20, 1008, 3648, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 128, 128, True, 128, 128, False, "bf16")),
     ((20, 800, 4000, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 128, 128, True, 128, 128, False, "f32")),
     ((2429, 3028, 65, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 128, 128, True, 128, 128, True, "bf16")),
@@ -112,7 +112,7 @@ BACKWARD = [
     ((5934, 134, 1156, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 256, 256, False, 256, 256, True, "bf16")),
     ((1697, 136, 4578, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 256, 256, False, 256, 256, True, "f32")),
     ((151, 619, 7030, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 256, 256, True, 256, 192, False, "bf16")),
-    ((165, 1172, 2906, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 256, 256, True, 256, 192, False, "f32")),
+    ((129, 672, 6928, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 256, 256, True, 256, 192, False, "f32")),
     ((1571, 1129, 779, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 256, 256, True, 256, 192, True, "bf16")),
     ((705, 2656, 464, "dx dw dbias", "f32", "silu"), ("dx dw dbias", 256, 256, True, 256, 192, True, "f32")),
     ((129, 848, 6496, "dx dw dbias", "bf16", "silu"), ("dx dw dbias", 256, 256, True, 256, 256, False, "bf16")),

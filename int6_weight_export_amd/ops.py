@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import warnings
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence, Tuple
 
@@ -467,13 +468,17 @@ def qlinear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias: Op
     x: bf16 [M, K]; codes: int8 [N, K]; scales: fp16 [N] (or int16 bit patterns); bias: fp32 or bf16
     [N]; residual: fp32 or bf16 [M, N], which may be `out` itself; act: "none", "relu", "relu2" (both
     with a leaky slope) or "silu".  Returns Y [M, N] in out_dtype (bf16 or fp32), or (Y, Z) with the
-    bf16 pre-activation Z that qlinear_backward takes when want_z.  No gradient is recorded: call
-    qlinear_backward."""
+    bf16 pre-activation Z that qlinear_backward takes when want_z.  No gradient is recorded (a warning
+    says so where one would be expected): call qlinear_backward."""
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x and codes must be matrices")
     (M, K), N, dev = x.shape, codes.shape[0], _gpu_of("x", x)
     ldx, ldc = _matrix("x", x, M, K, _B16, dev), _matrix("codes", codes, N, K, _I8, dev)
     pb = bt = pr = ldr = rt = pz = 0
+    if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
+        warnings.warn("qlinear records no gradient for its arguments: call qlinear_backward, or torch.no_grad() around it",
+                      stacklevel=2)
     if bias is not None:
         pb, bt = _vector("bias", bias, N, _B16_F32, dev), _dtype_code(bias.dtype)
     if residual is not None:

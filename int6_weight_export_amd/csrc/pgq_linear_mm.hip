@@ -4,6 +4,8 @@
 // instruction (checked on the device): lane l supplies row l % 32 of A (and column l % 32 of B) with 8
 // consecutive l, lanes 32..63 the next 8; accumulator register j of lane l is row 8 (j / 4) + 4 (l / 32) +
 // j % 4, column l % 32.
+//
+// Sizes with a measurement are I x J x L: rows of A, rows (columns, for dW) of B, contraction.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -200,8 +202,8 @@ struct Out {
 // of 32 x 32.  Each 64-wide stage of both operands goes from global memory straight into LDS (buffer
 // loads with the LDS destination), double-buffered, so the next stage's loads are in flight while the
 // matrix cores work on this one; a lane past I, J or L gets zeros from the buffer range check.  Where the LDS has room
-// A, which comes from memory, is three stages deep and B, which stays in the caches, two (16384 x 528 x 1584 52.6 ->
-// 46.9 us, 8192 x 8192 x 4096 483 -> 465).
+// A, which comes from memory, is three stages deep and B, which stays in the caches, two (16384 x 528 x 1584 with an
+// fp32 residual 60 -> 55 us for the call, 8192 x 8192 x 4096 483 -> 465).
 //
 // LDS slots are 16-byte granules, 8 to a row; granule g of row r sits in slot g ^ swz(r), so that the
 // rows a fragment read touches spread over distinct banks in every group of 8 and of 16 lanes.
@@ -554,8 +556,9 @@ NtKind nt_kind(int per_cu, double stage, double busy, double start = 4.0)
             reinterpret_cast<const void*>(&pgq_mm_nt_kernel<WR, WC, IB, JB, Q, NB, NA, uint16_t>),
             reinterpret_cast<const void*>(&pgq_mm_nt_reduce_kernel<WR, WC, IB, JB>), Q};
 }
-// (256 x 192 beside 256 x 256 for outputs that end shortly behind a multiple of 256: 16384 x 528 x 1584 runs in
-// 41.0 us with it against 46.9, 16384 x 1584 x 528 in 71.3 against 50.1)
+// (256 x 192 beside 256 x 256 for outputs that end shortly behind a multiple of 256; whole calls, inputs from memory:
+// 16384 x 528 x 1584 with an fp32 residual takes 59 us with it against 64, with bf16 Y alone 46 against 51;
+// 16384 x 1584 x 528 65 against 50)
 const NtKind kNt[] = {nt_kind<2, 4, 4, 2, false, 2, 3>(1, 1.70, 1.60), nt_kind<2, 2, 2, 2, false, 2, 3>(2, 0.50, 0.55), nt_kind<2, 2, 2, 1, false, 3>(2, 0.50, 0.36),
                       nt_kind<2, 2, 1, 1, false, 4>(2, 0.33, 0.24), nt_kind<1, 4, 4, 1, true, 3>(2, 0.50, 0.62, 6.0),
                       nt_kind<1, 4, 2, 1, true, 4>(2, 0.55, 0.40), nt_kind<4, 2, 2, 3, false, 2, 3>(1, 1.35, 1.35)};
@@ -700,8 +703,8 @@ __device__ __forceinline__ void tt_body(const MmTt& p, uint32_t wid, uint32_t to
     }
     int st = 0;
     if constexpr (kSpread<IB, JB>) {
-        // past the edge: only this wavefront's share of the loads (the backward of 16384 x 528 x 1584 96 -> 91 us: 1584 rows
-        // of dW leave three quarters of the last tile row empty)
+        // past the edge: only this wavefront's share of the loads (1584 x 528 x 16384 in one part, with its dX: 96 -> 91 us;
+        // 1584 rows of dW leave three quarters of the last tile row empty)
         if (i0 + wi >= p.I || j0 + wj >= p.J) {
             for (; st < nst; ++st) {
                 wait_barrier<0>();
@@ -844,7 +847,9 @@ int64_t tt_tiles(const TtKind& k, int64_t I, int64_t J) { return ((I + k.ti - 1)
 
 // Microseconds that workgroups of `per` stages each take: whole rounds over the places, then the rest.  A rest of at most
 // one workgroup a compute unit runs at the lone workgroup's pace, more at a pace between the two; a tile that has
-// its unit to itself runs a stage faster the fewer units share the memory (1.6 us with all of them, 1.3 with half).
+// its unit to itself runs a stage faster the fewer units are at work: the model goes straight from `busy` with all of
+// them to 0.8 of it with none.  Measured, as the difference of 128 and 32 stages: 256 x 256 1.74 us with all, 1.28 with
+// half and 1.22 with a quarter, where the model has 1.60, 1.44 and 1.36; 256 x 192 1.39, 1.03 and 1.00 (1.35, 1.22, 1.15).
 static double rounds_of_stages(const NtKind& kind, int64_t wgs, double per)
 {
     const int64_t places = 256 * kind.per_cu, full = wgs / places, rest = wgs % places;

@@ -491,7 +491,8 @@ pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bi
 
 /* The values 8-bit states stand for, m and r = sqrt(v), as bf16 (exact: 4 and 5 significant bits; a value
  * below bf16's range becomes a subnormal or zero).  m_out, r_out: host arrays of n device pointers (numel
- * bf16 each).  The table is the step's: same workspace and flags. */
+ * bf16 each); the outputs share no memory with each other or with the states.  The table is the step's: same
+ * workspace and flags. */
 pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* const* m_out, uint16_t* const* r_out,
                             void* workspace, size_t workspace_bytes, uint32_t flags, uint32_t* dev_status,
                             void* stream);

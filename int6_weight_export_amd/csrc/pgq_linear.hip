@@ -46,7 +46,7 @@ enum Product { P_FWD, P_DX, P_DW };
 // One part of a value, and what is left of it for the next: 8 bits cut off (so that the rest keeps the value's sign
 // and nothing overflows), the last part rounded to nearest.  Where the value ends before its last part the rest
 // goes on as 2^-40 of the value: a part of 0 would make NaN of an infinite weight or input, one of the other sign
-// would take its infinity away.
+// would take its infinity away.  (Below 2^-93 that underflows, and an infinity there may still become NaN.)
 __device__ __forceinline__ uint16_t next_part(float value, float& rest, bool last)
 {
     const uint32_t bits = __builtin_bit_cast(uint32_t, rest);

@@ -659,7 +659,7 @@ class AdamW:
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
              device_hyper: bool = False) -> None:
-        """One update from the gradients (fp32, bf16 or fp16, dense).  device_hyper: take the constants that
+        """One update from the gradients (fp32, bf16 or fp16, dense, in memory of their own).  device_hyper: take the constants that
         load_hyper wrote instead of counting this step here; a captured step needs it, since a graph would
         repeat one step's constants."""
         if len(grads) != self.n:
@@ -702,7 +702,8 @@ class AdamW:
 
     def decode_states(self, m_out: Optional[Sequence[torch.Tensor]] = None,
                       r_out: Optional[Sequence[torch.Tensor]] = None):
-        """The values that 8-bit states hold: lists of bf16 tensors m and r = sqrt(v) (exact)."""
+        """The values that 8-bit states hold: lists of bf16 tensors m and r = sqrt(v) (exact), in the given tensors
+        (which share no memory) or in new ones."""
         if self.state_bits != 8:
             raise ValueError("32-bit states are held as values")
         outs = []

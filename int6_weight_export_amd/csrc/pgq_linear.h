@@ -13,8 +13,14 @@ __device__ __forceinline__ float f16_to_f32(uint16_t h) { return (float)__builti
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
-// 1 / (1 + e^-z): the exponential within 2 units of the last place, the reciprocal within 1
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+// 1 / (1 + e^-z), for z <= 0 as e^z / (1 + e^z): the exponential, within 2 units of the last place, does not overflow,
+// and the reciprocal, within 1, is of a number between 1 and 2 (of one past 2^126 it would be 0: the instruction
+// gives no subnormals, and z = -88 lost its value of -5e-37)
+__device__ __forceinline__ float sigmoid(float z)
+{
+    const float a = expf(-fabsf(z));
+    return (z > 0.0f ? 1.0f : a) * __builtin_amdgcn_rcpf(1.0f + a);
+}
 
 __device__ __forceinline__ float act_value(int32_t act, float slope, float z)
 {

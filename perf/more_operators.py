@@ -175,6 +175,10 @@ def prepare(case, seed):
     if op == "quantize":
         rows, cols = case["rows"], case["cols"]
         s["w"] = (torch.randn(rows, cols + case["pad"], generator=g, device=dev) * 0.02).to(_TYPES[case["type"]])[:, :cols]
+        if own:
+            from int6_weight_export_amd import ops
+
+            s["status"] = ops.new_status()
         return s
     if op == "decode":
         s["codes"], s["scales"] = _codes(case["rows"], case["cols"], case["group"], case["pad"], g, dev)
@@ -280,7 +284,7 @@ def _run_own(s, c, op):
     if op == "clip":
         return {"norm": s["norm"].clip_(_falling(s)), "grads": s["grads"]}
     if op == "quantize":
-        got = ops.quantize_groups(s["w"], group=c["group"], dq_dtype=_TYPES[c["dq"]])
+        got = ops.quantize_groups(s["w"], group=c["group"], dq_dtype=_TYPES[c["dq"]], status=s["status"])
         return {"dq": got["dq"], "scales": got["scales"].view(torch.float16)}
     if op == "decode":
         return {"value": ops.dequant_groups(s["codes"], s["scales"], c["cols"], group=c["group"], out_dtype=_TYPES[c["type"]])}

@@ -25,6 +25,8 @@
  *     byte layout is this library's own, documented at pgq_dequant_codes);
  *   - the forward matmul over the STE-dequantized weights, dequantization fused: PR #69
  *     card, section Other.
+ * Beside the pages' methods: the linear layer's gradient, the AdamW step, the global gradient norm
+ * with clipping, and 4-bit codes with a scale per group of columns.
  *
  * The arithmetic, fixed where the pages leave it open (Q = 2^(bits-1) - 1, every step an
  * IEEE binary32 operation with round-to-nearest-even):
@@ -46,7 +48,7 @@
  * stream work that uses it has completed.  The library allocates no device memory and
  * keeps no state besides a per-device cache of launch limits; it is thread-safe.  Host
  * arrays are read during the call only.  Inputs and outputs must not overlap, except
- * that `mean` is updated in place.
+ * that `mean` (and what a call says is updated in place) is.
  */
 #ifndef PGQ_H
 #define PGQ_H
@@ -395,6 +397,64 @@ pgq_status pgq_linear_forward_plan(const pgq_linear_fwd* p, pgq_linear_plan* out
 pgq_status pgq_linear_backward_plan(const pgq_linear_bwd* p, pgq_linear_plan* out);
 
 /* ------------------------------------------------------------------------------------------ */
+/* 4-bit weights with a scale for every `group` consecutive columns of a row (group 32, 64 or    */
+/* 128; a row's last group may be shorter).  Per group, the row quantizer above with Q = 7:       */
+/*   clip = max |w|;  s = fp16(fl(clip / 7)), 1.0 when that rounds to zero                        */
+/*   code = clamp(rne(w / s), -7, 7);  value = code * s (exact in binary32)                       */
+/* Stored form: eight codes of a row, k = 8 g .. 8 g + 7, take four bytes: byte j holds code j in  */
+/* bits 0..3 and code j + 4 in bits 4..7, each as a sign (bit 3) and a magnitude 0..7 (bits 0..2;   */
+/* 1000 is written by no call and stands for 0).  A row is 4 * ceil(cols / 8) bytes, the last ones  */
+/* filled up with zero codes; scales: ceil(cols / group) fp16 per row.                             */
+/* ------------------------------------------------------------------------------------------ */
+
+/* w (PGQ_F32, PGQ_BF16 or PGQ_F16, rows x cols, row stride ld elements) into codes (row stride ldc    */
+/* bytes), scales (row stride lds) and, when dq is not NULL, the values (dq_dtype PGQ_F32, or PGQ_BF16:   */
+/* rounded to nearest even; row stride ldq).  Bytes of the outputs between their rows are left as they  */
+/* are.  dev_status: PGQ_DEV_NONFINITE and PGQ_DEV_SCALE_OVF; the outputs of such a group are          */
+/* unspecified.  Sizes below 2^31; PGQ_ERR_SHAPE too where the launch would pass 2^32 threads (about      */
+/* 2^35 elements).  Outputs that share memory with another argument: PGQ_ERR_PARAM.                    */
+pgq_status pgq_quantize_groups(const void* w, int32_t w_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t group,
+                               uint8_t* codes, int64_t ldc, uint16_t* scales, int64_t lds, void* dq, int32_t dq_dtype,
+                               int64_t ldq, uint32_t* dev_status, void* stream);
+
+/* The values of stored codes: out (out_dtype PGQ_F32, or PGQ_BF16: rounded to nearest even), row stride ldo. */
+/* The same limits and errors.                                                                       */
+pgq_status pgq_dequant_groups(const uint8_t* codes, int64_t ldc, const uint16_t* scales, int64_t lds, int64_t rows,
+                              int64_t cols, int32_t group, void* out, int32_t out_dtype, int64_t ldo, void* stream);
+
+/* The linear layer over such weights, for few tokens: Y = act(X W^T + b) + R, W[n][k] = code * s, never     */
+/* rounded.  Sums in binary32: those of a group's x * code, then of their products with the group's scale       */
+/* (one rounding each), so |x| of 2^118 and more may overflow where the formula does not.  A row with a      */
+/* scale that is not finite gives no finite sum.  The rest is pgq_linear_forward's: bias, act, residual and the   */
+/* single rounding of Y, memory that may not be shared, limits, recording into a HIP graph, the same bits for   */
+/* the same inputs (an element of Y does not depend on the other tokens of a call of the same M).  Any M;       */
+/* the kernels are made for up to 64 tokens and take more in blocks of 64: from a few hundred on,                */
+/* pgq_dequant_groups and a library product are faster.                                              */
+typedef struct {
+    int64_t M, N, K;             /* tokens, outputs, inputs; each below 2^31 */
+    const uint16_t* x;           /* bf16, M x K, row stride ldx */
+    int64_t ldx;
+    const uint8_t* codes;        /* N rows of 4 * ceil(K / 8) bytes, row stride ldc bytes */
+    int64_t ldc;
+    const uint16_t* scales;      /* fp16 bit patterns, N x ceil(K / group), row stride lds */
+    int64_t lds;
+    const void* bias;            /* NULL or N values of bias_dtype (PGQ_F32 or PGQ_BF16) */
+    const void* residual;        /* NULL or M x N of residual_dtype (PGQ_F32 or PGQ_BF16), row stride ldr.
+                                    May be y itself (same pointer, stride and type) */
+    int64_t ldr;
+    void* y;                     /* y_dtype (PGQ_F32 or PGQ_BF16), M x N, row stride ldy */
+    int64_t ldy;
+    int32_t bias_dtype, residual_dtype, y_dtype;
+    int32_t act;                 /* PGQ_ACT_* */
+    float slope;                 /* RELU, RELU2: finite */
+    int32_t group;               /* 32, 64 or 128 */
+} pgq_linear4_fwd;
+
+/* Device scratch the call needs (0 for most sizes): 256-byte aligned, one for each call that runs at a time. */
+pgq_status pgq_linear4_forward_workspace(const pgq_linear4_fwd* p, size_t* workspace_bytes);
+pgq_status pgq_linear4_forward(const pgq_linear4_fwd* p, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Weight averaging without quantization, grouped over n tensors in one launch.               */
 /* w[i]: the weights (fp32 or bf16, rows x cols, row stride ld; awq_s must be NULL; name is    */
 /* ignored).  The averages are caller-owned fp32 device buffers, rows x cols dense, updated in */
@@ -489,6 +549,15 @@ pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bi
                           const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, void* workspace,
                           size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream);
 
+/* The same step with grad_scale times *factor, a binary32 number in device memory, in place of grad_scale (one more */
+/* rounding): the factor of pgq_grad_norm, which then clips without a pass over the gradients.  With a NaN  */
+/* factor the step is skipped: nothing is written, the copies included, and PGQ_DEV_NONFINITE is set.        */
+/* factor NULL: pgq_adamw_step.                                                                   */
+pgq_status pgq_adamw_step_clipped(const pgq_adamw_tensor* t, int32_t n, int32_t state_bits, const void* const* grad,
+                                  const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, const float* factor,
+                                  void* workspace, size_t workspace_bytes, uint32_t flags, uint32_t* dev_status,
+                                  void* stream);
+
 /* The values 8-bit states stand for, m and r = sqrt(v), as bf16 (exact: 4 and 5 significant bits; a value
  * below bf16's range becomes a subnormal or zero).  m_out, r_out: host arrays of n device pointers (numel
  * bf16 each); the outputs share no memory with each other or with the states.  The table is the step's: same
@@ -496,6 +565,34 @@ pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bi
 pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* const* m_out, uint16_t* const* r_out,
                             void* workspace, size_t workspace_bytes, uint32_t flags, uint32_t* dev_status,
                             void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* The global norm of n gradient tensors and clipping to it.                                     */
+/*   norm   = fl32(|c| * sqrt(sum of g^2 over every element)), squares and sums in 64 bits         */
+/*   factor = 1 where norm <= max_norm, fl32(max_norm / norm) where it is larger (the quotient of   */
+/*            the unrounded norm), NaN where norm is not finite in binary32 (PGQ_DEV_NONFINITE)    */
+/* c: grad_scale, or, where grad_scale_dev is not NULL, the binary32 number there (a member of the AdamW   */
+/* constants in device memory, so that a recorded step follows them).  Sums run in an order that      */
+/* depends on the sizes alone: the same inputs give the same bits.                                  */
+/*   grad      host array of n device pointers, numel[i] dense values of dtype[i] (PGQ_F32, PGQ_BF16 or  */
+/*             PGQ_F16), aligned to their type; NULL only where numel[i] is 0                     */
+/*   max_norm  >= 0; infinity for the norm alone                                                   */
+/*   result    device, two floats: norm and factor                                                 */
+/*   workspace device, pgq_grad_norm_workspace() bytes, 64-byte aligned.  Its first 64 bytes have to be    */
+/*             zero before its first use and are left zero by every call; calls that run at the same      */
+/*             time (two graphs, two streams) need one each                                          */
+/* The three host arrays are read during the call only.  May be recorded into a HIP graph: the recorded call   */
+/* keeps its pointers and max_norm.  Sizes: each below 2^40.                                        */
+/* ------------------------------------------------------------------------------------------ */
+pgq_status pgq_grad_norm_workspace(const int64_t* numel, int32_t n, size_t* workspace_bytes);
+pgq_status pgq_grad_norm(const void* const* grad, const int64_t* numel, const int32_t* dtype, int32_t n, float grad_scale,
+                         const float* grad_scale_dev, float max_norm, float* result, void* workspace,
+                         size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/* The same with c = 1, and then every gradient times factor in place: g = fl32(g * factor), rounded to its type.   */
+/* Nothing is written where factor is 1 or NaN.  No two tensors may share memory (PGQ_ERR_PARAM).          */
+pgq_status pgq_grad_clip(void* const* grad, const int64_t* numel, const int32_t* dtype, int32_t n, float max_norm,
+                         float* result, void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------------------------ */
 /* Timing aid (no method step): the next pgq_* call made by this host thread that launches     */

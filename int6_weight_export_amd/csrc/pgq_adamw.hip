@@ -59,6 +59,7 @@ struct AdArgs {
     uint64_t checksum;
     uint32_t* status;
     const pgq_adamw_hyper* h_dev;
+    const float* factor;                          // NULL, or a number in device memory that grad_scale is multiplied by
     pgq_adamw_hyper h;
     uint32_t first_tile;                          // tiles before this launch's
     uint32_t first_desc;                          // tensors before its pointers
@@ -178,6 +179,12 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
         if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, PGQ_DEV_NO_HYPER);
         return;
     }
+    const float factor = a.factor ? *a.factor : 1.0f;
+    if (factor != factor) {                       // no step: elements kept one by one would still round 8-bit states anew
+        if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, PGQ_DEV_NONFINITE);
+        return;
+    }
+    const float grad_scale = a.factor ? h.grad_scale * factor : h.grad_scale;
     const float lr = d.lr_scale * h.lr;
     const float step = lr * h.ib1;
     const float keep = 1.0f - lr * d.weight_decay;
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) pgq_adamw_kernel(AdArgs a, Ptrs grad
                 m[e] = value(q.m, e, PGQ_F32);
                 v[e] = value(q.v, e, PGQ_F32);
             }
-            const float gs = h.grad_scale * g;
+            const float gs = grad_scale * g;
             const float m1 = m[e] * h.beta1 + gs * h.c1;
             const float v1 = v[e] * h.beta2 + (gs * gs) * h.c2;
             const float root = sqrtf(v1);
@@ -459,7 +466,7 @@ uint64_t build_table(const pgq_adamw_tensor* t, int32_t n, int32_t bits, uint64_
 // Table upload (unless resident) and launches over runs of tensors whose pointers fit the kernel
 // arguments: per pointers a tensor, fn the kernel.
 pgq_status run(const pgq_adamw_tensor* t, int32_t n, int32_t bits, uint64_t tiles, const void* fn, int per,
-               const void* const* p0, const void* const* p1, const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev,
+               const void* const* p0, const void* const* p1, const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, const float* factor,
                void* workspace, size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream)
 {
     if (!workspace || workspace_bytes < table_size(n, tiles)) return PGQ_ERR_WORKSPACE;
@@ -493,6 +500,7 @@ pgq_status run(const pgq_adamw_tensor* t, int32_t n, int32_t bits, uint64_t tile
     a.checksum = sum;
     a.status = dev_status;
     a.h_dev = h_dev;
+    a.factor = factor;
     if (h) a.h = *h;
     void *ev_start = nullptr, *ev_stop = nullptr;
     take_timing_events(&ev_start, &ev_stop);
@@ -575,12 +583,19 @@ pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bi
                           const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, void* workspace,
                           size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream)
 {
+    return pgq_adamw_step_clipped(t, n, state_bits, grad, h, h_dev, nullptr, workspace, workspace_bytes, flags, dev_status, stream);
+}
+
+pgq_status pgq_adamw_step_clipped(const pgq_adamw_tensor* t, int32_t n, int32_t state_bits, const void* const* grad,
+                                  const pgq_adamw_hyper* h, const pgq_adamw_hyper* h_dev, const float* factor, void* workspace,
+                                  size_t workspace_bytes, uint32_t flags, uint32_t* dev_status, void* stream)
+{
     uint64_t tiles = 0;
     const pgq_status st = check_tensors(t, n, state_bits, &tiles);
     if (st != PGQ_OK) return st;
     if (!h && !h_dev) return PGQ_ERR_NULL;
     if (n > 0 && !grad) return PGQ_ERR_NULL;
-    if (h_dev && !is_aligned(h_dev, 4)) return PGQ_ERR_ALIGN;
+    if ((h_dev && !is_aligned(h_dev, 4)) || (factor && !is_aligned(factor, 4))) return PGQ_ERR_ALIGN;
     bool bf16_w = false, f32_g = true, bf16_g = true, grads_vec = true;
     for (int32_t i = 0; i < n; ++i) {
         if (t[i].numel == 0) continue;
@@ -596,7 +611,7 @@ pgq_status pgq_adamw_step(const pgq_adamw_tensor* t, int32_t n, int32_t state_bi
     // (gradients that are not aligned to four elements are handled by the element path of the mixed kernel)
     const int s = bf16_w || !grads_vec ? S_ANY : f32_g ? S_F32 : bf16_g ? S_BF16G : S_ANY;
     return run(t, n, state_bits, tiles, state_bits == 8 ? step_kernel<8>(s) : step_kernel<32>(s), 1, grad, nullptr,
-               h_dev ? nullptr : h, h_dev, workspace, workspace_bytes, flags, dev_status, stream);
+               h_dev ? nullptr : h, h_dev, factor, workspace, workspace_bytes, flags, dev_status, stream);
 }
 
 pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* const* m_out, uint16_t* const* r_out,
@@ -613,7 +628,7 @@ pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* cons
     }
     if (tiles == 0) return PGQ_OK;
     return run(t, n, 8, tiles, reinterpret_cast<const void*>(&pgq_adamw_decode_kernel), 2,
-               reinterpret_cast<const void* const*>(m_out), reinterpret_cast<const void* const*>(r_out), nullptr, nullptr,
+               reinterpret_cast<const void* const*>(m_out), reinterpret_cast<const void* const*>(r_out), nullptr, nullptr, nullptr,
                workspace, workspace_bytes, flags, dev_status, stream);
 }
 

@@ -5,13 +5,33 @@
 #include <stdint.h>
 
 #include "pgq_desc.h"
+#include "pgq_train.h"
 #include "../../include/pgq.h"
 
 namespace pgq {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 __device__ __forceinline__ float f16_to_f32(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
 __device__ __forceinline__ float bf16_to_f32(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+__device__ __forceinline__ float load_any(const void* p, int32_t dtype, int64_t i)
+{
+    return dtype == PGQ_F32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void* p, int32_t dtype, int64_t i, float v)
+{
+    if (dtype == PGQ_F32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
+}
+// 16 (8) bytes at any alignment: one load, the hardware takes unaligned global addresses
+__device__ __forceinline__ u32x4 load16(const void* p)
+{
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
 
 // 1 / (1 + e^-z), for z <= 0 as e^z / (1 + e^z): the exponential, within 2 units of the last place, does not overflow,
 // and the reciprocal, within 1, is of a number between 1 and 2 (of one past 2^126 it would be 0: the instruction
@@ -38,20 +58,6 @@ __device__ __forceinline__ float act_slope(int32_t act, float slope, float z)
     }
     const float d = z > 0.0f ? 1.0f : slope;
     return act == PGQ_ACT_RELU ? d : 2.0f * z * d * d;
-}
-
-// The runtime's limits: 2^31 - 1 workgroups, 2^32 - 1 threads.  A call one of whose launches would pass them is
-// refused before the first.
-inline bool grid_fits(int64_t grid, int block) { return grid <= 0x7FFFFFFF && grid * block <= 0xFFFFFFFFll; }
-// One launch of a linear grid; a refused one leaves no timing events for the thread's next call.
-inline hipError_t launch_grid(const void* fn, int64_t grid, int block, void** args, void* stream)
-{
-    if (!grid_fits(grid, block)) {
-        void *start, *stop;
-        take_timing_events(&start, &stop);
-        return hipErrorInvalidValue;
-    }
-    return launch_plain(fn, dim3((unsigned)grid), dim3((unsigned)block), args, stream);
 }
 
 // What a product does with its sums on the way out: v = act(sum + bias) + residual, Z stored on the side.

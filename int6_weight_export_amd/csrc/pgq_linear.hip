@@ -29,17 +29,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float load_any(const void* p, int32_t dtype, int64_t i)
-{
-    return dtype == PGQ_F32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-}
-__device__ __forceinline__ void store_any(void* p, int32_t dtype, int64_t i, float v)
-{
-    if (dtype == PGQ_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
-}
 
 enum Product { P_FWD, P_DX, P_DW };
 
@@ -141,13 +130,6 @@ __global__ void __launch_bounds__(256) pgq_linear_tile_kernel(pgq_linear_fwd f, 
     }
 }
 
-// 16 (8) bytes at any alignment: one load, the hardware takes unaligned global addresses
-__device__ __forceinline__ u32x4 load16(const void* p)
-{
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
-}
 // the same for values that this call reads once
 __device__ __forceinline__ u32x4 load16_once(const void* p)
 {
@@ -525,42 +507,6 @@ __global__ void __launch_bounds__(256) pgq_linear_join_kernel(pgq_linear_fwd f, 
     finish(f, at / f.N, at % f.N, z);
 }
 
-constexpr int64_t kMaxSize = ((int64_t)1 << 31) - 1;
-
-bool float_type(int32_t dt) { return dt == PGQ_F32 || dt == PGQ_BF16; }
-size_t float_size(int32_t dt) { return dt == PGQ_F32 ? 4 : 2; }
-bool act_ok(int32_t act, float slope)
-{
-    if (act == PGQ_ACT_NONE || act == PGQ_ACT_SILU) return true;
-    return (act == PGQ_ACT_RELU || act == PGQ_ACT_RELU2) && slope - slope == 0.0f;
-}
-
-// The bytes of a matrix argument.  clash: two of them share a byte, or might: rows of different strides in
-// one range of memory are not told apart.
-struct Span {
-    const void* at;
-    int64_t rows, width, ld;             // width and row stride in bytes
-};
-bool clash(const Span& a, const Span& b)
-{
-    if (!a.at || !b.at || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
-    const uintptr_t a0 = (uintptr_t)a.at, b0 = (uintptr_t)b.at;
-    const uintptr_t a1 = a0 + (uintptr_t)(a.rows - 1) * (uintptr_t)a.ld + (uintptr_t)a.width;
-    const uintptr_t b1 = b0 + (uintptr_t)(b.rows - 1) * (uintptr_t)b.ld + (uintptr_t)b.width;
-    if (a1 <= b0 || b1 <= a0) return false;
-    if (a.ld != b.ld) return true;
-    const int64_t d = (int64_t)(b0 - a0) % a.ld, at = d < 0 ? d + a.ld : d;       // columns of one buffer
-    return at < a.width || at + b.width > a.ld;
-}
-// one of the outputs (the first n_out spans) shares memory with another span
-bool any_clash(const Span* s, int n_out, int n)
-{
-    for (int i = 0; i < n_out; ++i)
-        for (int j = i + 1; j < n; ++j)
-            if (clash(s[i], s[j])) return true;
-    return false;
-}
-
 pgq_status check_fwd(const pgq_linear_fwd* p)
 {
     if (!p) return PGQ_ERR_NULL;
@@ -813,27 +759,6 @@ bool launches_fit(const pgq_linear_bwd& p, const BwdPlan& q)
     if (!mm) return (!q.dx || grid_fits(tiles_of(p.M, p.K), 256)) && (!q.dw || grid_fits(tiles_of(p.N, p.K), 256));
     return (!q.dx || mm_nt_fits(q.nt)) && (!q.dw || mm_tt_fits(q.tt));
 }
-
-// The launches of one call: the first takes a pending start event, the last the stop event.
-struct Launches {
-    void *start = nullptr, *stop = nullptr, *stream;
-    int left;
-    hipError_t e = hipSuccess;
-    Launches(int n, void* s) : stream(s), left(n) { take_timing_events(&start, &stop); }
-    bool next()
-    {
-        if (e != hipSuccess) return false;
-        set_timing_events(start, --left == 0 ? stop : nullptr);
-        start = nullptr;
-        return true;
-    }
-    void go(const void* fn, int64_t grid, int block, void** args)
-    {
-        if (!next()) return;
-        e = launch_grid(fn, grid, block, args, stream);
-    }
-    pgq_status done() const { return e == hipSuccess ? PGQ_OK : (pgq_status)note_hip_error(e); }
-};
 
 bool rows16(const void* p, int32_t dtype, int64_t ld) { return is_aligned(p, 16) && ld % (16 / (int64_t)float_size(dtype)) == 0; }
 

@@ -556,6 +556,117 @@ def qlinear_backward(dy: torch.Tensor, codes: Optional[torch.Tensor], scales: Op
     return res
 
 
+def _on_gpu(index: int, name: str, fn, *args) -> None:
+    """fn(*args, current stream) with GPU `index` current."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            rc = fn(*args, _stream_of(index))
+    else:
+        rc = fn(*args, _stream_of(index))
+    if rc != pgq.PGQ_OK:
+        pgq.check(rc, name)
+
+
+def _group_sizes(cols: int, group: int) -> Tuple[int, int]:
+    """Bytes of a row's codes and number of its groups."""
+    if group not in (32, 64, 128):
+        raise ValueError(f"group {group}: 32, 64 or 128 expected")
+    return (cols + 7) // 8 * 4, (cols + group - 1) // group
+
+
+def quantize_groups(w: torch.Tensor, group: int = 128, dq_dtype: Optional[torch.dtype] = None,
+                    status: Optional[torch.Tensor] = None) -> dict:
+    """4-bit codes of a matrix (fp32, bf16 or fp16, rows contiguous) with an fp16 scale for every `group` (32, 64 or 128)
+    consecutive columns: s = fp16(max |w| / 7) or 1, code = round(w / s) in [-7, 7].
+
+    Returns "codes" uint8 [rows, 4 ceil(cols / 8)] (eight columns to four bytes: byte j holds column j in its low and
+    column j + 4 in its high half, sign and magnitude), "scales" int16 [rows, ceil(cols / group)] (fp16 bit patterns), "dq" (the
+    values code * s in dq_dtype, fp32 or bf16, when given) and "status" (`status` when given: PGQ_DEV_* bits are OR-ed into it)."""
+    if w.dim() != 2:
+        raise ValueError("w must be a matrix")
+    rows, cols = w.shape
+    dev = _gpu_of("w", w)
+    nbytes, groups = _group_sizes(cols, group)
+    ld = _matrix("w", w, rows, cols, (torch.float32, torch.bfloat16, torch.float16), dev)
+    if dq_dtype is not None and dq_dtype not in _B16_F32:
+        raise TypeError(f"unsupported dq_dtype {dq_dtype}")
+    if status is None:
+        status = new_status(w.device)
+    out = {"codes": torch.empty(rows, nbytes, dtype=torch.uint8, device=w.device),
+           "scales": torch.empty(rows, groups, dtype=torch.int16, device=w.device)}
+    dq, dqt = 0, pgq.PGQ_F32
+    if dq_dtype is not None:
+        out["dq"] = torch.empty(rows, cols, dtype=dq_dtype, device=w.device)
+        dq, dqt = out["dq"].data_ptr(), _dtype_code(dq_dtype)
+    out["status"] = status
+    _on_gpu(dev, "pgq_quantize_groups", pgq._lib.pgq_quantize_groups, w.data_ptr(), _dtype_code(w.dtype), rows, cols, ld, group,
+            out["codes"].data_ptr(), nbytes, out["scales"].data_ptr(), groups, dq, dqt, cols,
+            _vector("status", status, 1, (torch.int32,), dev))
+    return out
+
+
+def dequant_groups(codes: torch.Tensor, scales: torch.Tensor, cols: int, group: int = 128,
+                   out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values code * s of quantize_groups' codes (uint8 [rows, 4 ceil(cols / 8)]) and scales (fp16, or int16 bit patterns,
+    [rows, ceil(cols / group)]) as a [rows, cols] matrix in out_dtype (fp32: exact; bf16: rounded)."""
+    if codes.dim() != 2:
+        raise ValueError("codes must be a matrix")
+    rows, dev = codes.shape[0], _gpu_of("codes", codes)
+    nbytes, groups = _group_sizes(cols, group)
+    ldc, lds = _matrix("codes", codes, rows, nbytes, _U8, dev), _matrix("scales", scales, rows, groups, _SCALE_TYPES, dev)
+    if out_dtype not in _B16_F32:
+        raise TypeError(f"unsupported out_dtype {out_dtype}")
+    if out is None:
+        out = torch.empty(rows, cols, dtype=out_dtype, device=codes.device)
+        ldo = cols
+    else:
+        ldo = _matrix("out", out, rows, cols, (out_dtype,), dev)
+    _on_gpu(dev, "pgq_dequant_groups", pgq._lib.pgq_dequant_groups, codes.data_ptr(), ldc, scales.data_ptr(), lds, rows, cols, group,
+            out.data_ptr(), _dtype_code(out_dtype), ldo)
+    return out
+
+
+_FWD4 = struct.Struct("14q4ifi")        # pgq_linear4_fwd
+
+
+def qlinear4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, group: int = 128, bias: Optional[torch.Tensor] = None,
+             act: str = "none", slope: float = 0.0, residual: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Y = act(X W^T + b) + R with 4-bit weights W = code * s, a scale for every `group` columns: qlinear's form for
+    serving, made for up to 64 tokens (more are taken in blocks of 64; from a few hundred on, dequant_groups and a library
+    product are faster).
+
+    x: bf16 [M, K]; codes: uint8 [N, 4 ceil(K / 8)] and scales: fp16 (or int16 bit patterns) [N, ceil(K / group)] as
+    quantize_groups makes them; the other arguments as in qlinear.  Returns Y [M, N] in out_dtype (bf16 or fp32).  No
+    gradient is recorded (a warning says so where one would be expected)."""
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x and codes must be matrices")
+    (M, K), N, dev = x.shape, codes.shape[0], _gpu_of("x", x)
+    nbytes, groups = _group_sizes(K, group)
+    ldx, ldc = _matrix("x", x, M, K, _B16, dev), _matrix("codes", codes, N, nbytes, _U8, dev)
+    lds = _matrix("scales", scales, N, groups, _SCALE_TYPES, dev)
+    pb = bt = pr = ldr = rt = 0
+    if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
+        warnings.warn("qlinear4 records no gradient for its arguments: call it under torch.no_grad()", stacklevel=2)
+    if bias is not None:
+        pb, bt = _vector("bias", bias, N, _B16_F32, dev), _dtype_code(bias.dtype)
+    if residual is not None:
+        ldr = _matrix("residual", residual, M, N, _B16_F32, dev)
+        pr, rt = residual.data_ptr(), _dtype_code(residual.dtype)
+    if out_dtype not in _B16_F32:
+        raise TypeError(f"unsupported out_dtype {out_dtype}")
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=x.device)
+        ldy = N
+    else:
+        ldy = _matrix("out", out, M, N, (out_dtype,), dev)
+    desc = _FWD4.pack(M, N, K, x.data_ptr(), ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, pb, pr, ldr, out.data_ptr(), ldy,
+                      bt, rt, _dtype_code(out_dtype), ACTS[act], slope, group)
+    _launch_linear(pgq._lib.pgq_linear4_forward, pgq._lib.pgq_linear4_forward_workspace, "pgq_linear4_forward", desc, dev)
+    return out
+
+
 def _same_device(tensors: Sequence[Optional[torch.Tensor]], device) -> None:
     for t in tensors:
         if t is not None and t.device != device:
@@ -575,6 +686,64 @@ def _dense(name: str, t: torch.Tensor, numel: int, dtypes) -> None:
         raise ValueError(f"{name}: {numel} dense values expected")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+
+
+def _norm_workspace(numel, device) -> torch.Tensor:
+    """The gradient norm's workspace for tensors of these sizes (a ctypes array).  Zeroed by a copy from the host, which is
+    over when it returns, so that any stream may use it."""
+    need = ctypes.c_size_t(0)
+    pgq.check(pgq.pgq_grad_norm_workspace(numel, len(numel), ctypes.byref(need)), "pgq_grad_norm_workspace")
+    return torch.zeros(need.value, dtype=torch.uint8).to(device)
+
+
+class GradNorm:
+    """The global L2 norm of a list of gradient tensors (fp32, bf16 or fp16, dense) and clipping to it, without the norm's
+    coming to the host.  The tensors and their addresses are taken once; bind() takes others of the same sizes.  `status` gets
+    PGQ_DEV_NONFINITE where a norm is not finite.  Not to be made while a graph is captured; its calls may be.  Calls
+    that run at the same time need an object each."""
+
+    def __init__(self, grads: Sequence[torch.Tensor]):
+        grads = list(grads)
+        self.n = n = len(grads)
+        if n == 0:
+            raise ValueError("no gradients")
+        self._index = _gpu_of("gradient 0", grads[0])
+        self.device = grads[0].device
+        self._numel = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+        self._dtype = (ctypes.c_int32 * n)()
+        self._ptrs = (ctypes.c_void_p * n)()
+        self.bind(grads)
+        self.workspace = _norm_workspace(self._numel, self.device)
+        self.status = new_status(self.device)
+        self.result = torch.empty(2, dtype=torch.float32, device=self.device)
+        self._views = self.result[0], self.result[1]
+        self._tail = (self.result.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr())
+
+    def bind(self, grads: Sequence[torch.Tensor]) -> None:
+        """Take these tensors, of the sizes of the first ones, from now on."""
+        grads = list(grads)
+        if len(grads) != self.n:
+            raise ValueError(f"{len(grads)} gradients, expected {self.n}")
+        for i, g in enumerate(grads):
+            _dense(f"gradient {i}", g, self._numel[i], (torch.float32, torch.bfloat16, torch.float16))
+            if g.get_device() != self._index:
+                raise ValueError(f"gradient {i} is on {g.device}, expected GPU {self._index}")
+        self.grads = grads
+        for i, g in enumerate(grads):
+            self._ptrs[i], self._dtype[i] = g.data_ptr(), _dtype_code(g.dtype)
+
+    def norm(self, max_norm: float = float("inf"), grad_scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
+        """(norm, factor), two fp32 numbers on the GPU that the next call overwrites: |grad_scale| sqrt(sum g^2), and 1, or
+        max_norm / norm where the norm is larger, or NaN where it is not finite."""
+        _on_gpu(self._index, "pgq_grad_norm", pgq._lib.pgq_grad_norm, self._ptrs, self._numel, self._dtype, self.n, grad_scale, None,
+                max_norm, *self._tail)
+        return self._views
+
+    def clip_(self, max_norm: float) -> torch.Tensor:
+        """Multiply the gradients by that factor in place (not where it is 1 or NaN); returns the norm they had."""
+        _on_gpu(self._index, "pgq_grad_clip", pgq._lib.pgq_grad_clip, self._ptrs, self._numel, self._dtype, self.n, max_norm,
+                *self._tail)
+        return self._views[0]
 
 
 class AdamW:
@@ -633,6 +802,11 @@ class AdamW:
         self._numel = [w.numel() for w in self.weights]
         self._ptrs = (ctypes.c_void_p * n)()
         self._g_dtypes = [torch.float32] * n
+        self._g_codes = (ctypes.c_int32 * n)(*[pgq.PGQ_F32] * n)
+        self._n_numel = (ctypes.c_int64 * n)(*self._numel)
+        self.norm_workspace = _norm_workspace(self._n_numel, self.device)
+        self.norm_result = torch.empty(2, dtype=torch.float32, device=self.device)
+        self.grad_norm = self.norm_result[0]
         self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
     def _zero_state(self, k: int):
@@ -658,10 +832,14 @@ class AdamW:
         self._loaded = True
 
     def step(self, grads: Sequence[torch.Tensor], lr: Optional[float] = None, grad_scale: float = 1.0,
-             device_hyper: bool = False) -> None:
+             device_hyper: bool = False, max_norm: Optional[float] = None) -> Optional[torch.Tensor]:
         """One update from the gradients (fp32, bf16 or fp16, dense, in memory of their own).  device_hyper: take the constants that
         load_hyper wrote instead of counting this step here; a captured step needs it, since a graph would
-        repeat one step's constants."""
+        repeat one step's constants.
+
+        max_norm: clip the gradients, times grad_scale, to this global norm on the way (they are not written): the step sees
+        them times grad_scale * min(1, max_norm / norm).  Returns the norm then, an fp32 number on the GPU that the next clipped step
+        overwrites.  Where it is not finite the step writes nothing and sets PGQ_DEV_NONFINITE in `status`."""
         if len(grads) != self.n:
             raise ValueError(f"{len(grads)} gradients for {self.n} weights")
         if not device_hyper and torch.cuda.is_current_stream_capturing():
@@ -676,17 +854,28 @@ class AdamW:
                 raise ValueError(f"gradient {i} is on {g.device}, expected GPU {index}")
             ptrs[i] = g.data_ptr()
             if g.dtype is not types[i]:
-                self._arr[i].g_dtype = _dtype_code(g.dtype)
+                self._arr[i].g_dtype = self._g_codes[i] = _dtype_code(g.dtype)
                 types[i] = g.dtype
         h = None if device_hyper else self._hyper(lr, grad_scale, self.step_count + 1)
-        self._on_device(self._enqueue_step, h, ptrs)
+        self._on_device(self._enqueue_step, h, ptrs, grad_scale, max_norm)
         if not device_hyper:
             self.step_count += 1
         self._uploaded = True
+        return None if max_norm is None else self.grad_norm
 
-    def _enqueue_step(self, h, ptrs) -> None:
-        rc = pgq._lib.pgq_adamw_step(self._arr, self.n, self.state_bits, ptrs, h, None if h is not None else _p(self.hyper),
-                                     self._ws_ptr, self._ws_bytes, self._table_flags(), self._status_ptr, _stream_of(self._index))
+    def _enqueue_step(self, h, ptrs, grad_scale, max_norm) -> None:
+        h_dev, stream = None if h is not None else self.hyper.data_ptr(), _stream_of(self._index)
+        factor = None
+        if max_norm is not None:
+            rc = pgq._lib.pgq_grad_norm(ptrs, self._n_numel, self._g_codes, self.n, grad_scale,
+                                        None if h_dev is None else h_dev + pgq.pgq_adamw_hyper.grad_scale.offset, max_norm,
+                                        self.norm_result.data_ptr(), self.norm_workspace.data_ptr(), self.norm_workspace.numel(),
+                                        self._status_ptr, stream)
+            if rc != pgq.PGQ_OK:
+                pgq.check(rc, "pgq_grad_norm")
+            factor = self.norm_result.data_ptr() + 4
+        rc = pgq._lib.pgq_adamw_step_clipped(self._arr, self.n, self.state_bits, ptrs, h, h_dev, factor, self._ws_ptr,
+                                             self._ws_bytes, self._table_flags(), self._status_ptr, stream)
         if rc != pgq.PGQ_OK:
             pgq.check(rc, "pgq_adamw_step")
 

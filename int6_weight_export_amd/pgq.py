@@ -109,6 +109,16 @@ class pgq_linear_bwd(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class pgq_linear4_fwd(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("slope", ctypes.c_float),
+                ("group", ctypes.c_int32)]
+
+
 class pgq_linear_plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("path", "tile_rows", "tile_cols", "parts", "from_codes", "copies_x", "dw_rows",
                                               "dw_cols", "dw_parts", "joint", "dz_dx", "dz_dw")]
@@ -158,6 +168,10 @@ SIGNATURES = {
     "pgq_linear_backward": (_I32, [_P, _P, _SZ, _P]),
     "pgq_linear_forward_plan": (_I32, [_P, ctypes.POINTER(pgq_linear_plan)]),
     "pgq_linear_backward_plan": (_I32, [_P, ctypes.POINTER(pgq_linear_plan)]),
+    "pgq_quantize_groups": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _P, _I32, _I64, _P, _P]),
+    "pgq_dequant_groups": (_I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _I64, _P]),
+    "pgq_linear4_forward_workspace": (_I32, [_P, ctypes.POINTER(_SZ)]),
+    "pgq_linear4_forward": (_I32, [_P, _P, _SZ, _P]),
     "pgq_average_workspace": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_SZ)]),
     "pgq_ema_update": (_I32, [ctypes.POINTER(pgq_tensor_in), _I32, ctypes.POINTER(_P), ctypes.c_float, _I32, _P,
                               _SZ, _U32, _P, _P]),
@@ -168,8 +182,14 @@ SIGNATURES = {
     "pgq_adamw_workspace": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, ctypes.POINTER(_SZ)]),
     "pgq_adamw_step": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, _I32, ctypes.POINTER(_P),
                               ctypes.POINTER(pgq_adamw_hyper), _P, _P, _SZ, _U32, _P, _P]),
+    "pgq_adamw_step_clipped": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, _I32, ctypes.POINTER(_P),
+                                      ctypes.POINTER(pgq_adamw_hyper), _P, _P, _P, _SZ, _U32, _P, _P]),
     "pgq_adamw_decode": (_I32, [ctypes.POINTER(pgq_adamw_tensor), _I32, ctypes.POINTER(_P), ctypes.POINTER(_P), _P,
                                 _SZ, _U32, _P, _P]),
+    # (the arrays by address: ctypes arrays, or integers)
+    "pgq_grad_norm_workspace": (_I32, [_P, _I32, ctypes.POINTER(_SZ)]),
+    "pgq_grad_norm": (_I32, [_P, _P, _P, _I32, ctypes.c_float, _P, ctypes.c_float, _P, _P, _SZ, _P, _P]),
+    "pgq_grad_clip": (_I32, [_P, _P, _P, _I32, ctypes.c_float, _P, _P, _SZ, _P, _P]),
     "pgq_time_next_launch": (_I32, [_P, _P]),
     "pgq_status_str": (ctypes.c_char_p, [_I32]),
     "pgq_version": (ctypes.c_char_p, []),
@@ -272,6 +292,23 @@ def pgq_linear_backward_plan(p, out):
     return _lib.pgq_linear_backward_plan(p, out)
 
 
+def pgq_quantize_groups(w, w_dtype, rows, cols, ld, group, codes, ldc, scales, lds, dq, dq_dtype, ldq, dev_status, stream):
+    return _lib.pgq_quantize_groups(w, w_dtype, rows, cols, ld, group, codes, ldc, scales, lds, dq, dq_dtype, ldq, dev_status,
+                                    stream)
+
+
+def pgq_dequant_groups(codes, ldc, scales, lds, rows, cols, group, out, out_dtype, ldo, stream):
+    return _lib.pgq_dequant_groups(codes, ldc, scales, lds, rows, cols, group, out, out_dtype, ldo, stream)
+
+
+def pgq_linear4_forward_workspace(p, workspace_bytes):
+    return _lib.pgq_linear4_forward_workspace(p, workspace_bytes)
+
+
+def pgq_linear4_forward(p, workspace, workspace_bytes, stream):
+    return _lib.pgq_linear4_forward(p, workspace, workspace_bytes, stream)
+
+
 def pgq_average_workspace(w, n, workspace_bytes):
     return _lib.pgq_average_workspace(w, n, workspace_bytes)
 
@@ -296,8 +333,27 @@ def pgq_adamw_step(t, n, state_bits, grad, h, h_dev, workspace, workspace_bytes,
     return _lib.pgq_adamw_step(t, n, state_bits, grad, h, h_dev, workspace, workspace_bytes, flags, dev_status, stream)
 
 
+def pgq_adamw_step_clipped(t, n, state_bits, grad, h, h_dev, factor, workspace, workspace_bytes, flags, dev_status, stream):
+    return _lib.pgq_adamw_step_clipped(t, n, state_bits, grad, h, h_dev, factor, workspace, workspace_bytes, flags, dev_status,
+                                       stream)
+
+
 def pgq_adamw_decode(t, n, m_out, r_out, workspace, workspace_bytes, flags, dev_status, stream):
     return _lib.pgq_adamw_decode(t, n, m_out, r_out, workspace, workspace_bytes, flags, dev_status, stream)
+
+
+def pgq_grad_norm_workspace(numel, n, workspace_bytes):
+    return _lib.pgq_grad_norm_workspace(numel, n, workspace_bytes)
+
+
+def pgq_grad_norm(grad, numel, dtype, n, grad_scale, grad_scale_dev, max_norm, result, workspace, workspace_bytes, dev_status,
+                  stream):
+    return _lib.pgq_grad_norm(grad, numel, dtype, n, grad_scale, grad_scale_dev, max_norm, result, workspace, workspace_bytes,
+                              dev_status, stream)
+
+
+def pgq_grad_clip(grad, numel, dtype, n, max_norm, result, workspace, workspace_bytes, dev_status, stream):
+    return _lib.pgq_grad_clip(grad, numel, dtype, n, max_norm, result, workspace, workspace_bytes, dev_status, stream)
 
 
 def pgq_time_next_launch(start_event, stop_event):

@@ -578,9 +578,9 @@ pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* cons
 /*             PGQ_F16), aligned to their type; NULL only where numel[i] is 0                     */
 /*   max_norm  >= 0; infinity for the norm alone                                                   */
 /*   result    device, two floats: norm and factor                                                 */
-/*   workspace device, pgq_grad_norm_workspace() bytes, 64-byte aligned.  Its first 64 bytes have to be    */
-/*             zero before its first use and are left zero by every call; calls that run at the same      */
-/*             time (two graphs, two streams) need one each                                          */
+/*   workspace device, pgq_grad_norm_workspace() bytes, 64-byte aligned.  All of it has to be zero before     */
+/*             its first use; a call leaves it ready for the next one.  Calls that run at the same time (two     */
+/*             graphs, two streams) need one each                                                     */
 /* The three host arrays are read during the call only.  May be recorded into a HIP graph: the recorded call   */
 /* keeps its pointers and max_norm.  Sizes: each below 2^40.                                        */
 /* ------------------------------------------------------------------------------------------ */

@@ -27,6 +27,13 @@ constexpr int kThreads = 256;
 constexpr int kArgTensors = 128;                  // tensors in the kernel arguments of a launch
 constexpr int64_t kTile = 16384;                  // elements of the smallest tile
 constexpr int64_t kTilesWanted = 2048;            // tiles grow until about so many are left: 8 workgroups a compute unit
+// Counts of finished workgroups.  One counter takes an increment every 13 ns, which for 1900 workgroups is longer than the
+// reading (30.7 M bf16: 32 us), so large grids count in kCounters groups and then the groups.  Each counter has a cache
+// line, and a memory channel, of its own.
+constexpr uint32_t kCounters = 16;
+constexpr uint32_t kOneCounter = 256;             // workgroups that a single counter is enough for: one step less at the end
+constexpr int kCounterBytes = 256;
+constexpr size_t kCountersBytes = (size_t)kCounterBytes * (kCounters + 1);
 constexpr int64_t kMaxNumel = (int64_t)1 << 40;
 
 struct Tensors {
@@ -37,7 +44,7 @@ struct Tensors {
 };
 
 struct NormArgs {
-    uint32_t* ticket;
+    uint8_t* counters;
     double* part;
     float* result;
     uint32_t* status;
@@ -47,6 +54,16 @@ struct NormArgs {
     uint32_t first, total;                        // this launch's first partial sum, partial sums in all
     int32_t last;                                 // 1: no launch of this call comes after this one
 };
+
+// One more workgroup of the grid is done: true in the one that is last.  Counters wrap to 0 for the next call.
+__device__ __forceinline__ bool is_last(uint8_t* counters)
+{
+    auto count = [&](uint32_t i, uint32_t most) { return atomicInc(reinterpret_cast<uint32_t*>(counters + i * kCounterBytes), most - 1) == most - 1; };
+    const uint32_t grid = gridDim.x;
+    if (grid <= kOneCounter) return count(0, grid);
+    const uint32_t g = blockIdx.x % kCounters;
+    return count(1 + g, (grid - g + kCounters - 1) / kCounters) && count(0, kCounters);
+}
 
 // the tensor of a tile: the number of tensors that end at or before it
 __device__ __forceinline__ int tensor_of(const Tensors& t, uint32_t tile)
@@ -136,7 +153,7 @@ __device__ __forceinline__ double block_sum(double x, double* lds)
 __global__ void __launch_bounds__(kThreads) pgq_grad_norm_kernel(NormArgs a, Tensors t)
 {
     __shared__ double lds[2][kThreads / 64];
-    __shared__ uint32_t place;
+    __shared__ bool last;
     double s = 0.0;
     const int ti = __builtin_amdgcn_readfirstlane(tensor_of(t, blockIdx.x));
     if (ti < kArgTensors) {                       // (an empty list has one workgroup and no tensor)
@@ -155,13 +172,12 @@ __global__ void __launch_bounds__(kThreads) pgq_grad_norm_kernel(NormArgs a, Ten
             // the store's end is all there is to wait for; a fence would write the whole L2 back, once a workgroup
             // (61 MB of bf16: 100 us with it).
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            // counts up to the grid's last workgroup and wraps to 0 for the next call
-            place = atomicInc(a.ticket, gridDim.x - 1);
+            last = is_last(a.counters);
         }
     }
     if (!a.last) return;
     __syncthreads();
-    if (place != gridDim.x - 1) return;
+    if (!last) return;
     double r = 0.0;
 #pragma unroll 8
     for (uint32_t i = threadIdx.x; i < a.total; i += kThreads) r += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -243,7 +259,7 @@ pgq_status plan(const int64_t* numel, int32_t n, int64_t* tile, int64_t* total)
     if (!grid_fits(*total, kThreads)) return PGQ_ERR_SHAPE;
     return PGQ_OK;
 }
-size_t workspace_size(int64_t total) { return 64 + ((size_t)std::max<int64_t>(total, 1) * 8 + 63) / 64 * 64; }
+size_t workspace_size(int64_t total) { return kCountersBytes + ((size_t)std::max<int64_t>(total, 1) * 8 + 63) / 64 * 64; }
 
 size_t size_of(int32_t dtype) { return dtype == PGQ_F32 ? 4 : 2; }
 
@@ -307,8 +323,8 @@ NormArgs args_of(float scale, const float* scale_dev, float max_norm, float* res
 {
     NormArgs a;
     memset(&a, 0, sizeof(a));
-    a.ticket = static_cast<uint32_t*>(workspace);
-    a.part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + 64);
+    a.counters = static_cast<uint8_t*>(workspace);
+    a.part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kCountersBytes);
     a.result = result;
     a.status = status;
     a.scale_dev = scale_dev;

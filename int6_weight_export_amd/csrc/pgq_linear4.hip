@@ -26,7 +26,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves4 = 8;
 constexpr int kMost = 64;                         // tokens of a workgroup
-constexpr int kBlockK = 128;                      // columns of a block: 64 bytes of a row's codes
+constexpr int kBlockK = 256;                      // columns of a block: 128 bytes of a row's codes, a cache line
+constexpr int kHalfK = 128;                       // of which an instruction's load takes half
 
 // Eight codes as bf16.  A byte 0000 0mmm (sign in its top bit) is, read as e4m3, the number m * 2^-9: below 2^-6 such
 // numbers are equally spaced, so the conversion from fp8 with a scale of 2^9 makes the whole number.  Ten instructions.
@@ -63,6 +64,12 @@ __device__ __forceinline__ int column(int d, int q)
     return 32 * d + 8 * q;
 }
 
+// 16 bytes at any address that this call reads once: past the caches that hold the tokens
+__device__ __forceinline__ u32x4 load16_once(const void* p)
+{
+    typedef u32x4 any_u32x4 __attribute__((aligned(1)));
+    return __builtin_nontemporal_load((const __attribute__((address_space(1))) any_u32x4*)p);
+}
 // 16 bytes of a row from byte `at` on, zeros past its last one: past the edge the row's last 16 bytes shifted down
 __device__ __forceinline__ u32x4 load16_edge(const void* row, int64_t at, int64_t bytes)
 {
@@ -88,86 +95,478 @@ __device__ __forceinline__ void finish(const pgq_linear4_fwd& f, int64_t m, int6
     store_any(f.y, f.y_dtype, m * f.ldy + n, y);
 }
 
-// T: tiles of 16 tokens.  Lane l: token l % 16 of A, weight row l % 16 of B, columns by the quarter l / 16.  Lanes past
-// M or N repeat the last row, whose sums they do not store.
-template <int T, int G>
-__global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_kernel(pgq_linear4_fwd f, int32_t token_blocks)
+// How the work is cut: workgroups of 16 R weight rows, their K in `parts` pieces of `blocks` blocks.
+struct Cut {
+    float* sums;                 // parts > 1: parts x M x N
+    int64_t blocks;
+    int32_t token_blocks, parts;
+};
+
+// T: tiles of 16 tokens, R: of 16 weight rows.  Lane l: token l % 16 of A, weight row l % 16 of B, columns by the quarter
+// l / 16.  Lanes past M or N repeat the last row, whose sums they do not store.
+template <int T, int R, int G>
+__global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_linear4_fwd f, Cut cut)
 {
-    __shared__ f32x4 sums[kWaves4][T][64];
+    __shared__ f32x4 sums[kWaves4][R * T][64];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     const int r = lane & 15, q = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x % (uint32_t)token_blocks) * kMost;
-    const int64_t n0 = (int64_t)(blockIdx.x / (uint32_t)token_blocks) * 16;
-    const int64_t n = min(n0 + r, f.N - 1);
-    const uint8_t* crow = f.codes + n * f.ldc;
-    const uint16_t* srow = f.scales + n * f.lds;
-    const uint16_t* xrow[T];
+    const uint32_t tb = blockIdx.x % (uint32_t)cut.token_blocks, rest = blockIdx.x / (uint32_t)cut.token_blocks;
+    const uint32_t part = rest % (uint32_t)cut.parts;
+    const int64_t m0 = (int64_t)tb * kMost, n0 = (int64_t)(rest / (uint32_t)cut.parts) * (16 * R);
+    const uint8_t* crow[R];
+    const uint16_t *srow[R], *xrow[T];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const int64_t n = min(n0 + 16 * j + r, f.N - 1);
+        crow[j] = f.codes + n * f.ldc + 16 * q;
+        srow[j] = f.scales + n * f.lds;
+    }
 #pragma unroll
     for (int t = 0; t < T; ++t) xrow[t] = f.x + min(m0 + 16 * t + r, f.M - 1) * f.ldx;
-    f32x4 acc[T];
+    f32x4 acc[R][T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) acc[t] = f32x4{};
-    constexpr int GB = kBlockK / G;               // groups of a block
-    auto multiply = [&](u32x4 c, const u32x4 (*x)[4], const float* s) __attribute__((always_inline)) {
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[j][t] = f32x4{};
+    bool live[T];                                 // lanes past M load nothing of X: their rows of the products go nowhere
+#pragma unroll
+    for (int t = 0; t < T; ++t) live[t] = m0 + 16 * t + r < f.M;
+    constexpr int GH = kHalfK / G;                // groups of half a block
+    constexpr int SB = 8 / (2 * GH);              // blocks whose scales are loaded together, 16 bytes of a row
+    const int64_t scale_bytes = 2 * ((f.K + G - 1) / G);
+    // products of half a block: sc holds the scales of its groups in its lowest halves
+    auto multiply = [&](u32x4 c, const u32x4 (*x)[4], uint64_t sc, f32x4* a) __attribute__((always_inline)) {
         trade<G>(c);
 #pragma unroll
-        for (int g = 0; g < GB; ++g) {
+        for (int g = 0; g < GH; ++g) {
             f32x4 p[T];
 #pragma unroll
             for (int t = 0; t < T; ++t) p[t] = f32x4{};
 #pragma unroll
-            for (int d = g * (4 / GB); d < (g + 1) * (4 / GB); ++d) {
+            for (int d = g * (4 / GH); d < (g + 1) * (4 / GH); ++d) {
                 const bf16x8 w = decode8(c[d]);
 #pragma unroll
                 for (int t = 0; t < T; ++t) p[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[t][d]), w, p[t], 0, 0, 0);
             }
+            const float s = f16_to_f32((uint16_t)(sc >> (16 * g)));
 #pragma unroll
             for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(p[t][e], s[g], acc[t][e]);
+                for (int e = 0; e < 4; ++e) a[t][e] = __builtin_fmaf(p[t][e], s, a[t][e]);
         }
     };
-    const int64_t full = f.K / kBlockK;
+    // the lowest GH scales of `half` of a block whose scales are the lowest of s
+    auto scales_of = [&](const u32x4& s, int half) __attribute__((always_inline)) -> uint64_t {
+        if (GH == 1) return half ? s[0] >> 16 : s[0];
+        if (GH == 2) return half ? s[1] : s[0];
+        return half ? (uint64_t)s[3] << 32 | s[2] : (uint64_t)s[1] << 32 | s[0];
+    };
+    struct Codes { u32x4 c[R][2]; };
+    auto load_codes = [&](int64_t b, Codes& h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            h.c[j][0] = load16(crow[j] + kBlockK / 2 * b);
+            h.c[j][1] = load16(crow[j] + kBlockK / 2 * b + kHalfK / 2);
+        }
+    };
+    auto load_scales = [&](int64_t b, u32x4* s) __attribute__((always_inline)) {
+        const int64_t at = 4 * GH * b;
+        if (at + 16 <= scale_bytes) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) s[j] = load16((const uint8_t*)srow[j] + at);
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j) s[j] = load16_edge(srow[j], at, scale_bytes);
+        }
+    };
+    // This wavefront's blocks: an equal run of its part's, so that the scales of a run are neighbours.  Codes of the next block
+    // are in flight while one is multiplied; X of a block is loaded before them, since loads complete in order and waiting for X
+    // must not be waiting for those.
+    const int64_t whole = f.K / kBlockK, blocks = (f.K + kBlockK - 1) / kBlockK;
+    const int64_t part_end = min(blocks, (int64_t)(part + 1) * cut.blocks);
+    const int64_t run = (cut.blocks + kWaves4 - 1) / kWaves4;
+    int64_t b = (int64_t)part * cut.blocks + wave * run;
+    const int64_t end = min(part_end, b + run), mine = min(whole, end);
+    if (b < mine) {
+        Codes h, next;
+        u32x4 s[R];
+        load_scales(b, s);
+        load_codes(b, h);
+        int held = SB;                            // blocks whose scales are in s
+        auto block = [&](bool more) __attribute__((always_inline)) {
+            u32x4 x[2][T][4];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) x[half][t][d] = u32x4{};
+                    if (live[t]) {
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) x[half][t][d] = load16(xrow[t] + kBlockK * b + kHalfK * half + column<G>(d, q));
+                    }
+                }
+            u32x4 sn[R];
+            const bool refill = more && held == 1;
+            if (refill) load_scales(b + 1, sn);
+            __builtin_amdgcn_sched_barrier(0);
+            if (more) load_codes(b + 1, next);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int j = 0; j < R; ++j) multiply(h.c[j][half], x[half], scales_of(s[j], half), acc[j]);
+            if (!more) return;
+            h = next;
+            if (refill) {
+#pragma unroll
+                for (int j = 0; j < R; ++j) s[j] = sn[j];
+                held = SB;
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j) s[j] = GH == 1 ? u32x4{s[j][1], s[j][2], s[j][3], 0} : u32x4{s[j][2], s[j][3], 0, 0};
+                --held;
+            }
+        };
 #pragma unroll 1
-    for (int64_t b = wave; b < full; b += kWaves4) {
-        const u32x4 c = load16(crow + 64 * b + 16 * q);
-        u32x4 x[T][4];
-        float s[GB];
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) x[t][d] = load16(xrow[t] + kBlockK * b + column<G>(d, q));
-#pragma unroll
-        for (int g = 0; g < GB; ++g) s[g] = f16_to_f32(srow[GB * b + g]);
-        multiply(c, x, s);
+        for (; b + 1 < mine; ++b) block(true);
+        block(false);
+        ++b;
     }
-    if (f.K % kBlockK && wave == (int)(full % kWaves4)) {          // the last block: nothing past K is read, X is 0 there
-        const int64_t k0 = full * kBlockK;
-        const int left = (int)(f.K - k0);
-        const u32x4 c = load16_edge(crow, 64 * full + 16 * q, (f.K + 7) / 8 * 4);
-        u32x4 x[T][4];
-        float s[GB];
+    if (b < end) {                                // the last block of all: nothing past K is read, X is 0 there
+        const int64_t row = (f.K + 7) / 8 * 4;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            const int64_t k0 = kBlockK * whole + kHalfK * half;
+            if (k0 >= f.K) break;
+            u32x4 x[T][4];
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+            for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) x[t][d] = load16_edge(xrow[t], 2 * (k0 + column<G>(d, q)), 2 * f.K);
+                for (int d = 0; d < 4; ++d) x[t][d] = load16_edge(xrow[t], 2 * (k0 + column<G>(d, q)), 2 * f.K);
 #pragma unroll
-        for (int g = 0; g < GB; ++g) s[g] = g * G < left ? f16_to_f32(srow[GB * full + g]) : 0.0f;
-        multiply(c, x, s);
+            for (int j = 0; j < R; ++j) {
+                const u32x4 c = load16_edge(crow[j] - 16 * q, k0 / 2 + 16 * q, row);
+                const u32x4 s = load16_edge(srow[j], 2 * (k0 / G), scale_bytes);
+                multiply(c, x, (uint64_t)s[1] << 32 | s[0], acc[j]);
+            }
+        }
     }
 #pragma unroll
-    for (int t = 0; t < T; ++t) sums[wave][t][lane] = acc[t];
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int t = 0; t < T; ++t) sums[wave][j * T + t][lane] = acc[j][t];
     __syncthreads();
     // accumulator element e of lane l: token 4 (l / 16) + e, weight row l % 16
-    for (int u = (int)threadIdx.x; u < 64 * T * 4; u += 64 * kWaves4) {
-        const int l = u & 63, e = (u >> 6) & 3, t = u >> 8;
-        const int64_t m = m0 + 16 * t + 4 * (l >> 4) + e, nn = n0 + (l & 15);
-        if (m >= f.M || nn >= f.N) continue;
-        float z = sums[0][t][l][e];
+#pragma unroll 1
+    for (int u = (int)threadIdx.x; u < R * T * 256; u += 64 * kWaves4) {
+        const int l = u & 63, e = (u >> 6) & 3, i = u >> 8;
+        const int64_t m = m0 + 16 * (i % T) + 4 * (l >> 4) + e, n = n0 + 16 * (i / T) + (l & 15);
+        if (m >= f.M || n >= f.N) continue;
+        float z = sums[0][i][l][e];
 #pragma unroll
-        for (int w = 1; w < kWaves4; ++w) z += sums[w][t][l][e];
-        finish(f, m, nn, z);
+        for (int w = 1; w < kWaves4; ++w) z += sums[w][i][l][e];
+        if (cut.parts > 1) cut.sums[((int64_t)part * f.M + m) * f.N + n] = z;
+        else finish(f, m, n, z);
     }
+}
+
+// the parts' sums, in their order, through the epilogue
+__global__ void __launch_bounds__(256) pgq_linear4_join_kernel(pgq_linear4_fwd f, Cut cut)
+{
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, mn = f.M * f.N;
+    if (at >= mn) return;
+    float z = cut.sums[at];
+#pragma unroll 4
+    for (int i = 1; i < cut.parts; ++i) z += cut.sums[at + i * mn];
+    finish(f, at / f.N, at % f.N, z);
+}
+
+// ---- many tokens ------------------------------------------------------------------------------------------
+// Four wavefronts of a workgroup take 16 R weight rows each and share the tokens of a step of 128 columns through LDS; the other
+// four do the same for every other step, and the sums of the two halves are added at the end.
+constexpr int kSharedWaves = 4, kSharedHalves = 2;
+
+template <int T, int R, int G>
+__global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4_shared_kernel(pgq_linear4_fwd f, Cut cut)
+{
+    __shared__ __align__(16) uint8_t lds[kSharedHalves][2][16 * T * 256];
+    const int tid = (int)threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
+    const int mine = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8);            // half
+    const int r = lane & 15, q = lane >> 4;
+    const uint32_t tb = blockIdx.x % (uint32_t)cut.token_blocks, rest = blockIdx.x / (uint32_t)cut.token_blocks;
+    const uint32_t part = rest % (uint32_t)cut.parts;
+    const int64_t m0 = (int64_t)tb * kMost, n0 = ((int64_t)(rest / (uint32_t)cut.parts) * kSharedWaves + wave) * (16 * R);
+    const uint8_t* crow[R];
+    const uint16_t* srow[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const int64_t n = min(n0 + 16 * j + r, f.N - 1);
+        crow[j] = f.codes + n * f.ldc + 16 * q;
+        srow[j] = f.scales + n * f.lds;
+    }
+    // Thread: piece tid % 16 (8 columns) of T token rows, into LDS rows of 256 bytes.  The piece that quarter q supplies to
+    // instruction d lies at place (4 d + q) ^ (row % 16): a 16-byte LDS read is done for lanes 0-3, 12-15 and 20-27 of a half wavefront
+    // together (then for the others), and those are 16 different places.
+    const int piece = tid & 15;
+    int place = piece;
+    if (G == 128) place = 4 * (piece & 3) + (piece >> 2);
+    if (G == 64) place = 8 * (piece >> 3) + 4 * (piece & 1) + 2 * ((piece >> 1) & 1) + ((piece >> 2) & 1);
+    const uint16_t* xrow[T];
+    uint32_t to[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int m = (tid >> 4) + 16 * t;
+        xrow[t] = f.x + min(m0 + m, f.M - 1) * f.ldx + 8 * piece;
+        to[t] = m * 256 + (place ^ (m & 15)) * 16;
+    }
+    constexpr int GH = kHalfK / G;
+    const int64_t row_bytes = (f.K + 7) / 8 * 4, scale_bytes = 2 * ((f.K + G - 1) / G);
+    const int64_t whole = f.K / kHalfK, steps = (f.K + kHalfK - 1) / kHalfK;
+    const int64_t b0 = (int64_t)part * cut.blocks, end = min(steps, b0 + cut.blocks);
+    struct Step { u32x4 x[T], c[R]; uint16_t s[R][GH]; };
+    auto load = [&](int64_t b, Step& h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) h.x[t] = load16(xrow[t] + kHalfK * b);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            h.c[j] = load16(crow[j] + kHalfK / 2 * b);
+            __builtin_memcpy(h.s[j], srow[j] + GH * b, 2 * GH);
+        }
+    };
+    auto put_x = [&](int i, const Step& h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) *reinterpret_cast<u32x4*>(&lds[mine][i & 1][to[t]]) = h.x[t];
+    };
+    f32x4 acc[R][T];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[j][t] = f32x4{};
+    auto step = [&](int i, const Step& h) __attribute__((always_inline)) {
+        u32x4 c[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            c[j] = h.c[j];
+            trade<G>(c[j]);
+        }
+#pragma unroll
+        for (int g = 0; g < GH; ++g) {
+            f32x4 p[R][T];
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+#pragma unroll
+                for (int t = 0; t < T; ++t) p[j][t] = f32x4{};
+#pragma unroll
+            for (int d = g * (4 / GH); d < (g + 1) * (4 / GH); ++d) {
+                bf16x8 x[T];
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    x[t] = *reinterpret_cast<const bf16x8*>(&lds[mine][i & 1][(16 * t + r) * 256 + ((4 * d + q) ^ r) * 16]);
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    const bf16x8 w = decode8(c[j][d]);
+#pragma unroll
+                    for (int t = 0; t < T; ++t) p[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t], w, p[j][t], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const float s = f16_to_f32(h.s[j][g]);
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][t][e] = __builtin_fmaf(p[j][t][e], s, acc[j][t][e]);
+            }
+        }
+    };
+    // Whole steps: this half's are b0 + mine, b0 + mine + 2, ...; both halves take as many turns, for the barriers' sake.
+    const int64_t last = min(end, whole);
+    const int n = (int)max((int64_t)0, last - b0), turns = (n + 1) / 2, own = (n - mine + 1) / 2;
+    if (n > 0) {
+        auto at = [&](int i) __attribute__((always_inline)) { return min(b0 + mine + 2 * i, last - 1); };      // (loads past the last repeat it)
+        Step ring[2];
+        load(at(0), ring[0]);
+        put_x(0, ring[0]);
+#pragma unroll 1
+        for (int b = 0; b < turns; b += 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                __syncthreads();
+                load(at(b + i + 1), ring[1 - i]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (b + i < own) step(b + i, ring[i]);
+                if (b + i + 1 >= turns) break;
+                put_x(b + i + 1, ring[1 - i]);
+            }
+        }
+    }
+    if (last < end) {                             // the last step, by the first half: nothing past K is read, X is 0 there
+        Step h;
+        if (mine == 0) {
+#pragma unroll
+            for (int t = 0; t < T; ++t) h.x[t] = load16_edge(xrow[t] - 8 * piece, 2 * (kHalfK * last + 8 * piece), 2 * f.K);
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                h.c[j] = load16_edge(crow[j] - 16 * q, kHalfK / 2 * last + 16 * q, row_bytes);
+                const u32x4 s = load16_edge(srow[j], 2 * GH * last, scale_bytes);
+                __builtin_memcpy(h.s[j], &s, 2 * GH);
+            }
+            put_x(turns, h);                      // (the buffer that the turn before the last one used)
+        }
+        __syncthreads();
+        if (mine == 0) step(turns, h);
+    }
+    __syncthreads();
+    f32x4(*sums)[kSharedWaves][R * T][64] = reinterpret_cast<f32x4(*)[kSharedWaves][R * T][64]>(&lds[0][0][0]);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int t = 0; t < T; ++t) sums[mine][wave][j * T + t][lane] = acc[j][t];
+    __syncthreads();
+    // accumulator element e of lane l: token 4 (l / 16) + e, weight row l % 16; each half finishes every other one
+#pragma unroll 1
+    for (int u = lane + 64 * mine; u < R * T * 256; u += 128) {
+        const int e = (u >> 6) & 3, i = u >> 8;
+        const int64_t m = m0 + 16 * (i % T) + 4 * q + e, nn = n0 + 16 * (i / T) + r;
+        if (m >= f.M || nn >= f.N) continue;
+        const float z = sums[0][wave][i][lane][e] + sums[1][wave][i][lane][e];
+        if (cut.parts > 1) cut.sums[((int64_t)part * f.M + m) * f.N + nn] = z;
+        else finish(f, m, nn, z);
+    }
+}
+
+// ---- one to four tokens ---------------------------------------------------------------------------------
+// A wavefront lies along K: lane l holds 32 columns of each slab of 2048, whose tokens stay in its registers while rows go by,
+// 16 bytes of codes and one scale a lane, row and slab; v_dot2_f32_bf16 multiplies.  Nothing is shared before a row's 64
+// partial sums are added, so the codes of the next rows are always in flight.
+constexpr int kStreamWaves = 4;
+constexpr int kSlab = 2048;
+
+struct Stream {
+    int32_t rows;                // of a wavefront, or of the `split` that share them
+    int32_t split;               // wavefronts of a workgroup that share rows, each with its slabs of K
+};
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float x)
+{
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false));
+}
+// the sum over the wavefront, in lane 63
+__device__ __forceinline__ float wave_sum(float x)
+{
+    x = dpp_add<0xB1, 0xF>(x);                    // quad_perm: lane ^ 1
+    x = dpp_add<0x4E, 0xF>(x);                    // quad_perm: lane ^ 2
+    x = dpp_add<0x141, 0xF>(x);                   // row_half_mirror
+    x = dpp_add<0x140, 0xF>(x);                   // row_mirror: every lane of a row of 16 has its sum
+    x = dpp_add<0x142, 0xA>(x);                   // row_bcast 15 to rows 1 and 3
+    return dpp_add<0x143, 0xC>(x);                // row_bcast 31 to rows 2 and 3
+}
+
+// S: slabs of a wavefront, M: tokens.  K a multiple of 32, K <= 2048 S split.
+template <int S, int M>
+__global__ void __launch_bounds__(64 * kStreamWaves) pgq_linear4_stream_kernel(pgq_linear4_fwd f, Stream a)
+{
+    constexpr int RG = 8 / S;       // rows loaded together: 8 KB
+    __shared__ float part[kStreamWaves][M][64];
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int piece = wave % a.split;
+    const int64_t w = (int64_t)blockIdx.x * (kStreamWaves / a.split) + wave / a.split;
+    const int64_t first = min(f.N, w * a.rows), last = min(f.N, first + a.rows);
+    const int shift = 31 - __builtin_clz((unsigned)f.group);
+    uint32_t x[M][S][16];
+    uint32_t code_at[S], scale_at[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int64_t k = ((int64_t)piece * S + s) * kSlab + 32 * lane;
+        const bool in = k < f.K;                          // lanes past K: token values of 0, any codes and scale of the row
+        code_at[s] = in ? (uint32_t)(k / 2) : 0u;
+        scale_at[s] = in ? (uint32_t)(k >> shift) : 0u;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32x4 v = {};
+                if (in) v = load16(f.x + m * f.ldx + k + 8 * i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[m][s][4 * i + e] = v[e];
+            }
+    }
+    struct Rows { u32x4 c[RG][S]; uint16_t s[RG][S]; };
+    auto load = [&](int64_t n, Rows& h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < RG; ++j) {
+            const int64_t row = min(n + j, f.N - 1);      // (rows past the last are not stored)
+            const uint8_t* c = f.codes + row * f.ldc;
+            const uint16_t* sc = f.scales + row * f.lds;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                h.c[j][s] = load16_once(c + code_at[s]);
+                h.s[j][s] = sc[scale_at[s]];
+            }
+        }
+    };
+    float sum[M];                                         // lane i: of row first + i
+#pragma unroll
+    for (int m = 0; m < M; ++m) sum[m] = 0.0f;
+    auto multiply = [&](int64_t n, const Rows& h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < RG; ++j) {
+            float acc[M];
+#pragma unroll
+            for (int m = 0; m < M; ++m) acc[m] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                float p[M];
+#pragma unroll
+                for (int m = 0; m < M; ++m) p[m] = 0.0f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const u32x4 v = __builtin_bit_cast(u32x4, decode8(h.c[j][s][d]));
+#pragma unroll
+                    for (int m = 0; m < M; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t ve = v[e];
+                            p[m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, ve), __builtin_bit_cast(bf16x2, x[m][s][4 * d + e]), p[m], false);
+                        }
+                }
+#pragma unroll
+                for (int m = 0; m < M; ++m) acc[m] = __builtin_fmaf(p[m], f16_to_f32(h.s[j][s]), acc[m]);
+            }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const int total = __builtin_amdgcn_readlane(__builtin_bit_cast(int, wave_sum(acc[m])), 63);
+                sum[m] = lane == (int)(n - first) + j ? __builtin_bit_cast(float, total) : sum[m];
+            }
+        }
+    };
+    if (first < last) {
+        Rows h, next;
+        load(first, h);
+        int64_t n = first;
+#pragma unroll 1
+        for (; n + RG < last; n += RG) {
+            load(n + RG, next);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(n, h);
+            h = next;
+        }
+        multiply(n, h);
+    }
+    if (a.split > 1) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) part[wave][m][lane] = sum[m];
+        __syncthreads();
+        if (piece != 0) return;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            for (int i = 1; i < a.split; ++i) sum[m] += part[wave + i][m][lane];
+    }
+    if (first + lane >= last) return;
+#pragma unroll
+    for (int m = 0; m < M; ++m) finish(f, m, first + lane, sum[m]);
 }
 
 pgq_status check(const pgq_linear4_fwd* p)
@@ -198,15 +597,133 @@ pgq_status check(const pgq_linear4_fwd* p)
     return any_clash(spans, 1, 6) ? PGQ_ERR_PARAM : PGQ_OK;
 }
 int64_t token_blocks(const pgq_linear4_fwd& p) { return (p.M + kMost - 1) / kMost; }
-int64_t grid_of(const pgq_linear4_fwd& p) { return (p.N + 15) / 16 * token_blocks(p); }
-bool launches_fit(const pgq_linear4_fwd& p) { return grid_fits(grid_of(p), 64 * kWaves4); }
+int token_tiles(const pgq_linear4_fwd& p) { return p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4; }
 
-template <int T>
-const void* kernel(int32_t group)
+// ---- how a call runs ----------------------------------------------------------------------------------
+enum Path { P_STREAM, P_ROWS, P_SHARED };
+struct Plan {
+    int path;
+    int rows;                    // R, or the slabs of a streaming wavefront
+    Stream stream;
+    Cut cut;
+    size_t bytes;
+};
+
+// Streaming: wavefronts along K.
+bool stream_plan(const pgq_linear4_fwd& p, Plan& q)
 {
-    return group == 32   ? reinterpret_cast<const void*>(&pgq_linear4_kernel<T, 32>)
-           : group == 64 ? reinterpret_cast<const void*>(&pgq_linear4_kernel<T, 64>)
-                         : reinterpret_cast<const void*>(&pgq_linear4_kernel<T, 128>);
+    const int64_t slabs = (p.K + kSlab - 1) / kSlab, most = p.M == 1 ? 4 : 2;
+    if (p.M > 2 || p.K == 0 || p.K % 32 != 0 || slabs > most * kStreamWaves) return false;
+    q.path = P_STREAM;
+    q.stream.split = slabs <= most ? 1 : slabs <= 2 * most ? 2 : 4;
+    q.rows = (int)((slabs + q.stream.split - 1) / q.stream.split);
+    const int64_t group = 8 / q.rows, waves = (q.rows >= 3 ? 1024 : 8192) / q.stream.split, per = (p.N + waves - 1) / waves;
+    q.stream.rows = (int32_t)std::min<int64_t>(64, (per + group - 1) / group * group);
+    return true;
+}
+
+// One way to cut a call for the kernels of 16-row tiles, and its estimated microseconds past the launch: turns of the kernel's K
+// loop times their measured length, 256 workgroups at a time, and the second launch with the traffic of the parts' sums (at
+// 5 TB/s, written and read).
+double tile_cost(const pgq_linear4_fwd& p, int path, int rows, int64_t parts, Cut& cut)
+{
+    const int t = token_tiles(p);
+    const int64_t units = path == P_ROWS ? (p.K + kBlockK - 1) / kBlockK : (p.K + kHalfK - 1) / kHalfK;
+    const int64_t together = path == P_ROWS ? kWaves4 : kSharedHalves;        // units of K a workgroup takes at a time
+    const int64_t tile = 16 * rows * (path == P_ROWS ? 1 : kSharedWaves);
+    const int64_t grid = (p.N + tile - 1) / tile * token_blocks(p) * parts, per = (units + parts - 1) / parts;
+    if (parts > 1 && (per < together || (parts - 1) * per >= units || grid > 512)) return -1.0;
+    cut.parts = (int32_t)parts;
+    cut.blocks = per;
+    const double full = (double)grid / 256.0;
+    double turn;
+    if (path == P_ROWS) turn = t == 1 ? 0.9 + 0.07 * (double)p.M + 0.3 * (rows - 1) : 3.6 + 1.5 * (rows - 1);
+    else turn = t == 2 ? 0.95 : rows == 1 ? 1.0 + 0.3 * std::min(1.0, full) : 1.8;
+    const double join = parts > 1 ? 4.0 + (double)parts * (double)p.M * (double)p.N * 8.0 / 5e6 : 0.0;
+    return (double)((per + together - 1) / together) * turn * std::max(1.0, full) + join;
+}
+
+// Streaming for one or two tokens; tiles of 16 rows with K spread over a workgroup for up to 16 tokens, with the tokens shared through
+// LDS for more than 32, and the cheaper of both between.  Measured on one MI355X in us (rows kernel, shared kernel, plan):
+//   tokens x K x N        rows    shared        tokens x K x N         rows    shared
+//   16 x 4096 x 4096       7.1     11.4         32 x 4096 x 14336      23.1     19.6
+//   16 x 8192 x 8192      15.7     20.7         32 x 28672 x 8192      70       58
+//   32 x 4096 x 4096      10.7     12.2         64 x 4096 x 4096       18.6     14.8
+//   32 x 8192 x 8192      23.1     23.4         64 x 8192 x 8192       41       28
+// The number of rows and parts chosen this way was within 8% of the best of all that were tried at 28 of 30 sizes.
+Plan plan(const pgq_linear4_fwd& p)
+{
+    Plan q;
+    memset(&q, 0, sizeof(q));
+    if (stream_plan(p, q)) return q;
+    const int t = token_tiles(p);
+    double best = -1.0;
+    for (int path = t == 4 ? P_SHARED : P_ROWS; path <= (t == 1 ? P_ROWS : P_SHARED); ++path)
+        for (int rows = 1; rows <= (t == 1 ? 4 : path == P_SHARED && t == 2 ? 1 : 2); rows *= 2)
+            for (int64_t parts = 1; parts <= 16; parts *= 2) {
+                Cut cut = {};
+                const double us = tile_cost(p, path, rows, parts, cut);
+                if (us < 0) break;
+                if (best >= 0 && us >= best) continue;
+                best = us;
+                q.path = path;
+                q.rows = rows;
+                q.cut = cut;
+            }
+    q.cut.token_blocks = (int32_t)token_blocks(p);
+    q.bytes = q.cut.parts > 1 ? ((size_t)q.cut.parts * p.M * p.N * 4 + 255) / 256 * 256 : 0;
+    return q;
+}
+int64_t stream_grid(const pgq_linear4_fwd& p, const Plan& q)
+{
+    const int64_t rows = (int64_t)q.stream.rows * (kStreamWaves / q.stream.split);
+    return (p.N + rows - 1) / rows;
+}
+int64_t grid_of(const pgq_linear4_fwd& p, const Plan& q)
+{
+    if (q.path == P_STREAM) return stream_grid(p, q);
+    const int64_t rows = 16 * q.rows * (q.path == P_SHARED ? kSharedWaves : 1);
+    return (p.N + rows - 1) / rows * q.cut.token_blocks * q.cut.parts;
+}
+int block_of(const Plan& q) { return 64 * (q.path == P_STREAM ? kStreamWaves : q.path == P_SHARED ? kSharedWaves * kSharedHalves : kWaves4); }
+int64_t join_grid(const pgq_linear4_fwd& p) { return (p.M * p.N + 255) / 256; }
+bool launches_fit(const pgq_linear4_fwd& p, const Plan& q)
+{
+    return grid_fits(grid_of(p, q), block_of(q)) && (q.cut.parts <= 1 || grid_fits(join_grid(p), 256));
+}
+
+const void* stream_kernel(int slabs, int m)
+{
+    if (m == 2) return slabs == 1 ? reinterpret_cast<const void*>(&pgq_linear4_stream_kernel<1, 2>) : reinterpret_cast<const void*>(&pgq_linear4_stream_kernel<2, 2>);
+    return slabs == 1   ? reinterpret_cast<const void*>(&pgq_linear4_stream_kernel<1, 1>)
+           : slabs == 2 ? reinterpret_cast<const void*>(&pgq_linear4_stream_kernel<2, 1>)
+           : slabs == 3 ? reinterpret_cast<const void*>(&pgq_linear4_stream_kernel<3, 1>)
+                        : reinterpret_cast<const void*>(&pgq_linear4_stream_kernel<4, 1>);
+}
+template <int T, int R>
+const void* rows_kernel(int32_t group)
+{
+    return group == 32   ? reinterpret_cast<const void*>(&pgq_linear4_rows_kernel<T, R, 32>)
+           : group == 64 ? reinterpret_cast<const void*>(&pgq_linear4_rows_kernel<T, R, 64>)
+                         : reinterpret_cast<const void*>(&pgq_linear4_rows_kernel<T, R, 128>);
+}
+template <int T, int R>
+const void* shared_kernel(int32_t group)
+{
+    return group == 32   ? reinterpret_cast<const void*>(&pgq_linear4_shared_kernel<T, R, 32>)
+           : group == 64 ? reinterpret_cast<const void*>(&pgq_linear4_shared_kernel<T, R, 64>)
+                         : reinterpret_cast<const void*>(&pgq_linear4_shared_kernel<T, R, 128>);
+}
+const void* kernel_of(const pgq_linear4_fwd& p, const Plan& q)
+{
+    const int t = token_tiles(p), g = p.group;
+    if (q.path == P_STREAM) return stream_kernel(q.rows, (int)p.M);
+    if (q.path == P_ROWS) {
+        if (t == 1) return q.rows == 1 ? rows_kernel<1, 1>(g) : q.rows == 2 ? rows_kernel<1, 2>(g) : rows_kernel<1, 4>(g);
+        return q.rows == 1 ? rows_kernel<2, 1>(g) : rows_kernel<2, 2>(g);
+    }
+    if (t == 2) return shared_kernel<2, 1>(g);
+    return q.rows == 1 ? shared_kernel<4, 1>(g) : shared_kernel<4, 2>(g);
 }
 
 }  // namespace
@@ -221,8 +738,9 @@ pgq_status pgq_linear4_forward_workspace(const pgq_linear4_fwd* p, size_t* works
     if (!workspace_bytes) return PGQ_ERR_NULL;
     const pgq_status st = check(p);
     if (st != PGQ_OK) return st;
-    if (!launches_fit(*p)) return PGQ_ERR_SHAPE;
-    *workspace_bytes = 0;
+    const Plan q = plan(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
+    *workspace_bytes = q.bytes;
     return PGQ_OK;
 }
 
@@ -230,12 +748,16 @@ pgq_status pgq_linear4_forward(const pgq_linear4_fwd* p, void* workspace, size_t
 {
     const pgq_status st = check(p);
     if (st != PGQ_OK || p->M == 0 || p->N == 0) return st;
-    if (!launches_fit(*p)) return PGQ_ERR_SHAPE;
+    Plan q = plan(*p);
+    if (!launches_fit(*p, q)) return PGQ_ERR_SHAPE;
+    if (q.bytes && (!workspace || workspace_bytes < q.bytes)) return PGQ_ERR_WORKSPACE;
+    if (q.bytes && !is_aligned(workspace, 256)) return PGQ_ERR_ALIGN;
     pgq_linear4_fwd f = *p;
-    int32_t tb = (int32_t)token_blocks(f);
-    void* args[] = {&f, &tb};
-    Launches l(1, stream);
-    l.go(f.M <= 16 ? kernel<1>(f.group) : f.M <= 32 ? kernel<2>(f.group) : kernel<4>(f.group), grid_of(f), 64 * kWaves4, args);
+    q.cut.sums = static_cast<float*>(workspace);
+    void *sargs[] = {&f, &q.stream}, *args[] = {&f, &q.cut};
+    Launches l(q.cut.parts > 1 ? 2 : 1, stream);
+    l.go(kernel_of(f, q), grid_of(f, q), block_of(q), q.path == P_STREAM ? sargs : args);
+    if (q.cut.parts > 1) l.go(reinterpret_cast<const void*>(&pgq_linear4_join_kernel), join_grid(f), 256, args);
     return l.done();
 }
 

@@ -411,8 +411,8 @@ pgq_status pgq_linear_backward_plan(const pgq_linear_bwd* p, pgq_linear_plan* ou
 /* bytes), scales (row stride lds) and, when dq is not NULL, the values (dq_dtype PGQ_F32, or PGQ_BF16:   */
 /* rounded to nearest even; row stride ldq).  Bytes of the outputs between their rows are left as they  */
 /* are.  dev_status: PGQ_DEV_NONFINITE and PGQ_DEV_SCALE_OVF; the outputs of such a group are          */
-/* unspecified.  Sizes below 2^31; PGQ_ERR_SHAPE too where the launch would pass 2^32 threads (about      */
-/* 2^35 elements).  Outputs that share memory with another argument: PGQ_ERR_PARAM.                    */
+/* unspecified.  Sizes below 2^31; PGQ_ERR_SHAPE too where the launch would pass 2^32 threads (no matrix of  */
+/* less than 2^34 elements).  Outputs that share memory with another argument: PGQ_ERR_PARAM.            */
 pgq_status pgq_quantize_groups(const void* w, int32_t w_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t group,
                                uint8_t* codes, int64_t ldc, uint16_t* scales, int64_t lds, void* dq, int32_t dq_dtype,
                                int64_t ldq, uint32_t* dev_status, void* stream);

@@ -26,8 +26,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kArgTensors = 128;                  // tensors in the kernel arguments of a launch
 constexpr int64_t kTile = 16384;                  // elements of the smallest tile
-constexpr int64_t kTilesWanted = 1024;            // tiles grow until about so many are left: 4 workgroups a compute unit (30.7 M bf16
-                                                  // 14.3 us, 16.0 with 2048, 14.0 with 512, whose scaling pass takes 2 to 4 us longer)
+// Tiles grow until about so many are left, 4 workgroups a compute unit (30.7 M bf16 a call 13.3 us, with 2048 15.0, with 512 14.0).
+constexpr int64_t kTilesWanted = 1024;
 // Counts of finished workgroups.  One counter takes an increment every 13 ns, which for 1900 workgroups is longer than the
 // reading (30.7 M bf16: 32 us), so large grids count in kCounters groups and then the groups.  Each counter has a cache
 // line, and a memory channel, of its own.
@@ -193,13 +193,9 @@ __global__ void __launch_bounds__(kThreads) pgq_grad_norm_kernel(NormArgs a, Ten
     if (!finite && a.status) atomicOr(a.status, PGQ_DEV_NONFINITE);
 }
 
-// Loads and stores go past the caches: written through them, 87 MB of fp32 gradients were still on their way out while the next
-// norm was read (norm and scaling of five such sets in turn 58 us each, so 49).
 template <typename T>
 __device__ __forceinline__ void scale_all(T* p, int64_t count, float factor)
 {
-    typedef u32x4 any_u32x4 __attribute__((aligned(2)));
-    typedef __attribute__((address_space(1))) any_u32x4 Piece;
     constexpr int V = 16 / sizeof(T), U = 4;
     constexpr int64_t kStep = (int64_t)kThreads * V;
     auto times = [&](u32x4 v) __attribute__((always_inline)) {
@@ -215,9 +211,12 @@ __device__ __forceinline__ void scale_all(T* p, int64_t count, float factor)
     for (; i + (U - 1) * kStep + V <= count; i += U * kStep) {
         u32x4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = __builtin_nontemporal_load((const Piece*)(p + i + u * kStep));
+        for (int u = 0; u < U; ++u) v[u] = load16(p + i + u * kStep);
 #pragma unroll
-        for (int u = 0; u < U; ++u) __builtin_nontemporal_store(times(v[u]), (Piece*)(p + i + u * kStep));
+        for (int u = 0; u < U; ++u) {
+            const u32x4 o = times(v[u]);
+            __builtin_memcpy(p + i + u * kStep, &o, 16);
+        }
     }
     for (; i + V <= count; i += kStep) {
         const u32x4 o = times(load16(p + i));

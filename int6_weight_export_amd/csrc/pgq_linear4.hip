@@ -1,11 +1,15 @@
 // pgq_linear4.hip -- the linear layer over 4-bit weights with group scales, for few tokens (gfx950):
 // Y = act(X W^T + b) + R, W[n][k] = code[n][k] * s[n][k / group].
 //
-// The codes are the traffic: N K / 2 bytes, each read once.  A workgroup takes 16 weight rows and its wavefronts
-// blocks of 128 columns in turn; v_mfma_f32_16x16x32_bf16 multiplies 16 tokens (A) with the 16 rows (B).  Codes are
-// whole numbers, which bf16 holds, and products with bf16 tokens are exact in fp32: the matrix cores sum x * code over
-// a group and one multiply-add per sum brings in the group's scale, so no weight is ever rounded and a weight costs no
-// multiplication of its own.
+// The codes are the traffic: N K / 2 bytes, each read once.  Codes are whole numbers, which bf16 holds, and their products
+// with bf16 tokens are exact in fp32: x * code is summed over a group and one multiply-add per sum brings in the group's
+// scale, so no weight is ever rounded and a weight costs no multiplication of its own.  Three kernels:
+//   stream   1 and 2 tokens: a wavefront along K, tokens in its registers, rows streaming by (8192 -> 28672, one token: 22 us,
+//            5.5 TB/s; the tiles below 33)
+//   rows     up to 32: 16 R weight rows a workgroup, K spread over its wavefronts, sums joined through LDS
+//   shared   17 to 64: 64 R rows a workgroup, the tokens of a step of K shared through LDS
+// The last two multiply on the matrix cores, v_mfma_f32_16x16x32_bf16 with 16 tokens as A and 16 weight rows as B, so that a lane
+// has the sums of one weight row and needs one scale.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -64,7 +68,8 @@ __device__ __forceinline__ int column(int d, int q)
     return 32 * d + 8 * q;
 }
 
-// 16 bytes at any address that this call reads once: past the caches that hold the tokens
+// 16 bytes at any address, past the caches: for whole rows in one go (8192 -> 28672 25.7 -> 22.2 us).  The tiles' loads, 64 bytes
+// of a row each, lose by it: the other half of the line is gone when its turn comes (64 tokens 71 -> 82 us).
 __device__ __forceinline__ u32x4 load16_once(const void* p)
 {
     typedef u32x4 any_u32x4 __attribute__((aligned(1)));
@@ -95,7 +100,8 @@ __device__ __forceinline__ void finish(const pgq_linear4_fwd& f, int64_t m, int6
     store_any(f.y, f.y_dtype, m * f.ldy + n, y);
 }
 
-// How the work is cut: workgroups of 16 R weight rows, their K in `parts` pieces of `blocks` blocks.
+// ---- rows ---------------------------------------------------------------------------------------------
+// How the work is cut: K in `parts` pieces of `blocks` units (256 columns; shared: steps of 128), one for each of as many workgroups.
 struct Cut {
     float* sums;                 // parts > 1: parts x M x N
     int64_t blocks;
@@ -103,7 +109,12 @@ struct Cut {
 };
 
 // T: tiles of 16 tokens, R: of 16 weight rows.  Lane l: token l % 16 of A, weight row l % 16 of B, columns by the quarter
-// l / 16.  Lanes past M or N repeat the last row, whose sums they do not store.
+// l / 16.  Lanes past N repeat the last row, whose sums they do not store.
+//
+// What bounds it is how fast a compute unit takes in cache lines: besides the codes every workgroup reads all of X (16 tokens
+// by 4096: 131 KB beside 32 KB of codes for R = 1).  R = 2 and 4 read it half and a quarter as often and serve where N still fills the
+// machine (8192 -> 8192, 16 tokens, R = 1, 2, 4: 21.3, 15.7, 19.6 us; 4096 -> 28672: 35, 35, 26).  Scales come 16 bytes of a row at a
+// time, not a few for each block (one token 8192 -> 28672 38 -> 33 us).
 template <int T, int R, int G>
 __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_linear4_fwd f, Cut cut)
 {
@@ -282,9 +293,13 @@ __global__ void __launch_bounds__(256) pgq_linear4_join_kernel(pgq_linear4_fwd f
     finish(f, at / f.N, at % f.N, z);
 }
 
-// ---- many tokens ------------------------------------------------------------------------------------------
+// ---- shared ---------------------------------------------------------------------------------------------
 // Four wavefronts of a workgroup take 16 R weight rows each and share the tokens of a step of 128 columns through LDS; the other
-// four do the same for every other step, and the sums of the two halves are added at the end.
+// four do the same for every other step, and the sums of the two halves are added at the end.  One barrier a turn; the next
+// turn's operands are loaded into registers meanwhile (two turns ahead: no faster, the registers cost a workgroup).
+//
+// Bounded by cache lines again, mostly X's (8192 -> 28672, 64 tokens, R = 1, 70 us: without X's loads 46, without the codes' 49;
+// without the LDS reads or the decoding 70).  R = 2 halves them: 63 us.
 constexpr int kSharedWaves = 4, kSharedHalves = 2;
 
 template <int T, int R, int G>
@@ -436,10 +451,12 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
     }
 }
 
-// ---- one to four tokens ---------------------------------------------------------------------------------
+// ---- stream ---------------------------------------------------------------------------------------------
 // A wavefront lies along K: lane l holds 32 columns of each slab of 2048, whose tokens stay in its registers while rows go by,
-// 16 bytes of codes and one scale a lane, row and slab; v_dot2_f32_bf16 multiplies.  Nothing is shared before a row's 64
-// partial sums are added, so the codes of the next rows are always in flight.
+// 16 bytes of codes and one scale a lane, row and slab; v_dot2_f32_bf16 multiplies (two additions of fp32 each).  Nothing is shared
+// before a row's 64 partial sums are added, so the codes of the next 8 KB of rows are always in flight, and a row is read in one go:
+// 4096 -> 4096 4.1 us of which 2.5 are any kernel's, 8192 -> 8192 9.0, 8192 -> 28672 22.2, 4096 -> 128256 45.5 (5.9 TB/s).  With
+// three and four tokens the multiplications take over (8192 -> 28672: 42 and 50 us, the tiles 35).
 constexpr int kStreamWaves = 4;
 constexpr int kSlab = 2048;
 
@@ -609,7 +626,10 @@ struct Plan {
     size_t bytes;
 };
 
-// Streaming: wavefronts along K.
+// Streaming needs whole 32 columns a lane and at most four slabs (two tokens: two) a wavefront, sixteen (eight) a workgroup.  With three or
+// four slabs one wavefront a SIMD takes an equal share of the rows (8192 -> 28672, 1024 and 8192 wavefronts: 22.2 and 25.8 us, 14336
+// -> 4096 9.0 and 10.4); with fewer, every load of rows has a wavefront of its own (4096 -> 14336 8.9 and 8.6, 2048 -> 16384 6.5
+// and 5.5).
 bool stream_plan(const pgq_linear4_fwd& p, Plan& q)
 {
     const int64_t slabs = (p.K + kSlab - 1) / kSlab, most = p.M == 1 ? 4 : 2;

@@ -199,6 +199,37 @@ def test_linear_shapes(M, N, K, group):
         within(got, yr, ey, "y")
 
 
+# sizes that bring every kernel, tile and way of cutting K into use: rows streamed by one, two and four wavefronts with one to four
+# slabs each; 16, 32 and 64 rows a workgroup; tokens through LDS; parts of K
+KERNELS = [(1, 40, 2048), (1, 100, 4096), (1, 33, 6144), (1, 70, 8192), (1, 20, 16384), (1, 35, 26656), (2, 50, 2048), (2, 90, 4064),
+           (2, 40, 8192), (2, 9, 16384), (1, 70000, 64), (1, 66000, 6176), (2, 70000, 32),
+           (1, 4100, 520), (3, 4100, 520), (16, 8200, 520), (9, 16000, 300), (6, 48, 16392), (16, 130, 9000), (20, 4100, 520), (32, 8192, 4000), (25, 14400, 520),
+           (30, 48, 16392), (40, 4100, 520), (64, 30000, 300), (33, 30000, 520), (64, 80, 16392), (50, 520, 4100), (64, 8200, 1030), (129, 300, 4100)]
+
+
+@pytest.mark.parametrize("M,N,K", KERNELS)
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear_kernels(M, N, K, group):
+    say(f"linear4 kernels {M}x{N}x{K} group {group}")
+    rng = np.random.default_rng(M + N + K)
+    code = rng.integers(-7, 8, (N, K)).astype(np.int8)
+    scale = (rng.random((N, -(-K // group))) * 0.02).astype(np.float16)
+    x = randn((M, K), 1, torch.bfloat16)
+    r = randn((M, N), 2)
+    got = ops.qlinear4(x, torch.from_numpy(g4_pack_fast(code)).cuda(), torch.from_numpy(scale).cuda(), group=group, residual=r,
+                       out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    # (in 64 bits on the GPU: the largest of these have 10^9 products)
+    w = torch.from_numpy(code).cuda().double() * torch.from_numpy(scale).cuda().double().repeat_interleave(group, 1)[:, :K]
+    z, mag = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    want = z + r.double()
+    # (K - 1 additions and a scale's rounding, the residual's addition, the store: linear_ref.forward's terms)
+    bound = K * ref.U * mag
+    bound = bound + 2 * ref.U * (want.abs() + bound) + ref.TINY["f32"]
+    err = (got.double() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+
+
 @pytest.mark.parametrize("act,slope", [("none", 0.0), ("relu", 0.0), ("relu", 0.25), ("relu2", 0.0), ("relu2", -0.5), ("silu", 0.0)])
 @pytest.mark.parametrize("M", [1, 20, 64])
 @pytest.mark.parametrize("y,res,bias", [("bf16", "", ""), ("f32", "f32", "bf16"), ("bf16", "bf16", "f32"), ("f32", "bf16", "f32"),
@@ -303,35 +334,40 @@ def test_linear_sums_of_whole_numbers_are_exact(M, K, group):
     assert np.array_equal(got.cpu().numpy().astype(np.float64), want)
 
 
-def test_linear_infinities_and_nan():
+@pytest.mark.parametrize("M,K", [(1, 320), (2, 320), (1, 4096), (5, 320), (20, 320), (40, 320), (40, 4096), (70, 330)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear_infinities_and_nan(M, K, group):
     """An infinite token value gives the formula's infinity or NaN in its own row and leaves the other rows alone; so does a
     bad scale in its own column."""
-    say("linear4 infinities")
-    M, N, K, group = 5, 40, 320, 64
+    say(f"linear4 infinities M={M} K={K} group {group}")
+    N = 40
     codes, scales, w = weights(N, K, group, 21)
     x = randn((M, K), 22, torch.bfloat16)
     clean = ops.qlinear4(x, codes, scales, group=group, out_dtype=torch.float32)
-    x[2, 100] = float("inf")
-    x[3, 7] = float("nan")
+    bad, nan = M // 2, M - 1 if M > 1 else None
+    x[bad, 100] = float("inf")
+    if nan is not None:
+        x[nan, 7] = float("nan")
     got = ops.qlinear4(x, codes, scales, group=group, out_dtype=torch.float32)
     torch.cuda.synchronize()
-    rows = [0, 1, 4]
+    rows = [m for m in range(M) if m not in (bad, nan)]
     assert torch.equal(got[rows], clean[rows])
-    assert bool(torch.isnan(got[3]).all())
-    v = torch.from_numpy(w[:, 100])
-    inf = got[2].cpu()
-    assert bool(torch.isnan(inf[v == 0]).all()) and bool((inf[v > 0] == float("inf")).all()) and bool((inf[v < 0] == float("-inf")).all())
+    assert nan is None or bool(torch.isnan(got[nan]).all())
+    if bad != nan:
+        v = torch.from_numpy(w[:, 100])
+        inf = got[bad].cpu()
+        assert bool(torch.isnan(inf[v == 0]).all()) and bool((inf[v > 0] == float("inf")).all()) and bool((inf[v < 0] == float("-inf")).all())
     x = randn((M, K), 22, torch.bfloat16)
-    for bad in (float("inf"), float("nan")):
+    for value in (float("inf"), float("nan")):
         s = scales.clone()
-        s[9, 4] = bad
+        s[9, scales.shape[1] - 1] = value
         got = ops.qlinear4(x, codes, s, group=group, out_dtype=torch.float32)
         torch.cuda.synchronize()
         cols = [n for n in range(N) if n != 9]
         assert torch.equal(got[:, cols], clean[:, cols]) and not bool(torch.isfinite(got[:, 9]).any())
 
 
-@pytest.mark.parametrize("M", [1, 16, 33])
+@pytest.mark.parametrize("M", [1, 2, 16, 33, 64])
 def test_linear_same_bits_each_time_and_on_two_streams(M):
     say(f"linear4 repeated and on two streams M={M}")
     N, K, group = 400, 4096, 128
@@ -348,11 +384,12 @@ def test_linear_same_bits_each_time_and_on_two_streams(M):
     assert all(torch.equal(o, first) for o in outs)
 
 
-def test_captured_calls_replay():
-    say("quantize, decode and linear4 in a graph")
-    N, K, group = 200, 1000, 64
-    w, x = randn((N, K), 41, std=0.05), randn((4, K), 42, torch.bfloat16)
-    w2, x2 = randn((N, K), 43, std=0.05), randn((4, K), 44, torch.bfloat16)
+@pytest.mark.parametrize("M,K", [(1, 1024), (4, 1000), (4, 16384), (30, 1000), (64, 8192)])
+def test_captured_calls_replay(M, K):
+    say(f"quantize, decode and linear4 in a graph, M={M} K={K}")
+    N, group = 200, 64
+    w, x = randn((N, K), 41, std=0.05), randn((M, K), 42, torch.bfloat16)
+    w2, x2 = randn((N, K), 43, std=0.05), randn((M, K), 44, torch.bfloat16)
     st = ops.new_status()
     torch.cuda.synchronize()
 
@@ -376,7 +413,7 @@ def test_captured_calls_replay():
 
 
 def test_long_rows():
-    """One row of 2^21 + 9 columns: every sum, and a decode past 2^31 bytes of output is addressed with 64 bits elsewhere."""
+    """Two rows of 2^21 + 9 columns of whole numbers: every sum, equal to the last bit."""
     say("linear4 K = 2^21 + 9")
     K, group = (1 << 21) + 9, 128
     rng = np.random.default_rng(1)

@@ -88,6 +88,24 @@ def test_sizes_past_one_launch_are_refused():
     assert pgq.pgq_linear4_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == pgq.PGQ_ERR_SHAPE
 
 
+@pytest.mark.parametrize("M,N,K", [(6, 48, 16392), (30, 48, 16392), (64, 48, 16392), (64, 4096, 4096)])
+def test_workspace_is_required_when_k_is_cut(M, N, K):
+    n = ctypes.c_size_t(0)
+    p = linear(M=M, N=N, K=K, ldx=K, ldc=(K + 7) // 8 * 4, lds=(K + 31) // 32, ldy=N, x=1 << 40, codes=1 << 41, scales=1 << 42, y=1 << 43)
+    assert pgq.pgq_linear4_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == pgq.PGQ_OK
+    assert n.value > 0 and n.value % 256 == 0
+    assert pgq.pgq_linear4_forward(ctypes.byref(p), None, 0, None) == pgq.PGQ_ERR_WORKSPACE
+    assert pgq.pgq_linear4_forward(ctypes.byref(p), FAKE, n.value - 1, None) == pgq.PGQ_ERR_WORKSPACE
+    assert pgq.pgq_linear4_forward(ctypes.byref(p), FAKE + 128, n.value, None) == pgq.PGQ_ERR_ALIGN
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (2, 28672, 8192), (16, 4096, 4096), (5, 717, 1031)])
+def test_no_workspace_otherwise(M, N, K):
+    n = ctypes.c_size_t(7)
+    p = linear(M=M, N=N, K=K, ldx=K, ldc=(K + 7) // 8 * 4, lds=(K + 31) // 32, ldy=N, x=1 << 40, codes=1 << 41, scales=1 << 42, y=1 << 43)
+    assert pgq.pgq_linear4_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == pgq.PGQ_OK and n.value == 0
+
+
 def test_null_descriptors():
     n, p = ctypes.c_size_t(0), linear()
     assert pgq.pgq_linear4_forward(None, None, 0, None) == pgq.PGQ_ERR_NULL

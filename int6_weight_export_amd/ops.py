@@ -23,6 +23,9 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+# The current GPU's index (torch.cuda.current_device() without its 0.2 us of checks: it has been initialized by whoever made the
+# tensors)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # The current stream's handle of GPU `index`: what torch.cuda.current_stream(index).cuda_stream gives, without
 # building the Stream object (2.8 us a call against 0.1).
 _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -446,7 +449,7 @@ def _gpu_of(name: str, t: torch.Tensor) -> int:
 def _launch_linear(fn, size_fn, name: str, desc: bytes, index: int) -> None:
     """One call of a linear-layer entry point on GPU `index`: the scratch, when the call asks for any,
     comes from torch's allocator (ordered with the current stream, private to a graph under capture)."""
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             return _launch_linear(fn, size_fn, name, desc, index)
     stream = _stream_of(index)
@@ -558,7 +561,7 @@ def qlinear_backward(dy: torch.Tensor, codes: Optional[torch.Tensor], scales: Op
 
 def _on_gpu(index: int, name: str, fn, *args) -> None:
     """fn(*args, current stream) with GPU `index` current."""
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             rc = fn(*args, _stream_of(index))
     else:
@@ -715,7 +718,7 @@ class GradNorm:
         self.bind(grads)
         self.workspace = _norm_workspace(self._numel, self.device)
         self.status = new_status(self.device)
-        self.result = torch.empty(2, dtype=torch.float32, device=self.device)
+        self.result = torch.zeros(2).to(self.device)
         self._views = self.result[0], self.result[1]
         self._tail = (self.result.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr())
 
@@ -805,7 +808,7 @@ class AdamW:
         self._g_codes = (ctypes.c_int32 * n)(*[pgq.PGQ_F32] * n)
         self._n_numel = (ctypes.c_int64 * n)(*self._numel)
         self.norm_workspace = _norm_workspace(self._n_numel, self.device)
-        self.norm_result = torch.empty(2, dtype=torch.float32, device=self.device)
+        self.norm_result = torch.zeros(2).to(self.device)
         self.grad_norm = self.norm_result[0]
         self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
@@ -881,7 +884,7 @@ class AdamW:
 
     def _on_device(self, call, *args):
         """call(*args) with this optimizer's GPU current."""
-        if self._index == torch.cuda.current_device():
+        if self._index == _current_device():
             return call(*args)
         with torch.cuda.device(self._index):
             return call(*args)

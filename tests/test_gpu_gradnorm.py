@@ -136,6 +136,18 @@ def test_magnitudes_whose_squares_leave_binary32():
     check([rand(1000, 1)], 1.0, scale=-3.0)
 
 
+def test_more_than_2_31_elements():
+    """Ones: the sum of squares is the number of elements, exact in 64 bits; the last elements are scaled like the first."""
+    say("grad norm of 2^31 + 5 bf16 elements")
+    n = (1 << 31) + 5
+    g = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    gn = ops.GradNorm([g, rand(3, 1)[:0]])
+    gn.clip_(math.sqrt(n) / 4)
+    torch.cuda.synchronize()
+    assert abs(float(gn.result[0]) - math.sqrt(n)) <= REL * math.sqrt(n) and abs(float(gn.result[1]) - 0.25) <= 2.0 ** -25
+    assert int((g != 0.25).sum()) == 0
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), "overflow"])
 def test_not_finite(bad):
     say(f"grad norm with {bad}")

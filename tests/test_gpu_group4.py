@@ -140,6 +140,21 @@ def test_outputs_in_strided_buffers_leave_the_rest():
         assert bool((ob[:, 0] == 5).all()) and bool((ob[:, cols + 1:] == 5).all())
 
 
+def test_more_than_2_32_lanes():
+    """Rows of one column take a whole group of lanes each: places past 2^32 are right."""
+    say("quantize 2^27 + 3 rows of one column")
+    rows = (1 << 27) + 3
+    w = (torch.arange(rows, dtype=torch.int32, device="cuda") % 1999 - 999).float()[:, None] * 0.125
+    got = ops.quantize_groups(w, group=128)
+    torch.cuda.synchronize()
+    a = w[:, 0].abs()
+    s = (a / torch.full_like(a, 7)).half()
+    s = torch.where(s == 0, torch.ones_like(s), s)
+    assert torch.equal(got["scales"][:, 0], s.view(torch.int16))
+    code = torch.where(a == 0, 0, torch.where(w[:, 0] < 0, 15, 7)).to(torch.uint8)
+    assert torch.equal(got["codes"][:, 0], code) and not bool(got["codes"][:, 1:].any()) and int(got["status"].item()) == 0
+
+
 def test_decode_takes_every_code():
     """Bytes that no quantizer writes decode as the layout says: 1000 is +0."""
     say("decode every byte")

@@ -48,7 +48,7 @@
  * stream work that uses it has completed.  The library allocates no device memory and
  * keeps no state besides a per-device cache of launch limits; it is thread-safe.  Host
  * arrays are read during the call only.  Inputs and outputs must not overlap, except
- * that `mean` (and what a call says is updated in place) is.
+ * that `mean`, and whatever else a call says so of, is updated in place.
  */
 #ifndef PGQ_H
 #define PGQ_H
@@ -412,7 +412,8 @@ pgq_status pgq_linear_backward_plan(const pgq_linear_bwd* p, pgq_linear_plan* ou
 /* rounded to nearest even; row stride ldq).  Bytes of the outputs between their rows are left as they  */
 /* are.  dev_status: PGQ_DEV_NONFINITE and PGQ_DEV_SCALE_OVF; the outputs of such a group are          */
 /* unspecified.  Sizes below 2^31; PGQ_ERR_SHAPE too where the launch would pass 2^32 threads (no matrix of  */
-/* less than 2^34 elements).  Outputs that share memory with another argument: PGQ_ERR_PARAM.            */
+/* less than 2^34 elements, its rows filled up to whole groups).  Outputs that share memory with another  */
+/* argument: PGQ_ERR_PARAM.                                                                        */
 pgq_status pgq_quantize_groups(const void* w, int32_t w_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t group,
                                uint8_t* codes, int64_t ldc, uint16_t* scales, int64_t lds, void* dq, int32_t dq_dtype,
                                int64_t ldq, uint32_t* dev_status, void* stream);

@@ -696,7 +696,12 @@ def _norm_workspace(numel, device) -> torch.Tensor:
     over when it returns, so that any stream may use it."""
     need = ctypes.c_size_t(0)
     pgq.check(pgq.pgq_grad_norm_workspace(numel, len(numel), ctypes.byref(need)), "pgq_grad_norm_workspace")
-    return torch.zeros(need.value, dtype=torch.uint8).to(device)
+    return torch.zeros(need.value, dtype=torch.uint8, device="cpu").to(device)
+
+
+def _norm_result(device) -> torch.Tensor:
+    """Norm and factor; made in the same way."""
+    return torch.zeros(2, dtype=torch.float32, device="cpu").to(device)
 
 
 class GradNorm:
@@ -718,7 +723,7 @@ class GradNorm:
         self.bind(grads)
         self.workspace = _norm_workspace(self._numel, self.device)
         self.status = new_status(self.device)
-        self.result = torch.zeros(2).to(self.device)
+        self.result = _norm_result(self.device)
         self._views = self.result[0], self.result[1]
         self._tail = (self.result.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr())
 
@@ -808,7 +813,7 @@ class AdamW:
         self._g_codes = (ctypes.c_int32 * n)(*[pgq.PGQ_F32] * n)
         self._n_numel = (ctypes.c_int64 * n)(*self._numel)
         self.norm_workspace = _norm_workspace(self._n_numel, self.device)
-        self.norm_result = torch.zeros(2).to(self.device)
+        self.norm_result = _norm_result(self.device)
         self.grad_norm = self.norm_result[0]
         self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
@@ -842,7 +847,8 @@ class AdamW:
 
         max_norm: clip the gradients, times grad_scale, to this global norm on the way (they are not written): the step sees
         them times grad_scale * min(1, max_norm / norm).  Returns the norm then, an fp32 number on the GPU that the next clipped step
-        overwrites.  Where it is not finite the step writes nothing and sets PGQ_DEV_NONFINITE in `status`."""
+        overwrites.  Where it is not finite the step writes nothing and sets PGQ_DEV_NONFINITE in `status`; it has been counted all
+        the same, as the host does not wait for the norm."""
         if len(grads) != self.n:
             raise ValueError(f"{len(grads)} gradients for {self.n} weights")
         if not device_hyper and torch.cuda.is_current_stream_capturing():

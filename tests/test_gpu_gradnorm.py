@@ -230,6 +230,23 @@ def test_bind_takes_other_tensors():
     check(other, 1.0, gn=gn)                                # a refused list changes nothing
 
 
+def test_made_under_other_defaults():
+    say("grad norm and optimizer made under another default type and device")
+    g = [rand(1000, 1)]
+    torch.set_default_dtype(torch.bfloat16)
+    torch.set_default_device("cuda")
+    try:
+        gn, opt = ops.GradNorm(g), ops.AdamW([torch.zeros(1000, dtype=torch.float32)], lr=1e-3)
+    finally:
+        torch.set_default_device(None)
+        torch.set_default_dtype(torch.float32)
+    assert gn.result.dtype == torch.float32 and opt.norm_result.dtype == torch.float32
+    check(g, 1.0, gn=gn)
+    norm = opt.step(g, max_norm=1.0)
+    torch.cuda.synchronize()
+    assert torch.equal(norm, gn.result[0])
+
+
 def test_refusals():
     say("grad norm refuses wrong arguments")
     g = rand(100, 1)

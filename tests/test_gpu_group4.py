@@ -349,6 +349,29 @@ def test_linear_sums_of_whole_numbers_are_exact(M, K, group):
     assert np.array_equal(got.cpu().numpy().astype(np.float64), want)
 
 
+@pytest.mark.parametrize("M,K", [(1, 512), (2, 512), (5, 512), (20, 501), (40, 512), (64, 4096)])
+@pytest.mark.parametrize("e", [-130, -124])
+def test_linear_subnormal_tokens(M, K, e):
+    """Tokens 2^e times whole numbers, below binary32's normal range, with scales of 1; then larger ones with scales of 2^-18 to
+    2^-15, which are subnormal in fp16.  Every sum is a power of two times a whole number below 2^20 and a binary32 value, so
+    equal to the last bit, unless a multiplication takes subnormal numbers for zeros."""
+    say(f"linear4 subnormal tokens M={M} K={K} 2^{e}")
+    rng = np.random.default_rng(K + M)
+    N = 40
+    codes = rng.integers(-7, 8, (N, K)).astype(np.int8)
+    scales = (2.0 ** rng.integers(-18, -14, (N, -(-K // 64)))).astype(np.float16)
+    x = rng.integers(-3, 4, (M, K)) * 2.0 ** e
+    xt = torch.from_numpy(x.astype(np.float32)).bfloat16()
+    assert np.array_equal(xt.double().numpy(), x)
+    ones = np.ones_like(scales)
+    for s, up in ((ones, 1.0), (scales, 2.0 ** 30)):
+        got = ops.qlinear4((xt.double() * up).bfloat16().cuda(), torch.from_numpy(g4.pack(codes)).cuda(), torch.from_numpy(s).cuda(),
+                           group=64, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        want = (x * up) @ g4.values(codes, s.view(np.uint16), 64).T
+        assert np.array_equal(got.cpu().numpy().astype(np.float64), want)
+
+
 @pytest.mark.parametrize("M,K", [(1, 320), (2, 320), (1, 4096), (5, 320), (20, 320), (40, 320), (40, 4096), (70, 330)])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_linear_infinities_and_nan(M, K, group):

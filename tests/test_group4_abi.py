@@ -45,6 +45,7 @@ def linear(**kw):
     (dict(codes=FAKE), pgq.PGQ_ERR_PARAM), (dict(dq=FAKE), pgq.PGQ_ERR_PARAM), (dict(scales=FAKE + 0x1000), pgq.PGQ_ERR_PARAM),
     (dict(rows=1 << 30, cols=1 << 10, ld=1 << 10, ldc=1 << 9, lds=1 << 5, codes=FAKE + (1 << 50), scales=FAKE + (1 << 51)),
      pgq.PGQ_ERR_SHAPE),                                      # 2^37 threads
+    (dict(rows=1 << 29, cols=1, ld=1, group=128, ldc=4, lds=1, codes=1 << 40, scales=1 << 41), pgq.PGQ_ERR_SHAPE),   # a group a row: 2^33 threads
     (dict(rows=0), pgq.PGQ_OK), (dict(cols=0, ldc=0, lds=0), pgq.PGQ_OK), (dict(rows=0, w=None, codes=None, scales=None), pgq.PGQ_OK),
 ])
 def test_quantize_argument_errors(args, want):

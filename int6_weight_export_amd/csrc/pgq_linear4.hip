@@ -5,9 +5,9 @@
 // with bf16 tokens are exact in fp32: x * code is summed over a group and one multiply-add per sum brings in the group's
 // scale, so no weight is ever rounded and a weight costs no multiplication of its own.  Three kernels:
 //   stream   1 and 2 tokens: a wavefront along K, tokens in its registers, rows streaming by (8192 -> 28672, one token: 22 us,
-//            5.5 TB/s; the tiles below 33)
-//   rows     up to 32: 16 R weight rows a workgroup, K spread over its wavefronts, sums joined through LDS
-//   shared   17 to 64: 64 R rows a workgroup, the tokens of a step of K shared through LDS
+//            5.5 TB/s)
+//   rows     3 to 32 tokens and few rows: 16 R weight rows a workgroup, K spread over its wavefronts, sums joined through LDS
+//   shared   the rest: 64 R rows a workgroup, the tokens of a block of K shared through LDS (8192 -> 28672, 16 tokens: 30 us)
 // The last two multiply on the matrix cores, v_mfma_f32_16x16x32_bf16 with 16 tokens as A and 16 weight rows as B, so that a lane
 // has the sums of one weight row and needs one scale.
 #include <hip/hip_runtime.h>
@@ -101,7 +101,7 @@ __device__ __forceinline__ void finish(const pgq_linear4_fwd& f, int64_t m, int6
 }
 
 // ---- rows ---------------------------------------------------------------------------------------------
-// How the work is cut: K in `parts` pieces of `blocks` units (256 columns; shared: steps of 128), one for each of as many workgroups.
+// How the work is cut: K in `parts` pieces of `blocks` blocks, one for each of as many workgroups.
 struct Cut {
     float* sums;                 // parts > 1: parts x M x N
     int64_t blocks;
@@ -112,9 +112,9 @@ struct Cut {
 // l / 16.  Lanes past N repeat the last row, whose sums they do not store.
 //
 // What bounds it is how fast a compute unit takes in cache lines: besides the codes every workgroup reads all of X (16 tokens
-// by 4096: 131 KB beside 32 KB of codes for R = 1).  R = 2 and 4 read it half and a quarter as often and serve where N still fills the
-// machine (8192 -> 8192, 16 tokens, R = 1, 2, 4: 21.3, 15.7, 19.6 us; 4096 -> 28672: 35, 35, 26).  Scales come 16 bytes of a row at a
-// time, not a few for each block (one token 8192 -> 28672 38 -> 33 us).
+// by 4096: 131 KB beside 32 KB of codes for R = 1), which R = 2 halves (8192 -> 8192, 16 tokens: 21.3 and 15.7 us; with R = 4 19.6,
+// half of the machine idle) and the shared kernel quarters.  Scales come 16 bytes of a row at a time, not a few for each block (one
+// token 8192 -> 28672 38 -> 33 us).
 template <int T, int R, int G>
 __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_linear4_fwd f, Cut cut)
 {
@@ -294,21 +294,29 @@ __global__ void __launch_bounds__(256) pgq_linear4_join_kernel(pgq_linear4_fwd f
 }
 
 // ---- shared ---------------------------------------------------------------------------------------------
-// Four wavefronts of a workgroup take 16 R weight rows each and share the tokens of a step of 128 columns through LDS; the other
-// four do the same for every other step, and the sums of the two halves are added at the end.  One barrier a turn; the next
-// turn's operands are loaded into registers meanwhile (two turns ahead: no faster, the registers cost a workgroup).
+// Four wavefronts of a workgroup take 16 R weight rows each and share the tokens of a block of 256 columns through LDS; the other
+// four do the same for the second half of the part's blocks, and the sums of the two halves are added at the end.  One barrier a
+// block; the next block's operands are loaded into registers meanwhile.
 //
-// Bounded by cache lines again, mostly X's (8192 -> 28672, 64 tokens, R = 1, 70 us: without X's loads 46, without the codes' 49;
-// without the LDS reads or the decoding 70).  R = 2 halves them: 63 us.
+// What bounds it first is again how many cache lines a compute unit takes in (8192 -> 28672, 32 tokens, R = 2): tokens, codes and
+// scales a million each when a step of K loads its own scales, and 44 us; with scales 64 bytes of a row at a time 37.  Blocks of 128
+// columns leave half of each line of codes for later: 53.  For 64 tokens the multiplications take over (55 us, without any loads of
+// operands 35); codes two and three blocks ahead: no faster.
 constexpr int kSharedWaves = 4, kSharedHalves = 2;
+constexpr int kSubs = kBlockK / kHalfK;
 
 template <int T, int R, int G>
 __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4_shared_kernel(pgq_linear4_fwd f, Cut cut)
 {
-    __shared__ __align__(16) uint8_t lds[kSharedHalves][2][16 * T * 256];
+    __shared__ __align__(16) uint8_t lds[kSharedHalves][2][kSubs * 16 * T * 256];
     const int tid = (int)threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
     const int mine = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8);            // half
     const int r = lane & 15, q = lane >> 4;
+    // A load of 64 bytes of 16 rows costs less where the four lanes of a row are neighbours (8192 -> 28672, R = 1: 16 tokens 31.8 ->
+    // 29.7 us, 32 41.6 -> 38.8), and the words then travel to the lanes that multiply them; with larger tiles the registers
+    // and the way through LDS cost more than that (32 tokens, R = 2: 36.4 -> 37.5; 64: 54 -> 58).
+    constexpr bool kQuads = T * R <= 2;
+    const int code_row = kQuads ? lane >> 2 : r, code_piece = kQuads ? lane & 3 : q;
     const uint32_t tb = blockIdx.x % (uint32_t)cut.token_blocks, rest = blockIdx.x / (uint32_t)cut.token_blocks;
     const uint32_t part = rest % (uint32_t)cut.parts;
     const int64_t m0 = (int64_t)tb * kMost, n0 = ((int64_t)(rest / (uint32_t)cut.parts) * kSharedWaves + wave) * (16 * R);
@@ -316,13 +324,12 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
     const uint16_t* srow[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        const int64_t n = min(n0 + 16 * j + r, f.N - 1);
-        crow[j] = f.codes + n * f.ldc + 16 * q;
-        srow[j] = f.scales + n * f.lds;
+        crow[j] = f.codes + min(n0 + 16 * j + code_row, f.N - 1) * f.ldc + 16 * code_piece;
+        srow[j] = f.scales + min(n0 + 16 * j + r, f.N - 1) * f.lds;
     }
-    // Thread: piece tid % 16 (8 columns) of T token rows, into LDS rows of 256 bytes.  The piece that quarter q supplies to
-    // instruction d lies at place (4 d + q) ^ (row % 16): a 16-byte LDS read is done for lanes 0-3, 12-15 and 20-27 of a half wavefront
-    // together (then for the others), and those are 16 different places.
+    // Thread: piece tid % 16 (8 columns) of each half block of T token rows, into LDS rows of 256 bytes.  The piece that quarter q
+    // supplies to instruction d lies at place (4 d + q) ^ (row % 16): a 16-byte LDS read is done for lanes 0-3, 12-15 and 20-27 of a
+    // half wavefront together (then for the others), and those are 16 different places.
     const int piece = tid & 15;
     int place = piece;
     if (G == 128) place = 4 * (piece & 3) + (piece >> 2);
@@ -337,103 +344,157 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
     }
     constexpr int GH = kHalfK / G;
     const int64_t row_bytes = (f.K + 7) / 8 * 4, scale_bytes = 2 * ((f.K + G - 1) / G);
-    const int64_t whole = f.K / kHalfK, steps = (f.K + kHalfK - 1) / kHalfK;
-    const int64_t b0 = (int64_t)part * cut.blocks, end = min(steps, b0 + cut.blocks);
-    struct Step { u32x4 x[T], c[R]; uint16_t s[R][GH]; };
-    auto load = [&](int64_t b, Step& h) __attribute__((always_inline)) {
+    const int64_t whole = f.K / kBlockK, blocks = (f.K + kBlockK - 1) / kBlockK;
+    const int64_t b0 = (int64_t)part * cut.blocks, end = min(blocks, b0 + cut.blocks);
+    struct Tokens { u32x4 x[kSubs][T]; };
+    struct Codes { u32x4 c[R][kSubs]; };
+    auto load_x = [&](int64_t b, Tokens& h) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) h.x[t] = load16(xrow[t] + kHalfK * b);
+        for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            h.c[j] = load16(crow[j] + kHalfK / 2 * b);
-            __builtin_memcpy(h.s[j], srow[j] + GH * b, 2 * GH);
-        }
+            for (int u = 0; u < kSubs; ++u) h.x[u][t] = load16(xrow[t] + kBlockK * b + kHalfK * u);
     };
-    auto put_x = [&](int i, const Step& h) __attribute__((always_inline)) {
+    auto load_codes = [&](int64_t b, Codes& h) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) *reinterpret_cast<u32x4*>(&lds[mine][i & 1][to[t]]) = h.x[t];
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) h.c[j][u] = load16(crow[j] + kBlockK / 2 * b + kHalfK / 2 * u);
+    };
+    auto put_x = [&](int i, const Tokens& h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+            for (int t = 0; t < T; ++t) *reinterpret_cast<u32x4*>(&lds[mine][i & 1][u * 16 * T * 256 + to[t]]) = h.x[u][t];
+    };
+    // Scales: 64 bytes of a row, 16 in each quarter of the wavefront, for the kRun blocks from a multiple of kRun on.
+    constexpr int SB = kSubs * GH / 2, SW = GH > 1 ? GH / 2 : 1, kRun = 16 / SB;       // words of a block, of half of one; blocks of a load
+    u32x4 held[R];
+    auto load_scales = [&](int64_t run, u32x4* s) __attribute__((always_inline)) {
+        if (64 * run + 64 <= scale_bytes) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) s[j] = load16((const uint8_t*)srow[j] + 64 * run + 16 * q);
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j) s[j] = load16_edge(srow[j], 64 * run + 16 * q, scale_bytes);
+        }
     };
     f32x4 acc[R][T];
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[j][t] = f32x4{};
-    auto step = [&](int i, const Step& h) __attribute__((always_inline)) {
-        u32x4 c[R];
+    // products of block b, whose tokens lie in buffer i
+    auto multiply = [&](int i, int b, const Codes& h) __attribute__((always_inline)) {
+        const int word = SB * b & 15, from = 4 * (16 * (word >> 2) + r);
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            c[j] = h.c[j];
-            trade<G>(c[j]);
-        }
-#pragma unroll
-        for (int g = 0; g < GH; ++g) {
-            f32x4 p[R][T];
+        for (int u = 0; u < kSubs; ++u) {
+            uint32_t sc[R][SW];
 #pragma unroll
             for (int j = 0; j < R; ++j)
 #pragma unroll
-                for (int t = 0; t < T; ++t) p[j][t] = f32x4{};
-#pragma unroll
-            for (int d = g * (4 / GH); d < (g + 1) * (4 / GH); ++d) {
-                bf16x8 x[T];
-#pragma unroll
-                for (int t = 0; t < T; ++t)
-                    x[t] = *reinterpret_cast<const bf16x8*>(&lds[mine][i & 1][(16 * t + r) * 256 + ((4 * d + q) ^ r) * 16]);
-#pragma unroll
-                for (int j = 0; j < R; ++j) {
-                    const bf16x8 w = decode8(c[j][d]);
-#pragma unroll
-                    for (int t = 0; t < T; ++t) p[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t], w, p[j][t], 0, 0, 0);
+                for (int i = 0; i < SW; ++i) {
+                    const int e = u * GH / 2 + i;              // of the block's words
+                    const uint32_t lo = SB == 4 ? held[j][e] : SB == 2 ? held[j][e] : word & 1 ? held[j][1] : held[j][0];
+                    const uint32_t hi = SB == 4 ? held[j][e] : SB == 2 ? held[j][2 + e] : word & 1 ? held[j][3] : held[j][2];
+                    sc[j][i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(word & 2 ? hi : lo));
                 }
-            }
+            u32x4 c[R];
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                const float s = f16_to_f32(h.s[j][g]);
+                c[j] = h.c[j][u];
+                if (kQuads) {
 #pragma unroll
-                for (int t = 0; t < T; ++t)
+                    for (int e = 0; e < 4; ++e) c[j][e] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * r + q), (int)c[j][e]);
+                }
+                trade<G>(c[j]);
+            }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][t][e] = __builtin_fmaf(p[j][t][e], s, acc[j][t][e]);
+            for (int g = 0; g < GH; ++g) {
+                f32x4 p[R][T];
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+#pragma unroll
+                    for (int t = 0; t < T; ++t) p[j][t] = f32x4{};
+#pragma unroll
+                for (int d = g * (4 / GH); d < (g + 1) * (4 / GH); ++d) {
+                    bf16x8 x[T];
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+                        x[t] = *reinterpret_cast<const bf16x8*>(&lds[mine][i & 1][u * 16 * T * 256 + (16 * t + r) * 256 + ((4 * d + q) ^ r) * 16]);
+#pragma unroll
+                    for (int j = 0; j < R; ++j) {
+                        const bf16x8 w = decode8(c[j][d]);
+#pragma unroll
+                        for (int t = 0; t < T; ++t) p[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t], w, p[j][t], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    const int i = u * GH % 2 + g;
+                    const float s = f16_to_f32((uint16_t)(sc[j][i / 2] >> (16 * (i & 1))));
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][t][e] = __builtin_fmaf(p[j][t][e], s, acc[j][t][e]);
+                }
             }
         }
     };
-    // Whole steps: this half's are b0 + mine, b0 + mine + 2, ...; both halves take as many turns, for the barriers' sake.
+    // Whole blocks: the first half takes as many as the second or one more; both take as many turns, for the barriers' sake.
     const int64_t last = min(end, whole);
-    const int n = (int)max((int64_t)0, last - b0), turns = (n + 1) / 2, own = (n - mine + 1) / 2;
+    const int n = (int)max((int64_t)0, last - b0), turns = (n + 1) / 2, own = mine ? n - turns : turns;
     if (n > 0) {
-        auto at = [&](int i) __attribute__((always_inline)) { return min(b0 + mine + 2 * i, last - 1); };      // (loads past the last repeat it)
-        Step ring[2];
-        load(at(0), ring[0]);
-        put_x(0, ring[0]);
+        const int64_t first = b0 + (mine ? turns : 0);
+        auto at = [&](int i) __attribute__((always_inline)) { return min(first + i, last - 1); };      // (loads past the last repeat it)
+        Codes ring[2];
+        Tokens x;
+        u32x4 next[R];
+        int64_t run = -1;
+        load_scales(at(0) / kRun, next);
+        load_x(at(0), x);
+        load_codes(at(0), ring[0]);
+        put_x(0, x);
 #pragma unroll 1
         for (int b = 0; b < turns; b += 2) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 __syncthreads();
-                load(at(b + i + 1), ring[1 - i]);
+                const int64_t now = at(b + i);
+                if (now / kRun != run) {
+                    run = now / kRun;
+#pragma unroll
+                    for (int j = 0; j < R; ++j) held[j] = next[j];
+                    if ((run + 1) * kRun < last) load_scales(run + 1, next);
+                }
+                load_x(at(b + i + 1), x);
+                load_codes(at(b + i + 1), ring[1 - i]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (b + i < own) step(b + i, ring[i]);
+                if (b + i < own) multiply(b + i, (int)now, ring[i]);
                 if (b + i + 1 >= turns) break;
-                put_x(b + i + 1, ring[1 - i]);
+                put_x(b + i + 1, x);
             }
         }
     }
-    if (last < end) {                             // the last step, by the first half: nothing past K is read, X is 0 there
-        Step h;
+    if (last < end) {                             // the last block, by the first half: nothing past K is read, X is 0 there
+        Codes h;
+        Tokens x;
         if (mine == 0) {
 #pragma unroll
-            for (int t = 0; t < T; ++t) h.x[t] = load16_edge(xrow[t] - 8 * piece, 2 * (kHalfK * last + 8 * piece), 2 * f.K);
+            for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                h.c[j] = load16_edge(crow[j] - 16 * q, kHalfK / 2 * last + 16 * q, row_bytes);
-                const u32x4 s = load16_edge(srow[j], 2 * GH * last, scale_bytes);
-                __builtin_memcpy(h.s[j], &s, 2 * GH);
+                for (int t = 0; t < T; ++t) x.x[u][t] = load16_edge(xrow[t] - 8 * piece, 2 * (kBlockK * last + kHalfK * u + 8 * piece), 2 * f.K);
+#pragma unroll
+                for (int j = 0; j < R; ++j) h.c[j][u] = load16_edge(crow[j] - 16 * code_piece, kBlockK / 2 * last + kHalfK / 2 * u + 16 * code_piece, row_bytes);
             }
-            put_x(turns, h);                      // (the buffer that the turn before the last one used)
+            load_scales(last / kRun, held);
+            put_x(turns, x);                      // (the buffer that the turn before the last one used)
         }
         __syncthreads();
-        if (mine == 0) step(turns, h);
+        if (mine == 0) multiply(turns, (int)last, h);
     }
     __syncthreads();
     f32x4(*sums)[kSharedWaves][R * T][64] = reinterpret_cast<f32x4(*)[kSharedWaves][R * T][64]>(&lds[0][0][0]);
+    static_assert(sizeof(f32x4) * kSharedHalves * kSharedWaves * R * T * 64 <= sizeof(lds), "sums fit in the tokens' place");
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
@@ -643,34 +704,45 @@ bool stream_plan(const pgq_linear4_fwd& p, Plan& q)
 }
 
 // One way to cut a call for the kernels of 16-row tiles, and its estimated microseconds past the launch: turns of the kernel's K
-// loop times their measured length, 256 workgroups at a time, and the second launch with the traffic of the parts' sums (at
-// 5 TB/s, written and read).
+// loop times their measured length and rounds of workgroups, what comes before and after the loop, and the second launch with the
+// traffic of the parts' sums (at 5 TB/s, written and read).  A turn is longer where the machine is full (`busy`).  Of the shared
+// kernel's larger tiles a compute unit holds one workgroup.
 double tile_cost(const pgq_linear4_fwd& p, int path, int rows, int64_t parts, Cut& cut)
 {
     const int t = token_tiles(p);
-    const int64_t units = path == P_ROWS ? (p.K + kBlockK - 1) / kBlockK : (p.K + kHalfK - 1) / kHalfK;
-    const int64_t together = path == P_ROWS ? kWaves4 : kSharedHalves;        // units of K a workgroup takes at a time
+    const int64_t blocks = (p.K + kBlockK - 1) / kBlockK;
+    const int64_t together = path == P_ROWS ? kWaves4 : kSharedHalves;        // blocks a workgroup takes at a time
     const int64_t tile = 16 * rows * (path == P_ROWS ? 1 : kSharedWaves);
-    const int64_t grid = (p.N + tile - 1) / tile * token_blocks(p) * parts, per = (units + parts - 1) / parts;
-    if (parts > 1 && (per < together || (parts - 1) * per >= units || grid > 512)) return -1.0;
+    const int64_t grid = (p.N + tile - 1) / tile * token_blocks(p) * parts, per = (blocks + parts - 1) / parts;
+    if (parts > 1 && (per < together || (parts - 1) * per >= blocks || grid > 512)) return -1.0;
     cut.parts = (int32_t)parts;
     cut.blocks = per;
-    const double full = (double)grid / 256.0;
-    double turn;
-    if (path == P_ROWS) turn = t == 1 ? 0.9 + 0.07 * (double)p.M + 0.3 * (rows - 1) : 3.6 + 1.5 * (rows - 1);
-    else turn = t == 2 ? 0.95 : rows == 1 ? 1.0 + 0.3 * std::min(1.0, full) : 1.8;
+    const bool one = path == P_SHARED && (t == 4 || rows == 2);
+    const double full = (double)grid / 256.0, busy = std::min(1.0, full);
+    const double rounds = one ? (double)((grid + 255) / 256) : std::max(1.0, full);
+    double turn, rest = 0.0;
+    if (path == P_ROWS) {
+        turn = t == 1 ? 1.2 + 0.088 * (double)p.M * busy + 0.85 * (rows - 1) : 1.6 + 2.75 * busy;
+    } else if (rows == 1) {
+        turn = t == 1 ? 0.6 + 0.4 * busy : t == 2 ? 0.9 + 0.4 * busy : 1.3 + 0.75 * busy;
+        rest = t == 4 ? 3.0 : 1.5;
+    } else {
+        turn = t == 1 ? 1.2 + 0.35 * busy : t == 2 ? 1.95 : 3.0;
+        rest = t == 4 ? 4.0 : 2.5;
+    }
     const double join = parts > 1 ? 4.0 + (double)parts * (double)p.M * (double)p.N * 8.0 / 5e6 : 0.0;
-    return (double)((per + together - 1) / together) * turn * std::max(1.0, full) + join;
+    return (double)((per + together - 1) / together) * turn * rounds + rest + join;
 }
 
-// Streaming for one or two tokens; tiles of 16 rows with K spread over a workgroup for up to 16 tokens, with the tokens shared through
-// LDS for more than 32, and the cheaper of both between.  Measured on one MI355X in us (rows kernel, shared kernel, plan):
+// Streaming for one or two tokens; the cheapest way through the kernels of 16-row tiles for more: K spread over a workgroup for up to 32
+// tokens and few rows, the tokens shared through LDS for more of either.  Measured on one MI355X in us, each at its best rows and parts:
 //   tokens x K x N        rows    shared        tokens x K x N         rows    shared
-//   16 x 4096 x 4096       7.1     11.4         32 x 4096 x 14336      23.1     19.6
-//   16 x 8192 x 8192      15.7     20.7         32 x 28672 x 8192      70       58
-//   32 x 4096 x 4096      10.7     12.2         64 x 4096 x 4096       18.6     14.8
-//   32 x 8192 x 8192      23.1     23.4         64 x 8192 x 8192       41       28
-// The number of rows and parts chosen this way was within 8% of the best of all that were tried at 28 of 30 sizes.
+//   4 x 4096 x 4096        5.8     10.0         4 x 8192 x 28672       34.0     27.1
+//   16 x 4096 x 4096       7.7      9.5         16 x 4096 x 14336      13.2     11.2
+//   16 x 8192 x 8192      15.6     16.2         16 x 8192 x 28672      40.4     29
+//   32 x 4096 x 4096      11.2     11.7         32 x 8192 x 28672      84       37
+//   32 x 1024 x 1024       4.8      6.0         32 x 16384 x 1024      14.0     12.7
+// The choice was within 8% of the best of all that were tried at 92 of 96 sizes.
 Plan plan(const pgq_linear4_fwd& p)
 {
     Plan q;
@@ -678,8 +750,8 @@ Plan plan(const pgq_linear4_fwd& p)
     if (stream_plan(p, q)) return q;
     const int t = token_tiles(p);
     double best = -1.0;
-    for (int path = t == 4 ? P_SHARED : P_ROWS; path <= (t == 1 ? P_ROWS : P_SHARED); ++path)
-        for (int rows = 1; rows <= (t == 1 ? 4 : path == P_SHARED && t == 2 ? 1 : 2); rows *= 2)
+    for (int path = t == 4 ? P_SHARED : P_ROWS; path <= P_SHARED; ++path)
+        for (int rows = 1; rows <= (path == P_ROWS && t == 2 ? 1 : 2); ++rows)
             for (int64_t parts = 1; parts <= 16; parts *= 2) {
                 Cut cut = {};
                 const double us = tile_cost(p, path, rows, parts, cut);
@@ -739,10 +811,11 @@ const void* kernel_of(const pgq_linear4_fwd& p, const Plan& q)
     const int t = token_tiles(p), g = p.group;
     if (q.path == P_STREAM) return stream_kernel(q.rows, (int)p.M);
     if (q.path == P_ROWS) {
-        if (t == 1) return q.rows == 1 ? rows_kernel<1, 1>(g) : q.rows == 2 ? rows_kernel<1, 2>(g) : rows_kernel<1, 4>(g);
-        return q.rows == 1 ? rows_kernel<2, 1>(g) : rows_kernel<2, 2>(g);
+        if (t == 2) return rows_kernel<2, 1>(g);
+        return q.rows == 1 ? rows_kernel<1, 1>(g) : rows_kernel<1, 2>(g);
     }
-    if (t == 2) return shared_kernel<2, 1>(g);
+    if (t == 1) return q.rows == 1 ? shared_kernel<1, 1>(g) : shared_kernel<1, 2>(g);
+    if (t == 2) return q.rows == 1 ? shared_kernel<2, 1>(g) : shared_kernel<2, 2>(g);
     return q.rows == 1 ? shared_kernel<4, 1>(g) : shared_kernel<4, 2>(g);
 }
 

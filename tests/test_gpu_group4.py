@@ -219,6 +219,8 @@ def test_linear_shapes(M, N, K, group):
 KERNELS = [(1, 40, 2048), (1, 100, 4096), (1, 33, 6144), (1, 70, 8192), (1, 20, 16384), (1, 35, 26656), (2, 50, 2048), (2, 90, 4064),
            (2, 40, 8192), (2, 9, 16384), (1, 70000, 64), (1, 66000, 6176), (2, 70000, 32),
            (1, 4100, 520), (3, 4100, 520), (16, 8200, 520), (9, 16000, 300), (6, 48, 16392), (16, 130, 9000), (20, 4100, 520), (32, 8192, 4000), (25, 14400, 520),
+           (16, 30000, 520), (5, 20000, 4500), (16, 9000, 12300), (3, 66000, 1030), (12, 1000, 30000),
+           (20, 30000, 520), (32, 20000, 4500), (24, 9000, 12300), (17, 500, 30000), (16, 28672, 2100), (30, 28672, 2100), (16, 8192, 20000), (32, 8192, 20000),
            (30, 48, 16392), (40, 4100, 520), (64, 30000, 300), (33, 30000, 520), (64, 80, 16392), (50, 520, 4100), (64, 8200, 1030), (129, 300, 4100)]
 
 

@@ -29,10 +29,11 @@ def test_no_kernel_spills():
     (r"pgq_linear4_stream_kernelILi[34]ELi1E", 2, 184, 2),
     (r"pgq_linear4_stream_kernelILi[12]ELi2E", 2, 168, 3),
     (r"pgq_linear4_rows_kernelILi1ELi1E", 3, 104, 4),
-    (r"pgq_linear4_rows_kernelILi1ELi[24]E", 6, 224, 2),
-    (r"pgq_linear4_rows_kernelILi2ELi[12]E", 6, 192, 2),
-    (r"pgq_linear4_shared_kernelILi2ELi1E", 3, 96, 5),
-    (r"pgq_linear4_shared_kernelILi4ELi[12]E", 6, 200, 2),
+    (r"pgq_linear4_rows_kernelILi1ELi2E", 3, 144, 3),
+    (r"pgq_linear4_rows_kernelILi2ELi1E", 3, 144, 3),
+    (r"pgq_linear4_shared_kernelILi[12]ELi1E", 6, 128, 4),
+    (r"pgq_linear4_shared_kernelILi[12]ELi2E", 6, 184, 2),
+    (r"pgq_linear4_shared_kernelILi4ELi[12]E", 6, 256, 2),
     (r"pgq_quantize_groups_kernelI", 6, 48, 8),
     (r"pgq_dequant_groups_kernelI", 2, 32, 8),
     (r"pgq_grad_norm_kernel", 1, 72, 7),

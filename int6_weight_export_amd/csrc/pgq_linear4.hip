@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
 // 16 bytes of codes and one scale a lane, row and slab; v_dot2_f32_bf16 multiplies (two additions of fp32 each).  Nothing is shared
 // before a row's 64 partial sums are added, so the codes of the next 8 KB of rows are always in flight, and a row is read in one go:
 // 4096 -> 4096 4.1 us of which 2.5 are any kernel's, 8192 -> 8192 9.0, 8192 -> 28672 22.2, 4096 -> 128256 45.5 (5.9 TB/s).  With
-// three and four tokens the multiplications take over (8192 -> 28672: 42 and 50 us, the tiles 35).
+// three and four tokens the multiplications take over (8192 -> 28672: 42 and 50 us, the shared kernel 27).
 constexpr int kStreamWaves = 4;
 constexpr int kSlab = 2048;
 

@@ -59,13 +59,14 @@ __device__ __forceinline__ void trade(u32x4& w)
         w = u32x4{a[0], a[1], b[0], b[1]};
     }
 }
-// first of the eight columns that lane quarter q supplies to instruction d
-template <int G>
-__device__ __forceinline__ int column(int d, int q)
+// A load of 64 bytes of each of 16 rows costs a compute unit's load path a quarter where four neighbouring lanes take a row (row l / 4,
+// piece l % 4 of it); the matrix instructions want row l % 16, piece l / 16.  16 bytes a lane on their way from one to the other.
+__device__ __forceinline__ u32x4 from_quads(u32x4 v, int lane)
 {
-    if (G == 128) return 32 * q + 8 * d;
-    if (G == 64) return 64 * (d >> 1) + 32 * (q & 1) + 16 * (q >> 1) + 8 * (d & 1);
-    return 32 * d + 8 * q;
+    const int from = 4 * (4 * (lane & 15) + (lane >> 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[e]);
+    return v;
 }
 
 // 16 bytes at any address, past the caches: for whole rows in one go (8192 -> 28672 25.7 -> 22.2 us).  The tiles' loads, 64 bytes
@@ -109,18 +110,19 @@ struct Cut {
 };
 
 // T: tiles of 16 tokens, R: of 16 weight rows.  Lane l: token l % 16 of A, weight row l % 16 of B, columns by the quarter
-// l / 16.  Lanes past N repeat the last row, whose sums they do not store.
+// l / 16.  Lanes past N repeat the last row, whose sums they do not store.  Loads are by quads, and a word of codes of every piece is
+// one instruction's (the order of groups of 32), so that a load of X serves one instruction too.
 //
-// What bounds it is how fast a compute unit takes in cache lines: besides the codes every workgroup reads all of X (16 tokens
-// by 4096: 131 KB beside 32 KB of codes for R = 1), which R = 2 halves (8192 -> 8192, 16 tokens: 21.3 and 15.7 us; with R = 4 19.6,
-// half of the machine idle) and the shared kernel quarters.  Scales come 16 bytes of a row at a time, not a few for each block (one
-// token 8192 -> 28672 38 -> 33 us).
+// What bounds it is the compute unit's load path: besides the codes every workgroup reads all of X (16 tokens by 4096: 131 KB beside
+// 32 KB of codes for R = 1).  By quads 16 x 4096 x 4096 goes from 7.6 to 6.5 us, 32 x 4096 x 4096 from 11.1 to 8.8, 16 x 8192 x 8192
+// with R = 1 from 21.6 to 15.8 (four tokens 5.7 -> 6.1: few of their lanes load at all).  R = 2 halves X (8192 -> 8192, 16 tokens:
+// 14.2).  Scales come 16 bytes of a row at a time, not a few for each block (one token 8192 -> 28672 38 -> 33 us).
 template <int T, int R, int G>
 __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_linear4_fwd f, Cut cut)
 {
     __shared__ f32x4 sums[kWaves4][R * T][64];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    const int r = lane & 15, q = lane >> 4;
+    const int r = lane & 15, quad = lane >> 2, piece = lane & 3;
     const uint32_t tb = blockIdx.x % (uint32_t)cut.token_blocks, rest = blockIdx.x / (uint32_t)cut.token_blocks;
     const uint32_t part = rest % (uint32_t)cut.parts;
     const int64_t m0 = (int64_t)tb * kMost, n0 = (int64_t)(rest / (uint32_t)cut.parts) * (16 * R);
@@ -128,12 +130,11 @@ __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_line
     const uint16_t *srow[R], *xrow[T];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        const int64_t n = min(n0 + 16 * j + r, f.N - 1);
-        crow[j] = f.codes + n * f.ldc + 16 * q;
-        srow[j] = f.scales + n * f.lds;
+        crow[j] = f.codes + min(n0 + 16 * j + quad, f.N - 1) * f.ldc + 16 * piece;
+        srow[j] = f.scales + min(n0 + 16 * j + r, f.N - 1) * f.lds;
     }
 #pragma unroll
-    for (int t = 0; t < T; ++t) xrow[t] = f.x + min(m0 + 16 * t + r, f.M - 1) * f.ldx;
+    for (int t = 0; t < T; ++t) xrow[t] = f.x + min(m0 + 16 * t + quad, f.M - 1) * f.ldx + 8 * piece;
     f32x4 acc[R][T];
 #pragma unroll
     for (int j = 0; j < R; ++j)
@@ -141,13 +142,14 @@ __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_line
         for (int t = 0; t < T; ++t) acc[j][t] = f32x4{};
     bool live[T];                                 // lanes past M load nothing of X: their rows of the products go nowhere
 #pragma unroll
-    for (int t = 0; t < T; ++t) live[t] = m0 + 16 * t + r < f.M;
+    for (int t = 0; t < T; ++t) live[t] = m0 + 16 * t + quad < f.M;
     constexpr int GH = kHalfK / G;                // groups of half a block
     constexpr int SB = 8 / (2 * GH);              // blocks whose scales are loaded together, 16 bytes of a row
     const int64_t scale_bytes = 2 * ((f.K + G - 1) / G);
     // products of half a block: sc holds the scales of its groups in its lowest halves
     auto multiply = [&](u32x4 c, const u32x4 (*x)[4], uint64_t sc, f32x4* a) __attribute__((always_inline)) {
-        trade<G>(c);
+        c = from_quads(c, lane);
+        trade<32>(c);
 #pragma unroll
         for (int g = 0; g < GH; ++g) {
             f32x4 p[T];
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_line
                     for (int d = 0; d < 4; ++d) x[half][t][d] = u32x4{};
                     if (live[t]) {
 #pragma unroll
-                        for (int d = 0; d < 4; ++d) x[half][t][d] = load16(xrow[t] + kBlockK * b + kHalfK * half + column<G>(d, q));
+                        for (int d = 0; d < 4; ++d) x[half][t][d] = load16(xrow[t] + kBlockK * b + kHalfK * half + 32 * d);
                     }
                 }
             u32x4 sn[R];
@@ -224,9 +226,14 @@ __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_line
             if (more) load_codes(b + 1, next);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) x[half][t][d] = from_quads(x[half][t][d], lane);
 #pragma unroll
                 for (int j = 0; j < R; ++j) multiply(h.c[j][half], x[half], scales_of(s[j], half), acc[j]);
+            }
             if (!more) return;
             h = next;
             if (refill) {
@@ -254,10 +261,10 @@ __global__ void __launch_bounds__(64 * kWaves4) pgq_linear4_rows_kernel(pgq_line
 #pragma unroll
             for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int d = 0; d < 4; ++d) x[t][d] = load16_edge(xrow[t], 2 * (k0 + column<G>(d, q)), 2 * f.K);
+                for (int d = 0; d < 4; ++d) x[t][d] = from_quads(load16_edge(xrow[t] - 8 * piece, 2 * (k0 + 32 * d + 8 * piece), 2 * f.K), lane);
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                const u32x4 c = load16_edge(crow[j] - 16 * q, k0 / 2 + 16 * q, row);
+                const u32x4 c = load16_edge(crow[j] - 16 * piece, k0 / 2 + 16 * piece, row);
                 const u32x4 s = load16_edge(srow[j], 2 * (k0 / G), scale_bytes);
                 multiply(c, x, (uint64_t)s[1] << 32 | s[0], acc[j]);
             }
@@ -312,9 +319,8 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
     const int tid = (int)threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
     const int mine = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8);            // half
     const int r = lane & 15, q = lane >> 4;
-    // A load of 64 bytes of 16 rows costs less where the four lanes of a row are neighbours (8192 -> 28672, R = 1: 16 tokens 31.8 ->
-    // 29.7 us, 32 41.6 -> 38.8), and the words then travel to the lanes that multiply them; with larger tiles the registers
-    // and the way through LDS cost more than that (32 tokens, R = 2: 36.4 -> 37.5; 64: 54 -> 58).
+    // Codes by quads (8192 -> 28672, R = 1: 16 tokens 31.8 -> 29.7 us, 32 41.6 -> 38.8), but with larger tiles the registers and the
+    // way through LDS cost more than that (32 tokens, R = 2: 36.4 -> 37.5; 64: 54 -> 58).
     constexpr bool kQuads = T * R <= 2;
     const int code_row = kQuads ? lane >> 2 : r, code_piece = kQuads ? lane & 3 : q;
     const uint32_t tb = blockIdx.x % (uint32_t)cut.token_blocks, rest = blockIdx.x / (uint32_t)cut.token_blocks;
@@ -402,10 +408,7 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 c[j] = h.c[j][u];
-                if (kQuads) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[j][e] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * r + q), (int)c[j][e]);
-                }
+                if (kQuads) c[j] = from_quads(c[j], lane);
                 trade<G>(c[j]);
             }
 #pragma unroll
@@ -722,7 +725,8 @@ double tile_cost(const pgq_linear4_fwd& p, int path, int rows, int64_t parts, Cu
     const double rounds = one ? (double)((grid + 255) / 256) : std::max(1.0, full);
     double turn, rest = 0.0;
     if (path == P_ROWS) {
-        turn = t == 1 ? 1.2 + 0.088 * (double)p.M * busy + 0.85 * (rows - 1) : 1.6 + 2.75 * busy;
+        turn = t == 1 ? 1.0 + (0.4 + 0.02 * (double)p.M) * busy + (0.5 + 0.6 * busy) * (rows - 1) : 1.0 + 1.5 * busy;
+        rest = 0.6;
     } else if (rows == 1) {
         turn = t == 1 ? 0.6 + 0.4 * busy : t == 2 ? 0.9 + 0.4 * busy : 1.3 + 0.75 * busy;
         rest = t == 4 ? 3.0 : 1.5;
@@ -737,12 +741,12 @@ double tile_cost(const pgq_linear4_fwd& p, int path, int rows, int64_t parts, Cu
 // Streaming for one or two tokens; the cheapest way through the kernels of 16-row tiles for more: K spread over a workgroup for up to 32
 // tokens and few rows, the tokens shared through LDS for more of either.  Measured on one MI355X in us, each at its best rows and parts:
 //   tokens x K x N        rows    shared        tokens x K x N         rows    shared
-//   4 x 4096 x 4096        5.8     10.0         4 x 8192 x 28672       34.0     27.1
-//   16 x 4096 x 4096       7.7      9.5         16 x 4096 x 14336      13.2     11.2
-//   16 x 8192 x 8192      15.6     16.2         16 x 8192 x 28672      40.4     29
-//   32 x 4096 x 4096      11.2     11.7         32 x 8192 x 28672      84       37
-//   32 x 1024 x 1024       4.8      6.0         32 x 16384 x 1024      14.0     12.7
-// The choice was within 8% of the best of all that were tried at 92 of 96 sizes.
+//   4 x 4096 x 4096        6.1     10.0         4 x 8192 x 28672       40.7     27.1
+//   16 x 4096 x 4096       6.5      9.5         16 x 4096 x 14336      15.7     11.2
+//   16 x 8192 x 8192      11.8     15.8         16 x 8192 x 28672      44       29
+//   32 x 4096 x 4096       8.8     11.7         32 x 8192 x 28672      79       37
+//   32 x 1024 x 1024       4.1      6.0         32 x 8192 x 8192       24.9     18.6
+// The choice was within 8% of the best of all that were tried at all but a few of 96 sizes.
 Plan plan(const pgq_linear4_fwd& p)
 {
     Plan q;

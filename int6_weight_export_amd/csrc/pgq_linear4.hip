@@ -6,7 +6,7 @@
 // scale, so no weight is ever rounded and a weight costs no multiplication of its own.  Three kernels:
 //   stream   1 and 2 tokens: a wavefront along K, tokens in its registers, rows streaming by (8192 -> 28672, one token: 22 us,
 //            5.5 TB/s)
-//   rows     3 to 32 tokens and few rows: 16 R weight rows a workgroup, K spread over its wavefronts, sums joined through LDS
+//   rows     small layers: 16 R weight rows a workgroup, K spread over its wavefronts, sums joined through LDS
 //   shared   the rest: 64 R rows a workgroup, the tokens of a block of K shared through LDS (8192 -> 28672, 16 tokens: 30 us)
 // The last two multiply on the matrix cores, v_mfma_f32_16x16x32_bf16 with 16 tokens as A and 16 weight rows as B, so that a lane
 // has the sums of one weight row and needs one scale.
@@ -725,7 +725,7 @@ double tile_cost(const pgq_linear4_fwd& p, int path, int rows, int64_t parts, Cu
     const double rounds = one ? (double)((grid + 255) / 256) : std::max(1.0, full);
     double turn, rest = 0.0;
     if (path == P_ROWS) {
-        turn = t == 1 ? 1.0 + (0.4 + 0.02 * (double)p.M) * busy + (0.5 + 0.6 * busy) * (rows - 1) : 1.0 + 1.5 * busy;
+        turn = t == 1 ? 1.0 + (0.4 + 0.02 * (double)p.M) * busy + (0.5 + 0.6 * busy) * (rows - 1) : t == 2 ? 1.0 + 1.5 * busy : 1.6 + 3.4 * busy;
         rest = 0.6;
     } else if (rows == 1) {
         turn = t == 1 ? 0.6 + 0.4 * busy : t == 2 ? 0.9 + 0.4 * busy : 1.3 + 0.75 * busy;
@@ -738,14 +738,17 @@ double tile_cost(const pgq_linear4_fwd& p, int path, int rows, int64_t parts, Cu
     return (double)((per + together - 1) / together) * turn * rounds + rest + join;
 }
 
-// Streaming for one or two tokens; the cheapest way through the kernels of 16-row tiles for more: K spread over a workgroup for up to 32
-// tokens and few rows, the tokens shared through LDS for more of either.  Measured on one MI355X in us, each at its best rows and parts:
+// Streaming for one or two tokens; the cheapest way through the kernels of 16-row tiles for more: K spread over a workgroup where the
+// layer is small, the tokens shared through LDS where X would be read too often.  Measured on one MI355X in us, each at its best rows
+// and parts:
 //   tokens x K x N        rows    shared        tokens x K x N         rows    shared
 //   4 x 4096 x 4096        6.1     10.0         4 x 8192 x 28672       40.7     27.1
 //   16 x 4096 x 4096       6.5      9.5         16 x 4096 x 14336      15.7     11.2
 //   16 x 8192 x 8192      11.8     15.8         16 x 8192 x 28672      44       29
 //   32 x 4096 x 4096       8.8     11.7         32 x 8192 x 28672      79       37
 //   32 x 1024 x 1024       4.1      6.0         32 x 8192 x 8192       24.9     18.6
+//   64 x 528 x 1584        5.4      8.7         64 x 2048 x 2048        7.5     12.0
+//   64 x 4096 x 4096      13.7     14.6         64 x 8192 x 8192       40       26
 // The choice was within 8% of the best of all that were tried at all but a few of 96 sizes.
 Plan plan(const pgq_linear4_fwd& p)
 {
@@ -754,8 +757,8 @@ Plan plan(const pgq_linear4_fwd& p)
     if (stream_plan(p, q)) return q;
     const int t = token_tiles(p);
     double best = -1.0;
-    for (int path = t == 4 ? P_SHARED : P_ROWS; path <= P_SHARED; ++path)
-        for (int rows = 1; rows <= (path == P_ROWS && t == 2 ? 1 : 2); ++rows)
+    for (int path = P_ROWS; path <= P_SHARED; ++path)
+        for (int rows = 1; rows <= (path == P_ROWS && t > 1 ? 1 : 2); ++rows)
             for (int64_t parts = 1; parts <= 16; parts *= 2) {
                 Cut cut = {};
                 const double us = tile_cost(p, path, rows, parts, cut);
@@ -815,7 +818,7 @@ const void* kernel_of(const pgq_linear4_fwd& p, const Plan& q)
     const int t = token_tiles(p), g = p.group;
     if (q.path == P_STREAM) return stream_kernel(q.rows, (int)p.M);
     if (q.path == P_ROWS) {
-        if (t == 2) return rows_kernel<2, 1>(g);
+        if (t > 1) return t == 2 ? rows_kernel<2, 1>(g) : rows_kernel<4, 1>(g);
         return q.rows == 1 ? rows_kernel<1, 1>(g) : rows_kernel<1, 2>(g);
     }
     if (t == 1) return q.rows == 1 ? shared_kernel<1, 1>(g) : shared_kernel<1, 2>(g);

@@ -218,10 +218,10 @@ def test_linear_shapes(M, N, K, group):
 # slabs each; 16, 32 and 64 rows a workgroup; tokens through LDS; parts of K
 KERNELS = [(1, 40, 2048), (1, 100, 4096), (1, 33, 6144), (1, 70, 8192), (1, 20, 16384), (1, 35, 26656), (2, 50, 2048), (2, 90, 4064),
            (2, 40, 8192), (2, 9, 16384), (1, 70000, 64), (1, 66000, 6176), (2, 70000, 32),
-           (1, 4100, 520), (3, 4100, 520), (16, 8200, 520), (9, 16000, 300), (6, 48, 16392), (16, 130, 9000), (20, 4100, 520), (32, 8192, 4000), (25, 14400, 520),
+           (1, 4100, 520), (3, 4100, 520), (16, 8200, 520), (10, 8100, 1030), (4, 8100, 4500), (9, 16000, 300), (6, 48, 16392), (16, 130, 9000), (20, 4100, 520), (32, 8192, 4000), (25, 14400, 520),
            (16, 30000, 520), (5, 20000, 4500), (16, 9000, 12300), (3, 66000, 1030), (12, 1000, 30000),
            (20, 30000, 520), (32, 20000, 4500), (24, 9000, 12300), (17, 500, 30000), (16, 28672, 2100), (30, 28672, 2100), (16, 8192, 20000), (32, 8192, 20000),
-           (30, 48, 16392), (40, 4100, 520), (64, 30000, 300), (33, 30000, 520), (64, 80, 16392), (50, 520, 4100), (64, 8200, 1030), (129, 300, 4100)]
+           (30, 48, 16392), (40, 4100, 520), (64, 30000, 300), (33, 30000, 520), (64, 14400, 4100), (50, 4100, 14500), (129, 4100, 4100), (64, 80, 16392), (50, 520, 4100), (64, 8200, 1030), (129, 300, 4100)]
 
 
 @pytest.mark.parametrize("M,N,K", KERNELS)
@@ -312,6 +312,49 @@ def test_linear_residual_in_place(M, t):
     assert got is r
     _, _, yr, ey = ref.forward(f64(x), w, None, "none", 0.0, r0, t)
     within(r, yr, ey, "y")
+
+
+@pytest.mark.parametrize("M", [5, 16, 27, 40, 64, 90])
+@pytest.mark.parametrize("K", [264, 512, 301])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear_wide_layers(M, K, group):
+    """Layers so wide that the tokens go through LDS: strided operands, every epilogue argument, Y between other columns."""
+    say(f"linear4 wide M={M} K={K} group {group}")
+    N = 6000
+    codes, scales, w = weights(N, K, group, 41, 3, 5)
+    x, b, r = randn((M, K), 42, torch.bfloat16, pad=3), randn((1, N), 43)[0], randn((M, N), 44, torch.bfloat16, pad=1)
+    for y in ("f32", "bf16"):
+        buf = torch.full((M, N + 3), 7.0, dtype=T[y], device="cuda")
+        ops.qlinear4(x, codes, scales, group=group, bias=b, act="silu", residual=r, out=buf[:, 1:1 + N], out_dtype=T[y])
+        torch.cuda.synchronize()
+        _, _, yr, ey = ref.forward(f64(x), w, f64(b), "silu", 0.0, f64(r), y)
+        within(buf[:, 1:1 + N], yr, ey, "y")
+        assert bool((buf[:, :1] == 7.0).all()) and bool((buf[:, 1 + N:] == 7.0).all())
+
+
+@pytest.mark.parametrize("M", [5, 16, 27, 40, 64])
+@pytest.mark.parametrize("K", [512, 330])
+def test_linear_wide_layers_infinities_and_nan(M, K):
+    """An infinite token value, a NaN and a scale that is not finite stay in their token's and output's elements."""
+    say(f"linear4 wide infinities M={M} K={K}")
+    N, group = 6000, 64
+    codes, scales, w = weights(N, K, group, 45)
+    x = randn((M, K), 46, torch.bfloat16)
+    clean = ops.qlinear4(x, codes, scales, group=group, out_dtype=torch.float32)
+    x[1, 100], x[M - 1, 7] = float("inf"), float("nan")
+    got = ops.qlinear4(x, codes, scales, group=group, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    rows = [m for m in range(M) if m not in (1, M - 1)]
+    v = torch.from_numpy(w[:, 100])
+    inf = got[1].cpu()
+    assert torch.equal(got[rows], clean[rows]) and bool(torch.isnan(got[M - 1]).all())
+    assert bool(torch.isnan(inf[v == 0]).all()) and bool((inf[v > 0] == float("inf")).all()) and bool((inf[v < 0] == float("-inf")).all())
+    s = scales.clone()
+    s[3009, scales.shape[1] - 1] = float("inf")
+    got = ops.qlinear4(randn((M, K), 46, torch.bfloat16), codes, s, group=group, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    cols = [n for n in range(N) if n != 3009]
+    assert torch.equal(got[:, cols], clean[:, cols]) and not bool(torch.isfinite(got[:, 3009]).any())
 
 
 def test_linear_empty_and_k_zero():

@@ -31,6 +31,7 @@ def test_no_kernel_spills():
     (r"pgq_linear4_rows_kernelILi1ELi1E", 3, 104, 4),
     (r"pgq_linear4_rows_kernelILi1ELi2E", 3, 144, 3),
     (r"pgq_linear4_rows_kernelILi2ELi1E", 3, 144, 3),
+    (r"pgq_linear4_rows_kernelILi4ELi1E", 3, 232, 2),
     (r"pgq_linear4_shared_kernelILi[12]ELi1E", 6, 128, 4),
     (r"pgq_linear4_shared_kernelILi[12]ELi2E", 6, 184, 2),
     (r"pgq_linear4_shared_kernelILi4ELi[12]E", 6, 256, 2),

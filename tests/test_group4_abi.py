@@ -89,7 +89,7 @@ def test_sizes_past_one_launch_are_refused():
     assert pgq.pgq_linear4_forward_workspace(ctypes.byref(p), ctypes.byref(n)) == pgq.PGQ_ERR_SHAPE
 
 
-@pytest.mark.parametrize("M,N,K", [(6, 48, 16392), (30, 48, 16392), (64, 48, 16392), (64, 4096, 4096)])
+@pytest.mark.parametrize("M,N,K", [(6, 48, 16392), (30, 48, 16392), (64, 48, 16392), (64, 8192, 8192)])
 def test_workspace_is_required_when_k_is_cut(M, N, K):
     n = ctypes.c_size_t(0)
     p = linear(M=M, N=N, K=K, ldx=K, ldc=(K + 7) // 8 * 4, lds=(K + 31) // 32, ldy=N, x=1 << 40, codes=1 << 41, scales=1 << 42, y=1 << 43)

@@ -545,7 +545,7 @@ __device__ __forceinline__ float wave_sum(float x)
     return dpp_add<0x143, 0xC>(x);                // row_bcast 31 to rows 2 and 3
 }
 
-// S: slabs of a wavefront, M: tokens.  K a multiple of 32, K <= 2048 S split.
+// S: slabs of a wavefront, M: tokens.  25 <= K <= 2048 S split, for two tokens a multiple of 32.
 template <int S, int M>
 __global__ void __launch_bounds__(64 * kStreamWaves) pgq_linear4_stream_kernel(pgq_linear4_fwd f, Stream a)
 {
@@ -558,22 +558,30 @@ __global__ void __launch_bounds__(64 * kStreamWaves) pgq_linear4_stream_kernel(p
     const int shift = 31 - __builtin_clz((unsigned)f.group);
     uint32_t x[M][S][16];
     uint32_t code_at[S], scale_at[S];
+    // `past`: K is not whole lanes (one token only).  The lane that reaches past the row takes its last 32 columns, with token values of 0
+    // where they are another lane's.  Lanes wholly past K: token values of 0, any codes and scale of the row.
+    auto load_x = [&](bool past) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int64_t k = ((int64_t)piece * S + s) * kSlab + 32 * lane;
-        const bool in = k < f.K;                          // lanes past K: token values of 0, any codes and scale of the row
-        code_at[s] = in ? (uint32_t)(k / 2) : 0u;
-        scale_at[s] = in ? (uint32_t)(k >> shift) : 0u;
+        for (int s = 0; s < S; ++s) {
+            const int64_t k = ((int64_t)piece * S + s) * kSlab + 32 * lane;
+            const int64_t at = past ? min(k, (f.K + 7) / 8 * 8 - 32) : k;
+            const bool in = k < f.K;
+            code_at[s] = in ? (uint32_t)(at / 2) : 0u;
+            scale_at[s] = in ? (uint32_t)(k >> shift) : 0u;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u32x4 v = {};
-                if (in) v = load16(f.x + m * f.ldx + k + 8 * i);
+                for (int i = 0; i < 4; ++i) {
+                    u32x4 v = {};
+                    if (past && i == 3 && in && at + 32 > f.K) v = load16_edge(f.x, 2 * (at + 24), 2 * f.K);
+                    else if (past ? in && at + 8 * i >= k : in) v = load16(f.x + m * f.ldx + at + 8 * i);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[m][s][4 * i + e] = v[e];
-            }
-    }
+                    for (int e = 0; e < 4; ++e) x[m][s][4 * i + e] = v[e];
+                }
+        }
+    };
+    if (M == 1 && f.K % 32 != 0) load_x(true);
+    else load_x(false);
     struct Rows { u32x4 c[RG][S]; uint16_t s[RG][S]; };
     auto load = [&](int64_t n, Rows& h) __attribute__((always_inline)) {
 #pragma unroll
@@ -690,14 +698,14 @@ struct Plan {
     size_t bytes;
 };
 
-// Streaming needs whole 32 columns a lane and at most four slabs (two tokens: two) a wavefront, sixteen (eight) a workgroup.  With three or
+// Streaming needs the 16 bytes of codes that a lane loads and at most four slabs (two tokens: two) a wavefront, sixteen (eight) a workgroup.  With three or
 // four slabs one wavefront a SIMD takes an equal share of the rows (8192 -> 28672, 1024 and 8192 wavefronts: 22.2 and 25.8 us, 14336
 // -> 4096 9.0 and 10.4); with fewer, every load of rows has a wavefront of its own (4096 -> 14336 8.9 and 8.6, 2048 -> 16384 6.5
-// and 5.5).
+// and 5.5).  K that is not whole lanes of 32 columns: for one token (4100 -> 4100 5.9, the tiles 7.5; 8200 -> 28672 29 and 35).
 bool stream_plan(const pgq_linear4_fwd& p, Plan& q)
 {
     const int64_t slabs = (p.K + kSlab - 1) / kSlab, most = p.M == 1 ? 4 : 2;
-    if (p.M > 2 || p.K == 0 || p.K % 32 != 0 || slabs > most * kStreamWaves) return false;
+    if (p.M > 2 || p.K < 25 || (p.M > 1 && p.K % 32 != 0) || slabs > most * kStreamWaves) return false;
     q.path = P_STREAM;
     q.stream.split = slabs <= most ? 1 : slabs <= 2 * most ? 2 : 4;
     q.rows = (int)((slabs + q.stream.split - 1) / q.stream.split);

@@ -216,7 +216,8 @@ def test_linear_shapes(M, N, K, group):
 
 # sizes that bring every kernel, tile and way of cutting K into use: rows streamed by one, two and four wavefronts with one to four
 # slabs each; 16, 32 and 64 rows a workgroup; tokens through LDS; parts of K
-KERNELS = [(1, 40, 2048), (1, 100, 4096), (1, 33, 6144), (1, 70, 8192), (1, 20, 16384), (1, 35, 26656), (2, 50, 2048), (2, 90, 4064),
+KERNELS = [(1, 5, 25), (1, 6, 31), (1, 300, 24), (1, 33, 4101), (1, 70, 6001), (1, 20, 8190), (1, 9, 14001), (1, 70, 30031), (1, 9, 32766), (1, 9, 32770),
+           (1, 40, 2048), (1, 100, 4096), (1, 33, 6144), (1, 70, 8192), (1, 20, 16384), (1, 35, 26656), (2, 50, 2048), (2, 90, 4064),
            (2, 40, 8192), (2, 9, 16384), (1, 70000, 64), (1, 66000, 6176), (2, 70000, 32),
            (1, 4100, 520), (3, 4100, 520), (16, 8200, 520), (10, 8100, 1030), (4, 8100, 4500), (9, 16000, 300), (6, 48, 16392), (16, 130, 9000), (20, 4100, 520), (32, 8192, 4000), (25, 14400, 520),
            (16, 30000, 520), (5, 20000, 4500), (16, 9000, 12300), (3, 66000, 1030), (12, 1000, 30000),

@@ -574,7 +574,7 @@ pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* cons
 /*            the unrounded norm), NaN where norm is not finite in binary32 (PGQ_DEV_NONFINITE)    */
 /* c: grad_scale, or, where grad_scale_dev is not NULL, the binary32 number there (a member of the AdamW   */
 /* constants in device memory, so that a recorded step follows them).  Sums run in an order that      */
-/* depends on the sizes alone: the same inputs give the same bits.                                  */
+/* depends on the entry point, the sizes and the types alone: the same inputs give the same bits.      */
 /*   grad      host array of n device pointers, numel[i] dense values of dtype[i] (PGQ_F32, PGQ_BF16 or  */
 /*             PGQ_F16), aligned to their type; NULL only where numel[i] is 0                     */
 /*   max_norm  >= 0; infinity for the norm alone                                                   */

@@ -151,6 +151,20 @@ __device__ __forceinline__ double block_sum(double x, double* lds)
     return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+// norm and factor from the sum of squares; returns the factor
+__device__ __forceinline__ float put_result(const NormArgs& a, double r)
+{
+    const double c = (double)(a.scale_dev ? *a.scale_dev : a.scale);
+    const double norm = fabs(c) * sqrt(r);
+    const float nf = (float)norm;
+    const bool finite = nf < INFINITY;
+    const float factor = !finite ? NAN : norm > (double)a.max_norm ? (float)((double)a.max_norm / norm) : 1.0f;
+    a.result[0] = nf;
+    a.result[1] = factor;
+    if (!finite && a.status) atomicOr(a.status, PGQ_DEV_NONFINITE);
+    return factor;
+}
+
 __global__ void __launch_bounds__(kThreads) pgq_grad_norm_kernel(NormArgs a, Tensors t)
 {
     __shared__ double lds[2][kThreads / 64];
@@ -184,13 +198,7 @@ __global__ void __launch_bounds__(kThreads) pgq_grad_norm_kernel(NormArgs a, Ten
     for (uint32_t i = threadIdx.x; i < a.total; i += kThreads) r += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     r = block_sum(r, lds[1]);
     if (threadIdx.x != 0) return;
-    const double c = (double)(a.scale_dev ? *a.scale_dev : a.scale);
-    const double norm = fabs(c) * sqrt(r);
-    const float nf = (float)norm;
-    const bool finite = nf < INFINITY;
-    a.result[0] = nf;
-    a.result[1] = !finite ? NAN : norm > (double)a.max_norm ? (float)((double)a.max_norm / norm) : 1.0f;
-    if (!finite && a.status) atomicOr(a.status, PGQ_DEV_NONFINITE);
+    put_result(a, r);
 }
 
 template <typename T>
@@ -240,6 +248,102 @@ __global__ void __launch_bounds__(kThreads) pgq_grad_scale_kernel(NormArgs a, Te
     if (dtype == PGQ_F32) scale_all(static_cast<float*>(p) + base, count, factor);
     else if (dtype == PGQ_BF16) scale_all(static_cast<Bf16*>(p) + base, count, factor);
     else scale_all(static_cast<F16*>(p) + base, count, factor);
+}
+
+// Clipping of a few small tensors in one launch: one workgroup, which keeps what it has read (16-byte pieces, kSmallPieces a
+// thread) until the factor is known.  What bounds it is latency, of the piece's tensor, its load, the sum and the store, then what one
+// compute unit can load; two launches against this one: 18 x 512 bf16 12.2 and 5.2 us, 45 x 257 fp32 12.6 and 7.3, 60 x 1000 bf16
+// 12.9 and 9.4, 32768 fp32 (all the pieces there are) 9.7 and 8.0.
+constexpr int kSmallThreads = 1024, kSmallPieces = 8;
+constexpr int64_t kSmallMost = (int64_t)kSmallThreads * kSmallPieces;
+
+template <typename T>
+__device__ __forceinline__ double piece_squares(u32x4 v)
+{
+    constexpr int V = 16 / sizeof(T);
+    float f[V];
+    unpack<T>(v, f);
+    double s = 0.0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = __builtin_fma((double)f[e], (double)f[e], s);
+    return s;
+}
+template <typename T>
+__device__ __forceinline__ u32x4 piece_times(u32x4 v, float factor)
+{
+    constexpr int V = 16 / sizeof(T);
+    float f[V];
+    unpack<T>(v, f);
+    T o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) put(o + e, f[e] * factor);
+    __builtin_memcpy(&v, o, 16);
+    return v;
+}
+
+// (t.end: one past the last piece of each tensor; a.total: pieces in all)
+__global__ void __launch_bounds__(kSmallThreads) pgq_grad_clip_small_kernel(NormArgs a, Tensors t)
+{
+    __shared__ uint32_t end[kArgTensors];
+    __shared__ double sums[kSmallThreads / 64];
+    __shared__ float factor;
+    const uint32_t tid = threadIdx.x;
+    if (tid < kArgTensors) end[tid] = t.end[tid];
+    __syncthreads();
+    uint8_t* p[kSmallPieces];
+    u32x4 v[kSmallPieces];
+    int32_t bytes[kSmallPieces], dtype[kSmallPieces];
+#pragma unroll
+    for (int u = 0; u < kSmallPieces; ++u) {
+        const uint32_t piece = tid + u * kSmallThreads;
+        v[u] = u32x4{};
+        bytes[u] = 0;
+        dtype[u] = PGQ_F32;
+        p[u] = nullptr;
+        if (piece >= a.total) continue;
+        uint32_t ti = 0;                          // tensors that end at or before the piece
+#pragma unroll
+        for (uint32_t d = kArgTensors / 2; d > 0; d /= 2)
+            if (end[ti + d - 1] <= piece) ti += d;
+        const uint32_t first = ti > 0 ? end[ti - 1] : 0u;
+        dtype[u] = t.dtype[ti];
+        const int64_t at = (int64_t)(piece - first) * 16, size = t.numel[ti] * (dtype[u] == PGQ_F32 ? 4 : 2);
+        p[u] = static_cast<uint8_t*>(const_cast<void*>(t.p[ti])) + at;
+        bytes[u] = (int32_t)min(size - at, (int64_t)16);
+    }
+#pragma unroll
+    for (int u = 0; u < kSmallPieces; ++u) {
+        if (bytes[u] == 16) v[u] = load16(p[u]);
+        else
+            for (int e = 0; e < bytes[u]; e += 2) {
+                const uint32_t h = *reinterpret_cast<const uint16_t*>(p[u] + e);
+                v[u][e >> 2] |= h << (8 * (e & 2));
+            }
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int u = 0; u < kSmallPieces; ++u)
+        s += dtype[u] == PGQ_F32 ? piece_squares<float>(v[u]) : dtype[u] == PGQ_BF16 ? piece_squares<Bf16>(v[u]) : piece_squares<F16>(v[u]);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_down(s, d);
+    if ((tid & 63) == 0) sums[tid >> 6] = s;
+    __syncthreads();
+    if (tid == 0) {
+        double r = 0.0;
+#pragma unroll
+        for (int i = 0; i < kSmallThreads / 64; ++i) r += sums[i];
+        factor = put_result(a, r);
+    }
+    __syncthreads();
+    const float f = factor;
+    if (!(f < 1.0f)) return;                      // 1, or NaN
+#pragma unroll
+    for (int u = 0; u < kSmallPieces; ++u) {
+        const u32x4 o = dtype[u] == PGQ_F32 ? piece_times<float>(v[u], f) : dtype[u] == PGQ_BF16 ? piece_times<Bf16>(v[u], f) : piece_times<F16>(v[u], f);
+        if (bytes[u] == 16) __builtin_memcpy(p[u], &o, 16);
+        else
+            for (int e = 0; e < bytes[u]; e += 2) *reinterpret_cast<uint16_t*>(p[u] + e) = (uint16_t)(o[e >> 2] >> (8 * (e & 2)));
+    }
 }
 
 // Elements of a tile, and the number of tiles of all tensors.
@@ -320,6 +424,33 @@ int launches_of(const int64_t* numel, int32_t n)
     return (int)((filled + kArgTensors - 1) / kArgTensors);
 }
 
+// 16-byte pieces of all tensors (more than kSmallMost: some number past it)
+int64_t pieces_of(const int64_t* numel, const int32_t* dtype, int32_t n)
+{
+    int64_t pieces = 0;
+    for (int32_t i = 0; i < n && pieces <= kSmallMost; ++i) pieces += (numel[i] * (int64_t)size_of(dtype[i]) + 15) / 16;
+    return pieces;
+}
+pgq_status run_small(Launches& l, NormArgs a, void* const* grad, const int64_t* numel, const int32_t* dtype, int32_t n)
+{
+    Tensors t;
+    memset(&t, 0, sizeof(t));
+    memset(t.end, 0xFF, sizeof(t.end));
+    uint32_t end = 0;
+    int k = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (numel[i] == 0) continue;
+        t.p[k] = grad[i];
+        t.numel[k] = numel[i];
+        t.dtype[k] = (uint8_t)dtype[i];
+        end += (uint32_t)((numel[i] * (int64_t)size_of(dtype[i]) + 15) / 16);
+        t.end[k++] = end;
+    }
+    void* args[] = {&a, &t};
+    l.go(reinterpret_cast<const void*>(&pgq_grad_clip_small_kernel), 1, kSmallThreads, args);
+    return l.done();
+}
+
 NormArgs args_of(float scale, const float* scale_dev, float max_norm, float* result, void* workspace, uint32_t* status, int64_t tile, int64_t total)
 {
     NormArgs a;
@@ -387,8 +518,14 @@ pgq_status pgq_grad_clip(void* const* grad, const int64_t* numel, const int32_t*
     if (ranges != few) delete[] ranges;
     if (st != PGQ_OK) return st;
     const int per = launches_of(numel, n);
+    NormArgs a = args_of(1.0f, nullptr, max_norm, result, workspace, dev_status, tile, total);
+    const int64_t pieces = per <= 1 ? pieces_of(numel, dtype, n) : kSmallMost + 1;
+    if (pieces <= kSmallMost) {
+        a.total = (uint32_t)pieces;
+        Launches l(1, stream);
+        return run_small(l, a, grad, numel, dtype, n);
+    }
     Launches l(std::max(per, 1) + per, stream);
-    const NormArgs a = args_of(1.0f, nullptr, max_norm, result, workspace, dev_status, tile, total);
     st = run(reinterpret_cast<const void*>(&pgq_grad_norm_kernel), l, a, grad, numel, dtype, n, true);
     if (st != PGQ_OK) return st;
     return run(reinterpret_cast<const void*>(&pgq_grad_scale_kernel), l, a, grad, numel, dtype, n, false);

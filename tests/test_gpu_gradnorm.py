@@ -114,6 +114,65 @@ def test_clip(sizes, t):
     assert gn.result.tolist() == [0.0, 1.0] and int(gn.status.item()) == 0
 
 
+# either side of what one launch takes (8192 pieces of 16 bytes in 128 tensors): the last full one, one more piece, one more tensor
+EDGES = [[0], [0, 0, 3], [8], [9], [1, 0, 1023, 4096, 5], [3] * 128, [3] * 129, [0] * 5 + [7] * 127 + [0, 2], [0] * 5 + [7] * 128 + [0, 2],
+         [32768], [32767, 1], [32769], [65536], [65535, 9], [65528, 8], [65537], [256] * 128, [257] * 127]
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("sizes", EDGES, ids=lambda s: f"{len(s)}x{s[0]}-{sum(s)}")
+def test_clip_of_small_lists(sizes, t):
+    say(f"grad clip, {len(sizes)} tensors of {sum(sizes)} elements {t}")
+    buf = torch.full((sum(sizes) + 3 * len(sizes) + 3,), 9.0).to(T[t]).cuda()      # neighbours that no tensor holds
+    mine, grads, at = torch.zeros(buf.numel(), dtype=torch.bool), [], 1
+    for n in sizes:
+        grads.append(buf[at:at + n])
+        mine[at:at + n] = True
+        at += n + 3
+    buf[mine.cuda()] = rand(sum(sizes), 3, 0.5, t)
+    before, want = buf.clone(), exact_norm(grads)
+    gn = ops.GradNorm(grads)
+    for most, clipped in ((1e6, False), (want / 3, True)):
+        norm = gn.clip_(most)
+        torch.cuda.synchronize()
+        assert abs(float(norm) - want) <= REL * want
+        f = float(gn.result[1])
+        if not clipped or want == 0:
+            assert f == 1.0 and torch.equal(buf, before)
+        else:
+            assert abs(f - 1 / 3) <= 2 * REL
+            assert torch.equal(buf, torch.where(mine.cuda(), (before.float() * torch.tensor(f, device="cuda")).to(T[t]), before))
+    assert int(gn.status.item()) == 0
+
+
+def test_clip_of_small_lists_in_mixed_types_captured():
+    say("grad clip of a small list, mixed types, captured and replayed")
+    grads = [rand(n, n, 1.0, t) for n, t in ((700, "f32"), (33, "bf16"), (1, "f16"), (4095, "bf16"), (2, "f32"))]
+    gn = ops.GradNorm(grads)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gn.clip_(1.5)
+    for i in range(4):
+        bad = i == 2
+        new = [rand(g.numel(), 10 * i + j, 1.0).to(g.dtype) for j, g in enumerate(grads)]
+        if bad:
+            new[3][4094] = float("nan")
+        for g, x in zip(grads, new):
+            g.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        f = float(gn.result[1])
+        if bad:
+            assert math.isnan(f) and int(gn.status.item()) == pgq.PGQ_DEV_NONFINITE
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(grads, new))
+            gn.status.zero_()
+            continue
+        want = exact_norm(new)
+        assert abs(float(gn.result[0]) - want) <= REL * want and abs(f - 1.5 / want) <= REL * f
+        assert all(torch.equal(a, (b.float() * torch.tensor(f, device="cuda")).to(a.dtype)) for a, b in zip(grads, new))
+    assert int(gn.status.item()) == 0
+
+
 def test_mixed_types_and_many_tensors():
     say("grad norm and clip over 700 tensors of mixed types")
     grads = [rand((37 * i) % 211, i, 0.3, ["f32", "bf16", "f16"][i % 3]) for i in range(700)]

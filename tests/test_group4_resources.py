@@ -39,6 +39,7 @@ def test_no_kernel_spills():
     (r"pgq_dequant_groups_kernelI", 2, 32, 8),
     (r"pgq_grad_norm_kernel", 1, 72, 7),
     (r"pgq_grad_scale_kernel", 1, 64, 8),
+    (r"pgq_grad_clip_small_kernel", 1, 128, 4),
 ])
 def test_budgets(pattern, count, vgprs, occupancy):
     got = kernels(pattern)

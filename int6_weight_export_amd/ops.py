@@ -706,9 +706,11 @@ def _norm_result(device) -> torch.Tensor:
 
 class GradNorm:
     """The global L2 norm of a list of gradient tensors (fp32, bf16 or fp16, dense) and clipping to it, without the norm's
-    coming to the host.  The tensors and their addresses are taken once; bind() takes others of the same sizes.  `status` gets
-    PGQ_DEV_NONFINITE where a norm is not finite.  Not to be made while a graph is captured; its calls may be.  Calls
-    that run at the same time need an object each."""
+    coming to the host.  The tensors are taken once and kept, and each call takes them where they lie then (their .data may have
+    been replaced, by tensors of the same sizes); bind() takes others.  Gradients that a backward pass makes anew, as after
+    zero_grad(set_to_none=True), are other tensors: bind() them.  `status` gets PGQ_DEV_NONFINITE where a norm is not
+    finite.  Not to be made while a graph is captured; its calls may be, and a captured call keeps the addresses it was captured
+    with.  Calls that run at the same time need an object each."""
 
     def __init__(self, grads: Sequence[torch.Tensor]):
         grads = list(grads)
@@ -737,18 +739,30 @@ class GradNorm:
             if g.get_device() != self._index:
                 raise ValueError(f"gradient {i} is on {g.device}, expected GPU {self._index}")
         self.grads = grads
+        # (kept, so that memory at a known address is either still the tensor's or nobody's: a tensor whose storage was replaced
+        # cannot come back to that address with a smaller one)
+        self._storages = [g.untyped_storage() for g in grads]
+        self._at = [g.data_ptr() for g in grads]
         for i, g in enumerate(grads):
-            self._ptrs[i], self._dtype[i] = g.data_ptr(), _dtype_code(g.dtype)
+            self._ptrs[i], self._dtype[i] = self._at[i], _dtype_code(g.dtype)
+
+    def _follow(self) -> None:
+        """Take the kept tensors anew where one of them lies elsewhere than when it was taken: its storage was replaced or
+        reallocated, and its old memory may be another tensor's."""
+        if list(map(torch.Tensor.data_ptr, self.grads)) != self._at:
+            self.bind(self.grads)
 
     def norm(self, max_norm: float = float("inf"), grad_scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
         """(norm, factor), two fp32 numbers on the GPU that the next call overwrites: |grad_scale| sqrt(sum g^2), and 1, or
         max_norm / norm where the norm is larger, or NaN where it is not finite."""
+        self._follow()
         _on_gpu(self._index, "pgq_grad_norm", pgq._lib.pgq_grad_norm, self._ptrs, self._numel, self._dtype, self.n, grad_scale, None,
                 max_norm, *self._tail)
         return self._views
 
     def clip_(self, max_norm: float) -> torch.Tensor:
         """Multiply the gradients by that factor in place (not where it is 1 or NaN); returns the norm they had."""
+        self._follow()
         _on_gpu(self._index, "pgq_grad_clip", pgq._lib.pgq_grad_clip, self._ptrs, self._numel, self._dtype, self.n, max_norm,
                 *self._tail)
         return self._views[0]

@@ -691,17 +691,18 @@ def _dense(name: str, t: torch.Tensor, numel: int, dtypes) -> None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
 
 
-def _norm_workspace(numel, device) -> torch.Tensor:
+def _norm_workspace(numel, device, source="cpu") -> torch.Tensor:
     """The gradient norm's workspace for tensors of these sizes (a ctypes array).  Zeroed by a copy from the host, which is
-    over when it returns, so that any stream may use it."""
+    over when it returns, so that any stream may use it; source=device: by a kernel on the current stream, which a graph may
+    hold."""
     need = ctypes.c_size_t(0)
     pgq.check(pgq.pgq_grad_norm_workspace(numel, len(numel), ctypes.byref(need)), "pgq_grad_norm_workspace")
-    return torch.zeros(need.value, dtype=torch.uint8, device="cpu").to(device)
+    return torch.zeros(need.value, dtype=torch.uint8, device=source).to(device)
 
 
-def _norm_result(device) -> torch.Tensor:
+def _norm_result(device, source="cpu") -> torch.Tensor:
     """Norm and factor; made in the same way."""
-    return torch.zeros(2, dtype=torch.float32, device="cpu").to(device)
+    return torch.zeros(2, dtype=torch.float32, device=source).to(device)
 
 
 class GradNorm:
@@ -826,9 +827,7 @@ class AdamW:
         self._g_dtypes = [torch.float32] * n
         self._g_codes = (ctypes.c_int32 * n)(*[pgq.PGQ_F32] * n)
         self._n_numel = (ctypes.c_int64 * n)(*self._numel)
-        self.norm_workspace = _norm_workspace(self._n_numel, self.device)
-        self.norm_result = _norm_result(self.device)
-        self.grad_norm = self.norm_result[0]
+        self._norm = self._norm_shown = None
         self._ws_ptr, self._ws_bytes, self._status_ptr = self.workspace.data_ptr(), self.workspace.numel(), self.status.data_ptr()
 
     def _zero_state(self, k: int):
@@ -886,17 +885,41 @@ class AdamW:
         self._uploaded = True
         return None if max_norm is None else self.grad_norm
 
+    def _norm_buffers(self):
+        """(workspace, result) of clipped steps: made at the first one, so that an optimizer that never clips has none.  A step that
+        is captured before then gets its graph's own, which the graph clears at every replay."""
+        if self._norm is not None:
+            self._norm_shown = self._norm
+        elif torch.cuda.is_current_stream_capturing():
+            self._norm_shown = _norm_workspace(self._n_numel, self.device, self.device), _norm_result(self.device, self.device)
+        else:
+            self._norm = self._norm_shown = _norm_workspace(self._n_numel, self.device), _norm_result(self.device)
+        return self._norm_shown
+
+    @property
+    def norm_workspace(self) -> torch.Tensor:
+        return (self._norm_shown or self._on_device(self._norm_buffers))[0]
+
+    @property
+    def norm_result(self) -> torch.Tensor:
+        """Norm and factor of the latest clipped step (two fp32 numbers on the GPU)."""
+        return (self._norm_shown or self._on_device(self._norm_buffers))[1]
+
+    @property
+    def grad_norm(self) -> torch.Tensor:
+        return self.norm_result[0]
+
     def _enqueue_step(self, h, ptrs, grad_scale, max_norm) -> None:
         h_dev, stream = None if h is not None else self.hyper.data_ptr(), _stream_of(self._index)
         factor = None
         if max_norm is not None:
+            workspace, result = self._norm_buffers()
             rc = pgq._lib.pgq_grad_norm(ptrs, self._n_numel, self._g_codes, self.n, grad_scale,
                                         None if h_dev is None else h_dev + pgq.pgq_adamw_hyper.grad_scale.offset, max_norm,
-                                        self.norm_result.data_ptr(), self.norm_workspace.data_ptr(), self.norm_workspace.numel(),
-                                        self._status_ptr, stream)
+                                        result.data_ptr(), workspace.data_ptr(), workspace.numel(), self._status_ptr, stream)
             if rc != pgq.PGQ_OK:
                 pgq.check(rc, "pgq_grad_norm")
-            factor = self.norm_result.data_ptr() + 4
+            factor = result.data_ptr() + 4
         rc = pgq._lib.pgq_adamw_step_clipped(self._arr, self.n, self.state_bits, ptrs, h, h_dev, factor, self._ws_ptr,
                                              self._ws_bytes, self._table_flags(), self._status_ptr, stream)
         if rc != pgq.PGQ_OK:

@@ -762,7 +762,8 @@ class GradNorm:
         return self._views
 
     def clip_(self, max_norm: float) -> torch.Tensor:
-        """Multiply the gradients by that factor in place (not where it is 1 or NaN); returns the norm they had."""
+        """Multiply the gradients by that factor in place (not where it is 1 or NaN); returns the norm they had, the same number on
+        the GPU as norm()'s: the next call of either overwrites it, so one that is to be kept has to be cloned."""
         self._follow()
         _on_gpu(self._index, "pgq_grad_clip", pgq._lib.pgq_grad_clip, self._ptrs, self._numel, self._dtype, self.n, max_norm,
                 *self._tail)

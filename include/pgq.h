@@ -570,8 +570,9 @@ pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* cons
 /* ------------------------------------------------------------------------------------------ */
 /* The global norm of n gradient tensors and clipping to it.                                     */
 /*   norm   = fl32(|c| * sqrt(sum of g^2 over every element)), squares and sums in 64 bits         */
-/*   factor = 1 where norm <= max_norm, fl32(max_norm / norm) where it is larger (the quotient of   */
-/*            the unrounded norm), NaN where norm is not finite in binary32 (PGQ_DEV_NONFINITE)    */
+/*   factor = 1 where norm <= max_norm, fl32(max_norm / norm) where it is larger (comparison and    */
+/*            quotient with the unrounded norm), NaN where norm is not finite in binary32          */
+/*            (PGQ_DEV_NONFINITE)                                                               */
 /* c: grad_scale, or, where grad_scale_dev is not NULL, the binary32 number there (a member of the AdamW   */
 /* constants in device memory, so that a recorded step follows them).  Sums run in an order that      */
 /* depends on the entry point, the sizes and the types alone: the same inputs give the same bits.      */
@@ -583,7 +584,7 @@ pgq_status pgq_adamw_decode(const pgq_adamw_tensor* t, int32_t n, uint16_t* cons
 /*             its first use; a call leaves it ready for the next one.  Calls that run at the same time (two     */
 /*             graphs, two streams) need one each                                                     */
 /* The three host arrays are read during the call only.  May be recorded into a HIP graph: the recorded call   */
-/* keeps its pointers and max_norm.  Sizes: each below 2^40.                                        */
+/* keeps its pointers and max_norm.  Sizes: at most 2^40 each.                                      */
 /* ------------------------------------------------------------------------------------------ */
 pgq_status pgq_grad_norm_workspace(const int64_t* numel, int32_t n, size_t* workspace_bytes);
 pgq_status pgq_grad_norm(const void* const* grad, const int64_t* numel, const int32_t* dtype, int32_t n, float grad_scale,

@@ -1,10 +1,10 @@
 // pgq_gradnorm.hip -- the global norm of many gradient tensors and clipping to it (gfx950).
 //
-// norm = |c| sqrt(sum g^2); factor = min(1, max_norm / norm).  One launch reads every tensor once: a
+// norm = |c| sqrt(sum g^2); factor = min(1, max_norm / norm).  One launch for every 128 tensors reads each once: a
 // workgroup takes a tile of one tensor, squares and adds in 64 bits (an fp64 multiply-add goes at the rate of
 // an fp32 one here, no square overflows, and the sum of 2^36 squares is still good to 2^-52 or so of itself for
-// each addition), and writes one partial sum.  The workgroup that finishes last adds the partial sums, always in the
-// same order, and writes norm and factor: no second launch, and no atomic whose order the result depends on.
+// each addition), and writes one partial sum.  The last launch's workgroup that finishes last adds the partial sums, always in
+// the same order, and writes norm and factor: no launch of its own for that, and no atomic whose order the result depends on.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -66,7 +66,8 @@ __device__ __forceinline__ bool is_last(uint8_t* counters)
     return count(1 + g, (grid - g + kCounters - 1) / kCounters) && count(0, kCounters);
 }
 
-// the tensor of a tile: the number of tensors that end at or before it
+// the tensor of a tile: the number of tensors that end at or before it (unused entries end past every tile; without any tensor, the
+// one workgroup of the launch finds entry 0, of no elements)
 __device__ __forceinline__ int tensor_of(const Tensors& t, uint32_t tile)
 {
     const int lane = (int)threadIdx.x & 63;
@@ -169,16 +170,14 @@ __global__ void __launch_bounds__(kThreads) pgq_grad_norm_kernel(NormArgs a, Ten
 {
     __shared__ double lds[2][kThreads / 64];
     __shared__ bool last;
-    double s = 0.0;
+    double s;
     const int ti = __builtin_amdgcn_readfirstlane(tensor_of(t, blockIdx.x));
-    if (ti < kArgTensors) {                       // (an empty list has one workgroup and no tensor)
-        const int64_t base = (int64_t)(blockIdx.x - (ti > 0 ? t.end[ti - 1] : 0u)) * a.tile;
-        const int64_t count = min(a.tile, t.numel[ti] - base);
-        const int32_t dtype = t.dtype[ti];
-        if (dtype == PGQ_F32) s = sum_squares(static_cast<const float*>(t.p[ti]) + base, count);
-        else if (dtype == PGQ_BF16) s = sum_squares(static_cast<const Bf16*>(t.p[ti]) + base, count);
-        else s = sum_squares(static_cast<const F16*>(t.p[ti]) + base, count);
-    }
+    const int64_t base = (int64_t)(blockIdx.x - (ti > 0 ? t.end[ti - 1] : 0u)) * a.tile;
+    const int64_t count = min(a.tile, t.numel[ti] - base);
+    const int32_t dtype = t.dtype[ti];
+    if (dtype == PGQ_F32) s = sum_squares(static_cast<const float*>(t.p[ti]) + base, count);
+    else if (dtype == PGQ_BF16) s = sum_squares(static_cast<const Bf16*>(t.p[ti]) + base, count);
+    else s = sum_squares(static_cast<const F16*>(t.p[ti]) + base, count);
     s = block_sum(s, lds[0]);
     if (threadIdx.x == 0) {
         __hip_atomic_store(a.part + a.first + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -240,7 +239,6 @@ __global__ void __launch_bounds__(kThreads) pgq_grad_scale_kernel(NormArgs a, Te
     // the tiles last read come first: they are still in the caches
     const uint32_t tile = gridDim.x - 1 - blockIdx.x;
     const int ti = __builtin_amdgcn_readfirstlane(tensor_of(t, tile));
-    if (ti >= kArgTensors) return;
     const int64_t base = (int64_t)(tile - (ti > 0 ? t.end[ti - 1] : 0u)) * a.tile;
     const int64_t count = min(a.tile, t.numel[ti] - base);
     const int32_t dtype = t.dtype[ti];

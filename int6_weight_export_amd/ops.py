@@ -755,7 +755,7 @@ class GradNorm:
 
     def norm(self, max_norm: float = float("inf"), grad_scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
         """(norm, factor), two fp32 numbers on the GPU that the next call overwrites: |grad_scale| sqrt(sum g^2), and 1, or
-        max_norm / norm where the norm is larger, or NaN where it is not finite."""
+        max_norm / norm where the norm is larger, or NaN where it is not finite.  max_norm and grad_scale are taken as fp32 numbers."""
         self._follow()
         _on_gpu(self._index, "pgq_grad_norm", pgq._lib.pgq_grad_norm, self._ptrs, self._numel, self._dtype, self.n, grad_scale, None,
                 max_norm, *self._tail)

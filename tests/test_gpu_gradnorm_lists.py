@@ -1,5 +1,6 @@
-"""GPU tests of the gradient norm and clipping over lists that change under them: tensors whose memory was replaced between two
-calls.  Bounds as in test_gpu_gradnorm.py."""
+"""GPU tests of the gradient norm and clipping over lists: tensors whose memory was replaced between two
+calls, no tensors at all, and lists that take several launches.  Bounds as in test_gpu_gradnorm.py."""
+import ctypes
 import math
 import sys
 
@@ -12,7 +13,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
-from int6_weight_export_amd import ops  # noqa: E402
+from int6_weight_export_amd import ops, pgq  # noqa: E402
 
 T = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 REL = (1 + 2.0 ** -6) * 2.0 ** -24
@@ -55,3 +56,52 @@ def test_replaced_data_is_clipped_where_it_lies(sizes, t):
         assert all(torch.equal(a, b) for a, b in zip(left, kept))
         now = exact_norm(grads)
         assert abs(float(gn.norm(1.0)[0]) - now) <= REL * now
+
+
+def test_no_tensors_through_the_c_abi():
+    """The norm of nothing is 0; lists of empty tensors likewise, NULL pointers among them."""
+    say("grad norm and clip of no tensors")
+    stream = torch.cuda.current_stream().cuda_stream
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    st = ops.new_status()
+    torch.cuda.synchronize()
+    for n in (0, 1, 300):
+        p, m, d = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+        for call in ("norm", "clip"):
+            for _ in range(2):
+                r = torch.full((2,), 9.0, device="cuda")
+                tail = (r.data_ptr(), ws.data_ptr(), ws.numel(), st.data_ptr(), stream)
+                if call == "norm":
+                    rc = pgq.pgq_grad_norm(p, m, d, n, 1.0, None, 0.0, *tail)
+                else:
+                    rc = pgq.pgq_grad_clip(p, m, d, n, 0.0, *tail)
+                torch.cuda.synchronize()
+                assert rc == pgq.PGQ_OK and r.tolist() == [0.0, 1.0], (n, call)
+    assert int(st.item()) == 0 and not bool(ws[:17 * 256].any())
+
+
+# lists of several launches of 128 tensors: the first large and the last small, the last with more workgroups (over 256) than one
+# counter takes, both, and three launches with empty tensors between
+LISTS = [[100000] * 128 + [5] * 3, [5] * 128 + [5000003, 7], [70001] * 130 + [3000000], [17] * 128 + [0] * 9 + [40000] * 128 + [1 << 20] * 6]
+
+
+@pytest.mark.parametrize("sizes", LISTS, ids=lambda s: f"{len(s)}x{s[0]}-{sum(s)}")
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_lists_of_several_launches(sizes, t):
+    say(f"grad norm and clip of {len(sizes)} tensors, {sum(sizes)} elements {t}")
+    buf = rand(sum(sizes), len(sizes), 0.5, t)
+    grads, at = [], 0
+    for n in sizes:
+        grads.append(buf[at:at + n])
+        at += n
+    before, want = buf.clone(), exact_norm([buf])
+    gn = ops.GradNorm(grads)
+    for _ in range(3):
+        norm, factor = gn.norm(want / 4)
+        torch.cuda.synchronize()
+        assert abs(float(norm) - want) <= REL * want and abs(float(factor) - 0.25) <= 2 * REL
+    gn.clip_(want / 4)
+    torch.cuda.synchronize()
+    f = torch.tensor(float(gn.result[1]), device="cuda")
+    assert abs(float(f) - 0.25) <= 2 * REL and torch.equal(buf, (before.float() * f).to(T[t]))
+    assert int(gn.status.item()) == 0 and not bool(gn.workspace[:17 * 256].any())

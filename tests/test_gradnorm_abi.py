@@ -85,3 +85,20 @@ def test_clipped_step_checks_its_factor():
     assert pgq.pgq_adamw_hyper_at(1e-3, 0.9, 0.999, 1e-8, 1, 1.0, 0, ctypes.byref(h)) == pgq.PGQ_OK
     assert pgq.pgq_adamw_step_clipped(t, 1, 32, g, h, None, FAKE + 2, FAKE, 1 << 20, 0, None, None) == pgq.PGQ_ERR_ALIGN
     assert pgq.pgq_adamw_step_clipped(t, 1, 32, g, None, None, FAKE, FAKE, 1 << 20, 0, None, None) == pgq.PGQ_ERR_NULL
+
+
+@pytest.mark.parametrize("numel", [[], [0], [1], [16384] * 1024, [16385] * 1023, [(1 << 22) + 13] * 3, [1 << 40], [1 << 40, 0, 5], [3] * 5000])
+def test_workspace_is_the_counters_and_a_sum_a_tile(numel):
+    """Seventeen counters of 256 bytes and eight bytes for every tile, of which there are at most 1024 and one more a tensor."""
+    a, need = (ctypes.c_int64 * len(numel))(*numel), ctypes.c_size_t(0)
+    assert pgq.pgq_grad_norm_workspace(a, len(numel), ctypes.byref(need)) == pgq.PGQ_OK
+    filled = sum(n > 0 for n in numel)
+    least = max(1, filled, min(1024, sum(numel) // 16384) // 2)
+    assert 17 * 256 + 8 * least <= need.value <= 17 * 256 + 8 * (1024 + filled) + 56
+
+
+def test_workspace_of_small_lists_is_counted_in_tiles_of_16384():
+    for numel, tiles in (([1], 1), ([16384], 1), ([16385], 2), ([16384 * 3 + 1, 0, 7], 5), ([16384 * 1024], 1024)):
+        a, need = (ctypes.c_int64 * len(numel))(*numel), ctypes.c_size_t(0)
+        assert pgq.pgq_grad_norm_workspace(a, len(numel), ctypes.byref(need)) == pgq.PGQ_OK
+        assert need.value == 17 * 256 + -(-8 * tiles // 64) * 64

@@ -1,7 +1,7 @@
-"""GPU tests of the optimizer step that clips on the way: an optimizer made while a graph is captured, and clipped steps that are
-captured before the first eager one.  A clipped step is compared, bit for bit, with an unclipped one whose grad_scale is
-fl32(grad_scale * factor), the factor being read back from the device; the norm with the sum in 64 bits (bound as in
-test_gpu_gradnorm.py)."""
+"""GPU tests of the optimizer step that clips on the way: an optimizer made while a graph is captured, clipped steps that are captured
+before the first eager one, types of weights and gradients, lists of several launches, two streams.  A clipped step is compared, bit
+for bit, with an unclipped one whose grad_scale is fl32(grad_scale * factor), the factor being read back from the device; the norm
+with the sum in 64 bits (bound as in test_gpu_gradnorm.py)."""
 import math
 import sys
 
@@ -109,3 +109,45 @@ def test_clipped_step_captured_before_the_first_eager_one(bits):
         unclipped(b, grads, a.norm_result, 1.0)
         same(a, b)
     assert int(a.status.item()) == 0
+
+
+KINDS = {"bf16 weights": (("bf16",), ("bf16",)), "fp16 gradients": (("f32",), ("f16",)), "mixed": (("f32", "bf16"), ("f16", "f32", "bf16"))}
+LISTS = {"few": [4096, 700, 3, 20001], "several launches": [37 * i % 211 + 1 for i in range(300)], "large last": [9] * 130 + [3000001, 5]}
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sizes", LISTS)
+def test_types_and_long_lists(kind, sizes, bits):
+    say(f"clipped adamw step: {kind}, {sizes}, {bits}-bit states")
+    (types, gtypes), sizes = KINDS[kind], LISTS[sizes]
+    a, b = optimizer(sizes, bits, types), optimizer(sizes, bits, types)
+    for turn in range(3):
+        grads = [rand(n, 10 * turn + j, 0.5, gtypes[(j + turn) % len(gtypes)]) for j, n in enumerate(sizes)]      # (types change by the step)
+        want = 0.5 * exact_norm(grads)
+        most = 2 * want if turn == 1 else want / 3
+        norm = a.step(grads, grad_scale=0.5, max_norm=most)
+        torch.cuda.synchronize()
+        assert abs(float(norm) - want) <= REL * want and abs(float(a.norm_result[1]) - min(1, most / want)) <= 2 * REL
+        unclipped(b, grads, a.norm_result, 0.5)
+        same(a, b)
+    assert a.step_count == 3 and int(a.status.item()) == 0
+
+
+def test_two_optimizers_on_two_streams():
+    say("clipped adamw steps of two optimizers on two streams")
+    sizes = [300000, 17, 70001]
+    pair, alone = [optimizer(sizes, 32, seed=s) for s in (1, 50)], [optimizer(sizes, 32, seed=s) for s in (1, 50)]
+    grads = [[[rand(n, 1000 * k + 10 * turn + n % 7, 1.0 + k) for n in sizes] for turn in range(6)] for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(6):
+        for opt, stream, g in zip(pair, streams, grads):
+            with torch.cuda.stream(stream):
+                opt.step(g[turn], max_norm=1.0)
+    torch.cuda.synchronize()
+    for opt, other, g in zip(pair, alone, grads):
+        for turn in range(6):
+            other.step(g[turn], max_norm=1.0)
+        same(opt, other)
+        assert torch.equal(opt.grad_norm, other.grad_norm) and int(opt.status.item()) == 0

@@ -307,8 +307,11 @@ __global__ void __launch_bounds__(256) pgq_linear4_join_kernel(pgq_linear4_fwd f
 //
 // What bounds it first is again how many cache lines a compute unit takes in (8192 -> 28672, 32 tokens, R = 2): tokens, codes and
 // scales a million each when a step of K loads its own scales, and 44 us; with scales 64 bytes of a row at a time 37.  Blocks of 128
-// columns leave half of each line of codes for later: 53.  For 64 tokens the multiplications take over (55 us, without any loads of
-// operands 35); codes two and three blocks ahead: no faster.
+// columns leave half of each line of codes for later: 53.  For 64 tokens the loads of operands come first too, then the products: 60 us
+// with all of them, 41 without those of codes, 48 without those of tokens, 35 without both; without decoding 57, without the LDS reads 56
+// (then by steps to 55).  A compute unit holds one workgroup there, two wavefronts a SIMD: the tokens take 128 of its 160 KB of LDS, and
+// two workgroups would need both halves of that and at most 128 registers (R = 1: 157 to 172, R = 2: 235 to 256).  Codes two and three
+// blocks ahead: no faster.
 constexpr int kSharedWaves = 4, kSharedHalves = 2;
 constexpr int kSubs = kBlockK / kHalfK;
 
@@ -519,7 +522,8 @@ __global__ void __launch_bounds__(64 * kSharedWaves * kSharedHalves) pgq_linear4
 // A wavefront lies along K: lane l holds 32 columns of each slab of 2048, whose tokens stay in its registers while rows go by,
 // 16 bytes of codes and one scale a lane, row and slab; v_dot2_f32_bf16 multiplies (two additions of fp32 each).  Nothing is shared
 // before a row's 64 partial sums are added, so the codes of the next 8 KB of rows are always in flight, and a row is read in one go:
-// 4096 -> 4096 4.1 us of which 2.5 are any kernel's, 8192 -> 8192 9.0, 8192 -> 28672 22.2, 4096 -> 128256 45.5 (5.9 TB/s).  With
+// 4096 -> 4096 4.1 us of which 2.5 are any kernel's, 8192 -> 8192 9.0, 8192 -> 28672 22.2, 4096 -> 128256 49 (5.6 TB/s), 8192 -> 262144
+// 171 (6.5, as fast as anything here reads).  With
 // three and four tokens the multiplications take over (8192 -> 28672: 42 and 50 us, the shared kernel 27).
 constexpr int kStreamWaves = 4;
 constexpr int kSlab = 2048;

@@ -636,8 +636,8 @@ def qlinear4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, group: 
              act: str = "none", slope: float = 0.0, residual: Optional[torch.Tensor] = None,
              out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Y = act(X W^T + b) + R with 4-bit weights W = code * s, a scale for every `group` columns: qlinear's form for
-    serving, made for up to 64 tokens (more are taken in blocks of 64; from a few hundred on, dequant_groups and a library
-    product are faster).
+    serving, made for up to 64 tokens (more are taken in blocks of 64; from about 450 on for the largest layers, 640 for 4096 x
+    4096, dequant_groups and a library product are faster).
 
     x: bf16 [M, K]; codes: uint8 [N, 4 ceil(K / 8)] and scales: fp16 (or int16 bit patterns) [N, ceil(K / group)] as
     quantize_groups makes them; the other arguments as in qlinear.  Returns Y [M, N] in out_dtype (bf16 or fp32).  No
